@@ -435,6 +435,126 @@ int fv5b_head_argmax_embed(const int8_t* W, const float* S, int64_t V, int64_t K
 int fv5b_embed(const int8_t* W, const float* S, int64_t V, int64_t K, const int32_t* ids, int64_t M, float* out,
                uint16_t* out_bf16, void* stream);
 
+/* ---- attention over a paged int8 cache (between the q|k|v linear and o) ----
+ *
+ * The models behind these linears normalise every query and key head, rotate
+ * them by their position and share each key/value head among a group of query
+ * heads (32:8 and 16:8 heads of 128, rotary base 1e6; [P2], the model family's
+ * table), and the cache they grow overtakes the weights in a long context
+ * ([P2], the section on the KV cache).  Here it is held in 8 bits, as the head
+ * and the embedding are.
+ *
+ * Cache: a block holds TERN_KV_BLOCK = 64 consecutive tokens of one sequence.
+ * For each block, key/value head and side (0 = K, 1 = V) there are 64*D int8
+ * codes and one fp32 scale; a cached value is code * scale.
+ *   codes  int8 [blocks][heads][2][64*D], scales fp32 [blocks][heads][2]
+ *   order of the codes inside a block (an int8 matrix-core operand is one
+ *   16-byte load, and softmax weights meet V without leaving their lane):
+ *     K of token 16t + r, dim 64s + 16g + b:  (((t*(D/64) + s)*4 + g)*16 + r)*16 + b
+ *     V of token 16t + 4g + i, dim 16u + r:   ((u*4 + g)*16 + r)*16 + 4t + i
+ * The caller allocates both arrays; codes need no initial value, scales are
+ * set by the append that writes a block's first token.
+ *
+ * Batch: nseq sequences; rows cu[i] .. cu[i+1]-1 of the per-token tensors are
+ * the newest tokens of sequence i, whose length with them is lens[i]: row
+ * cu[i] + j stands at position lens[i] - (cu[i+1] - cu[i]) + j.  Block b of
+ * sequence i is table[i*table_stride + b].  All three are device memory, read
+ * by the kernels alone, so a captured graph follows their contents.  Rows in
+ * front of cu[0] and from cu[nseq] on are neither read nor written.  A table
+ * entry outside [0, blocks), a position below 0 and one past the table's
+ * width name no cached token: the append stores nothing there, the read gives
+ * zeros and the attention does not see it.  cu must not descend and must end
+ * within the T rows; a sequence for which that fails is skipped.
+ *
+ * Per-token tensors hold T rows of heads * D contiguous elements; row t starts
+ * at t * stride elements (the q, k and v parts of one fused row are three such
+ * tensors).  Their type is TERN_F32 or TERN_BF16; base and stride are multiples
+ * of 16 bytes.  D is 64 or 128. */
+#define TERN_KV_BLOCK 64
+
+typedef enum { TERN_F32 = 0, TERN_BF16 = 1 } tern_type;
+
+typedef struct i8_kv_cache {
+    int8_t* codes;        /* 16-byte aligned */
+    float* scales;        /* 4-byte aligned */
+    int64_t blocks, heads, D;
+} i8_kv_cache;
+
+typedef struct i8_kv_batch {
+    const int32_t* cu;    /* [nseq + 1] */
+    const int32_t* lens;  /* [nseq] */
+    const int32_t* table; /* [nseq][table_stride], the first table_width of a row in use */
+    int64_t nseq, table_width, table_stride;
+} i8_kv_batch;
+
+/* What is done to query and key heads on the way:
+ *   norm      x / sqrt(mean(x^2) + eps) * gain[d]          (gain NULL: left out)
+ *   rotation  pair (x1, x2) by a = pos * inv_freq[j]: (x1 cos a - x2 sin a,
+ *             x2 cos a + x1 sin a); pair j is dims (j, j + D/2), or
+ *             (2j, 2j + 1) when interleaved        (inv_freq NULL: left out)
+ * in fp32, the angle in fp64 (a position far out keeps its phase). */
+typedef struct tern_qk_transform {
+    const float* q_gain;     /* fp32 [D] or NULL, 16-byte aligned */
+    const float* k_gain;     /* fp32 [D] or NULL, 16-byte aligned */
+    const double* inv_freq;  /* fp64 [D/2], radians per position, or NULL */
+    float eps;
+    int32_t interleaved;
+} tern_qk_transform;
+
+/* q_out[t][h] = transform(q[t][h]) with q_gain, k_out the same with k_gain,
+ * outputs contiguous [T][heads][D] of out_type, one rounding each.
+ *   pos int32 [T] (needed only with inv_freq).  Hq or Hk may be 0 (that side's
+ *   pointers are then not used).  Outputs must not overlap inputs. */
+int qk_norm_rope(const tern_qk_transform* f, int64_t T, int64_t D, const void* q, int64_t Hq, int64_t q_stride,
+                 const void* k, int64_t Hk, int64_t k_stride, int in_type, const int32_t* pos, void* q_out,
+                 void* k_out, int out_type, void* stream);
+
+/* Append the batch's rows of k and v to the cache: k normalised and rotated as
+ * above, v as it is, both quantised.  With a = max |new value| over the new
+ * tokens of one block, head and side, and o the block's first new slot:
+ *   o == 0, or an old scale of 0:  scale = a / 127
+ *   else  scale = old * 2^g, the least g >= 0 with a <= fl(127 * old) * 2^g, and
+ *         the codes of the slots below o become rint(code / 2^g)
+ *   new code = clamp(rint(x / scale), -127, 127), 0 where scale is 0
+ * (fp32, IEEE division, ties to even).  Doubling keeps the error of old codes
+ * below one step of the final scale however often it grows.  A block whose new
+ * values hold an infinity or a NaN gets that as its scale and reads as NaN
+ * until its first slot is written again.  Slots behind the new tokens keep
+ * their bytes (they stand for nothing until written), so a sequence is cut
+ * short by lowering lens; a block's scale then stays.
+ * With Hq > 0 the rows of q (Hq heads) are normalised and rotated in the same
+ * launch into q_out, bf16 [T][Hq][D].  pos NULL takes a token's position in
+ * its sequence, else pos int32 [T] is what the rotation uses.
+ * A block must not be written by two sequences of one call, nor by two calls
+ * that overlap in time; blocks that are only read may be shared.
+ * Hq % heads == 0. */
+int i8_kv_append(const i8_kv_cache* cache, const i8_kv_batch* batch, const tern_qk_transform* f, int64_t T,
+                 const void* q, int64_t Hq, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                 int64_t v_stride, int in_type, const int32_t* pos, uint16_t* q_out, void* stream);
+
+/* The batch's tokens read back: k_out, v_out [T][heads][D] of out_type =
+ * code * scale, one rounding; zeros where there is no cached token. */
+int i8_kv_read(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, void* k_out, void* v_out, int out_type,
+               void* stream);
+
+/* Attention of the batch's rows over their sequences' cached tokens:
+ *   out[t][h] = sum_p w_p * V[p] / sum_p w_p,  w_p = exp(scale * q[t][h] . K[p])
+ * over the positions p <= the row's own (its own token among them, so append
+ * first) and, with window > 0, p > own - window; K, V of head h / (Hq/heads).
+ * A row that sees no token gives zeros.  NaN where a value that is seen, or
+ * the row's q, is not finite.
+ *   q bf16 [T] rows (q_stride as above); out bf16 [T][Hq][D]; Hq % heads == 0;
+ *   scale finite, window >= 0.
+ *   max_len: the longest length that lens will hold (a hint for the split of
+ *   long sequences; any length is right, one above max_len slower), > 0.
+ *   workspace: i8_kv_attend_workspace_bytes() bytes, 16-byte aligned, NULL when
+ *   that is 0; overwritten, so calls that share it must not overlap in time.
+ * The sums do not depend on timing: equal calls give equal bytes. */
+int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len);
+int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
+                 int64_t q_stride, float scale, int64_t window, int64_t max_len, uint16_t* out, void* workspace,
+                 void* stream);
+
 /* ---- launch-configuration introspection (no operation of the method) ----
  *
  * The one-pass GEMV configuration that tern_gemv (kind 0), tern_gemv_i8 (1),

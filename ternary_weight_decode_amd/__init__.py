@@ -19,7 +19,10 @@ block-scaled int8 head and embedding (FV5B-style) ``fv5b_head_gemv[_i8]``,
 ``fv5b_head_gemv_packed[_i8]``, ``fv5b_head_argmax_packed[_i8]`` over the
 packed copy), the
 packed int8 head ``i8_head_packed_bytes``, ``i8_head_pack``,
-``i8_head_gemv_packed[_i8]``, ``i8_head_argmax_packed[_i8]``, and the launch-configuration views
+``i8_head_gemv_packed[_i8]``, ``i8_head_argmax_packed[_i8]``, the attention
+side of a step ``qk_norm_rope``, ``i8_kv_append``, ``i8_kv_read`` and
+``i8_kv_attend`` (with the handles ``QkTransform``, ``I8KvCache`` and
+``I8KvBatch``), and the launch-configuration views
 ``tern_gemv_config`` and ``tern_prefill_config``.
 """
 from __future__ import annotations
@@ -38,7 +41,8 @@ SYMBOLS = ("tern_strerror", "tern_last_error", "tern_abi_version", "tern_packed_
            "tern_launch_probe", "i8_head_argmax_noalloc", "i8_head_packed_bytes", "i8_head_pack",
            "i8_head_gemv_packed", "i8_head_gemv_packed_i8", "i8_head_argmax_packed", "i8_head_argmax_packed_i8",
            "fv5b_head_gemv_packed", "fv5b_head_gemv_packed_i8", "fv5b_head_argmax_packed",
-           "fv5b_head_argmax_packed_i8")
+           "fv5b_head_argmax_packed_i8", "qk_norm_rope", "i8_kv_append", "i8_kv_read",
+           "i8_kv_attend_workspace_bytes", "i8_kv_attend")
 _INT_STATUS = ("tern_pack", "tern_stats", "tern_quantize_i8", "tern_gemv", "tern_gemv_i8", "i8_head_gemv",
                "i8_head_gemv_i8", "tern_gemm_prefill", "tern_chain_plan", "tern_gemv_chain", "i8_head_argmax",
                "i8_head_argmax_i8", "tern5_pack", "tern5_gemv", "tern5_gemv_i8", "fv5b_head_gemv", "fv5b_head_gemv_i8",
@@ -46,7 +50,8 @@ _INT_STATUS = ("tern_pack", "tern_stats", "tern_quantize_i8", "tern_gemv", "tern
                "tern_launch_probe", "i8_head_argmax_noalloc", "i8_head_pack", "i8_head_gemv_packed",
                "i8_head_gemv_packed_i8", "i8_head_argmax_packed", "i8_head_argmax_packed_i8",
                "fv5b_head_gemv_packed", "fv5b_head_gemv_packed_i8", "fv5b_head_argmax_packed",
-               "fv5b_head_argmax_packed_i8")
+               "fv5b_head_argmax_packed_i8", "qk_norm_rope", "i8_kv_append", "i8_kv_read", "i8_kv_attend")
+KV_BLOCK = 64
 
 _lib = None
 _i64 = ctypes.c_int64
@@ -56,6 +61,23 @@ _p = ctypes.c_void_p
 class TernChainStep(ctypes.Structure):
     """struct tern_chain_step of include/tern.h."""
     _fields_ = [("packed", _p), ("N", _i64), ("K", _i64), ("x", _p), ("x_from", _i64), ("y", _p)]
+
+
+class _KvCache(ctypes.Structure):
+    """struct i8_kv_cache of include/tern.h."""
+    _fields_ = [("codes", _p), ("scales", _p), ("blocks", _i64), ("heads", _i64), ("D", _i64)]
+
+
+class _KvBatch(ctypes.Structure):
+    """struct i8_kv_batch of include/tern.h."""
+    _fields_ = [("cu", _p), ("lens", _p), ("table", _p), ("nseq", _i64), ("table_width", _i64),
+                ("table_stride", _i64)]
+
+
+class _QkTransform(ctypes.Structure):
+    """struct tern_qk_transform of include/tern.h."""
+    _fields_ = [("q_gain", _p), ("k_gain", _p), ("inv_freq", _p), ("eps", ctypes.c_float),
+                ("interleaved", ctypes.c_int32)]
 
 
 def lib():
@@ -121,6 +143,15 @@ def lib():
         L.fv5b_head_gemv_packed_i8.argtypes = [_p, _p, _i64, _i64, _p, _p, _i64, _p, _p, _p]
         L.fv5b_head_argmax_packed.argtypes = [_p, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p]
         L.fv5b_head_argmax_packed_i8.argtypes = [_p, _p, _i64, _i64, _p, _p, _i64, _p, _p, _p, _p, _p]
+        cache, batch, transform = (ctypes.POINTER(t) for t in (_KvCache, _KvBatch, _QkTransform))
+        L.qk_norm_rope.argtypes = [transform, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, ctypes.c_int, _p, _p, _p,
+                                   ctypes.c_int, _p]
+        L.i8_kv_append.argtypes = [cache, batch, transform, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, ctypes.c_int,
+                                   _p, _p, _p]
+        L.i8_kv_read.argtypes = [cache, batch, _i64, _p, _p, ctypes.c_int, _p]
+        L.i8_kv_attend_workspace_bytes.restype = _i64
+        L.i8_kv_attend_workspace_bytes.argtypes = [_i64] * 6
+        L.i8_kv_attend.argtypes = [cache, batch, _i64, _p, _i64, _i64, ctypes.c_float, _i64, _i64, _p, _p, _p]
         for name in _INT_STATUS:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -713,3 +744,279 @@ def tern_mfma_peak(kind: str, iters: int, grid: int, sink=None, stream=None):
         sink = torch.empty(int(lib().tern_mfma_peak_sink_bytes(grid)) // 4, dtype=torch.int32, device="cuda")
     _check("tern_mfma_peak", lib().tern_mfma_peak(k, iters, grid, _ptr(sink), _stream(stream)))
     return ops
+
+
+# ---- attention over a paged int8 cache ----
+
+def _vec(t, name, dtype, shape, device=None):
+    """A contiguous device tensor of one dtype and shape (None: any size)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise RuntimeError(f"{name} must be a CUDA/HIP tensor")
+    if t.dtype != dtype:
+        raise RuntimeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+        raise RuntimeError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise RuntimeError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise RuntimeError(f"{name} is on {t.device}, expected {device}")
+
+
+def _rows(t, name, dtypes, device=None, heads=None, d=None, tokens=None):
+    """A [T, heads, D] tensor whose rows may be strided and whose heads are contiguous; its row stride."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise RuntimeError(f"{name} must be a CUDA/HIP tensor")
+    if t.dtype not in dtypes:
+        raise RuntimeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 3:
+        raise RuntimeError(f"{name} must be [T, heads, D]")
+    for got, want, what in zip(t.shape, (tokens, heads, d), ("T", "heads", "D")):
+        if want is not None and got != want:
+            raise RuntimeError(f"{name} has {what} = {got}, expected {want}")
+    if device is not None and t.device != device:
+        raise RuntimeError(f"{name} is on {t.device}, expected {device}")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise RuntimeError(f"{name}: the heads of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+class _on:
+    """Make a tensor's device the current one for a call (nothing to do where it already is)."""
+
+    def __init__(self, device):
+        import torch
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _device_stream(device, stream):
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def _new(shape, dtype, device, stream):
+    """An output or workspace for one call; memory used on a stream that is not the current one is kept
+    from reuse until that stream is done with it."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and stream != torch.cuda.current_stream(device):
+        t.record_stream(stream)
+    return t
+
+
+class QkTransform:
+    """Norm gains (fp32 [D]), inverse frequencies (fp64 [D/2], radians per position) and rotation
+    style of one layer's query and key heads; None leaves a part out."""
+
+    def __init__(self, d: int, q_gain=None, k_gain=None, eps: float = 1e-6, inv_freq=None, interleaved: bool = False):
+        import torch
+        self.d, self.q_gain, self.k_gain, self.inv_freq = d, q_gain, k_gain, inv_freq
+        self.device = None
+        for t, name, dtype, n in ((q_gain, "q_gain", torch.float32, d), (k_gain, "k_gain", torch.float32, d),
+                                  (inv_freq, "inv_freq", torch.float64, d // 2)):
+            if t is not None:
+                _vec(t, name, dtype, (n,), self.device)
+                self.device = t.device
+        self.c = _QkTransform(_addr(q_gain), _addr(k_gain), _addr(inv_freq), eps, int(interleaved))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+class I8KvCache:
+    """A paged int8 key/value cache: codes int8 [blocks, heads, 2, 64*D], scales fp32 [blocks, heads, 2]
+    (one for each block of 64 tokens, head and side K, V).  Allocated here, or over tensors given."""
+
+    def __init__(self, blocks: int = 0, heads: int = 0, d: int = 0, device="cuda", codes=None, scales=None):
+        import torch
+        if codes is None:
+            codes = torch.zeros((blocks, heads, 2, KV_BLOCK * d), dtype=torch.int8, device=device)
+            scales = torch.zeros((blocks, heads, 2), dtype=torch.float32, device=device)
+        _vec(codes, "codes", torch.int8, (None, None, 2, None))
+        blocks, heads, _, width = codes.shape
+        if width not in (KV_BLOCK * 64, KV_BLOCK * 128):
+            raise RuntimeError(f"codes hold {width} bytes a side, expected 64 * D with D 64 or 128")
+        _vec(scales, "scales", torch.float32, (blocks, heads, 2), codes.device)
+        self.codes, self.scales, self.device = codes, scales, codes.device
+        self.blocks, self.heads, self.d = blocks, heads, width // KV_BLOCK
+        self.c = _KvCache(codes.data_ptr(), scales.data_ptr(), blocks, heads, self.d)
+
+
+class I8KvBatch:
+    """The sequences of a step: cu int32 [nseq+1] (rows cu[i]..cu[i+1]-1 are the newest tokens of
+    sequence i), lens int32 [nseq] (lengths with them), table int32 [nseq, width] (their blocks).
+    The kernels read all three, so they may be changed in place between calls."""
+
+    def __init__(self, cu, lens, table):
+        import torch
+        _vec(cu, "cu", torch.int32, (None,))
+        nseq = cu.shape[0] - 1
+        if nseq < 0:
+            raise RuntimeError("cu needs nseq + 1 entries")
+        _vec(lens, "lens", torch.int32, (nseq,), cu.device)
+        if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.device != cu.device:
+            raise RuntimeError("table must be an int32 tensor on the device of cu")
+        if table.dim() != 2 or table.shape[0] != nseq or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise RuntimeError(f"table has shape {tuple(table.shape)}, expected ({nseq}, width) with contiguous rows")
+        self.cu, self.lens, self.table, self.device, self.nseq = cu, lens, table, cu.device, nseq
+        self.width = table.shape[1]
+        stride = table.stride(0) if nseq > 1 else self.width
+        self.c = _KvBatch(cu.data_ptr(), lens.data_ptr(), table.data_ptr(), nseq, self.width, stride)
+
+
+def _kv_types():
+    import torch
+    return {torch.float32: 0, torch.bfloat16: 1}
+
+
+def qk_norm_rope(transform, q, k, pos=None, q_out=None, k_out=None, out_dtype=None, stream=None):
+    """Norm and rotation of q [T, Hq, D] and k [T, Hk, D] (fp32 or bf16 rows, e.g. parts of one fused
+    row; either may be None) at positions pos int32 [T]: (q, k) contiguous, out_dtype bf16 (default) or fp32."""
+    import torch
+    types = _kv_types()
+    x = q if q is not None else k
+    if x is None:
+        raise RuntimeError("qk_norm_rope: q or k is needed")
+    device = x.device
+    args = []
+    outs = []
+    if out_dtype is None:
+        out_dtype = q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else torch.bfloat16
+    if out_dtype not in types:
+        raise RuntimeError(f"out_dtype {out_dtype}, expected one of {tuple(types)}")
+    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            args += [None, 0, 0]
+            outs.append(None)
+            continue
+        stride = _rows(t, name, (x.dtype,) if x.dtype in types else tuple(types), device, None, transform.d,
+                       x.shape[0])
+        args += [t.data_ptr(), t.shape[1], stride]
+        if out is None:
+            out = _new(t.shape, out_dtype, device, stream)
+        else:
+            _vec(out, f"{name}_out", out_dtype, tuple(t.shape), device)
+        outs.append(out)
+    if transform.device is not None and transform.device != device:
+        raise RuntimeError(f"transform is on {transform.device}, expected {device}")
+    if pos is not None:
+        _vec(pos, "pos", torch.int32, (x.shape[0],), device)
+    with _on(device):
+        _check("qk_norm_rope", lib().qk_norm_rope(ctypes.byref(transform.c), x.shape[0], transform.d, *args,
+                                                  types[x.dtype], _addr(pos), _addr(outs[0]), _addr(outs[1]),
+                                                  types[out_dtype], _device_stream(device, stream)))
+    return tuple(outs)
+
+
+def _kv_device(cache, batch, transform=None):
+    if batch.device != cache.device:
+        raise RuntimeError(f"batch is on {batch.device}, expected {cache.device}")
+    if transform is not None and transform.device is not None and transform.device != cache.device:
+        raise RuntimeError(f"transform is on {transform.device}, expected {cache.device}")
+    return cache.device
+
+
+def i8_kv_append(cache, batch, transform, k, v, q=None, pos=None, q_out=None, stream=None):
+    """Append k, v [T, heads, D] (fp32 or bf16 rows) to the cache, k normalised and rotated on the way;
+    with q [T, Hq, D] also its norm and rotation -> q bf16 [T, Hq, D] (else None)."""
+    import torch
+    types = _kv_types()
+    device = _kv_device(cache, batch, transform)
+    if transform.d != cache.d:
+        raise RuntimeError(f"transform is for D = {transform.d}, the cache for {cache.d}")
+    ks = _rows(k, "k", tuple(types), device, cache.heads, cache.d)
+    tokens = k.shape[0]
+    vs = _rows(v, "v", (k.dtype,), device, cache.heads, cache.d, tokens)
+    hq = qs = 0
+    if q is not None:
+        qs = _rows(q, "q", (k.dtype,), device, None, cache.d, tokens)
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = _new(q.shape, torch.bfloat16, device, stream)
+        else:
+            _vec(q_out, "q_out", torch.bfloat16, tuple(q.shape), device)
+    elif q_out is not None:
+        raise RuntimeError("q_out without q")
+    if pos is not None:
+        _vec(pos, "pos", torch.int32, (tokens,), device)
+    with _on(device):
+        _check("i8_kv_append", lib().i8_kv_append(ctypes.byref(cache.c), ctypes.byref(batch.c),
+                                                  ctypes.byref(transform.c), tokens, _addr(q), hq, qs, k.data_ptr(),
+                                                  ks, v.data_ptr(), vs, types[k.dtype], _addr(pos), _addr(q_out),
+                                                  _device_stream(device, stream)))
+    return q_out
+
+
+def i8_kv_read(cache, batch, tokens: int, dtype=None, k_out=None, v_out=None, stream=None):
+    """The batch's tokens (`tokens` rows) read back from the cache: (k, v) [T, heads, D], bf16 or fp32."""
+    import torch
+    types = _kv_types()
+    device = _kv_device(cache, batch)
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.bfloat16
+    if dtype not in types:
+        raise RuntimeError(f"dtype {dtype}, expected one of {tuple(types)}")
+    outs = []
+    for out, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if out is None:
+            out = _new((tokens, cache.heads, cache.d), dtype, device, stream)
+        else:
+            _vec(out, name, dtype, (tokens, cache.heads, cache.d), device)
+        outs.append(out)
+    with _on(device):
+        _check("i8_kv_read", lib().i8_kv_read(ctypes.byref(cache.c), ctypes.byref(batch.c), tokens, _addr(outs[0]),
+                                              _addr(outs[1]), types[dtype], _device_stream(device, stream)))
+    return tuple(outs)
+
+
+def i8_kv_attend_workspace_bytes(tokens: int, hq: int, heads: int, d: int, nseq: int, max_len: int) -> int:
+    return int(lib().i8_kv_attend_workspace_bytes(tokens, hq, heads, d, nseq, max_len))
+
+
+def i8_kv_attend_workspace(cache, batch, tokens: int, hq: int, max_len=None):
+    """A workspace for i8_kv_attend of `tokens` rows of hq heads (None where none is needed)."""
+    import torch
+    nbytes = i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, cache.d, batch.nseq,
+                                          max_len or max(1, batch.width * KV_BLOCK))
+    if nbytes < 0:
+        _check("i8_kv_attend_workspace_bytes", 2)
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
+
+
+def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, out=None, workspace=None, stream=None):
+    """Attention of q bf16 [T, Hq, D] over the batch's cached tokens, causal, with a sliding window
+    where window > 0 -> bf16 [T, Hq, D].  scale: D ** -0.5 by default.  max_len: the longest length
+    that batch.lens will hold (default: what the table can hold)."""
+    import torch
+    device = _kv_device(cache, batch)
+    stride = _rows(q, "q", (torch.bfloat16,), device, None, cache.d)
+    tokens, hq = q.shape[0], q.shape[1]
+    max_len = max_len or max(1, batch.width * KV_BLOCK)
+    if out is None:
+        out = _new(q.shape, torch.bfloat16, device, stream)
+    else:
+        _vec(out, "out", torch.bfloat16, tuple(q.shape), device)
+    need = lib().i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, cache.d, batch.nseq, max_len)
+    if workspace is None:
+        if need > 0:
+            workspace = _new(need, torch.uint8, device, stream)
+    elif workspace.device != device or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < need:
+        raise RuntimeError(f"workspace must be a contiguous tensor of at least {need} bytes on {device}")
+    with _on(device):
+        _check("i8_kv_attend", lib().i8_kv_attend(ctypes.byref(cache.c), ctypes.byref(batch.c), tokens, q.data_ptr(),
+                                                  hq, stride, cache.d ** -0.5 if scale is None else scale, window,
+                                                  max_len, out.data_ptr(), _addr(workspace),
+                                                  _device_stream(device, stream)))
+    return out

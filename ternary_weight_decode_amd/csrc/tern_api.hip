@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <vector>
@@ -604,6 +605,163 @@ int fv5b_embed(const int8_t* W, const float* S, int64_t V, int64_t K, const int3
     int rc = check_device();
     if (rc) return rc;
     return finish(tern::launch_fv5b_embed(W, S, V, K, ids, M, out, out_bf16, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+// ---- attention over the paged int8 cache ----
+namespace {
+
+constexpr int64_t kKvMaxRows = 1 << 24;     // rows of a per-token tensor, sequences of a batch
+constexpr int64_t kKvMaxHeads = 1024;
+constexpr int64_t kKvMaxGrid = 0x7FFFFFFF;  // workgroups of one launch
+
+bool kv_bad_d(int64_t D) { return D != 64 && D != 128; }
+bool kv_bad_type(int t) { return t != TERN_F32 && t != TERN_BF16; }
+
+// a per-token tensor's row stride: a row fits, every row 16-byte aligned
+bool kv_bad_stride(int64_t heads, int64_t D, int64_t stride, int type)
+{
+    return stride < heads * D || stride % (type == TERN_F32 ? 4 : 8) != 0;
+}
+
+int kv_check_transform(const tern_qk_transform* f)
+{
+    if (!f) return TERN_E_NULL;
+    if ((f->q_gain && !aligned16(f->q_gain)) || (f->k_gain && !aligned16(f->k_gain)) ||
+        (f->inv_freq && ((uintptr_t)f->inv_freq & 7u)))
+        return TERN_E_ALIGN;
+    return TERN_OK;
+}
+
+tern::QkTransform kv_transform(const tern_qk_transform* f)
+{
+    return {f->q_gain, f->k_gain, f->inv_freq, f->eps, f->interleaved};
+}
+
+// shapes of a cache, a batch and T rows; *empty when there is nothing to do
+int kv_check_shape(const i8_kv_cache* c, const i8_kv_batch* b, int64_t T, bool* empty)
+{
+    if (!c || !b) return TERN_E_NULL;
+    if (kv_bad_d(c->D) || c->heads < 1 || c->heads > kKvMaxHeads || c->blocks < 0 || c->blocks > kKvMaxGrid)
+        return TERN_E_SHAPE;
+    if (b->nseq < 0 || b->nseq > kKvMaxRows || b->table_width < 0 || b->table_width > kKvMaxGrid / TERN_KV_BLOCK ||
+        b->table_stride < b->table_width || T < 0 || T > kKvMaxRows)
+        return TERN_E_SHAPE;
+    if ((T / TERN_KV_BLOCK + 2 * b->nseq) * c->heads > kKvMaxGrid) return TERN_E_SHAPE;
+    *empty = T == 0 || b->nseq == 0;
+    return TERN_OK;
+}
+
+int kv_check_pointers(const i8_kv_cache* c, const i8_kv_batch* b)
+{
+    if ((c->blocks > 0 && (!c->codes || !c->scales)) || !b->cu || !b->lens || (b->table_width > 0 && !b->table))
+        return TERN_E_NULL;
+    if ((c->codes && !aligned16(c->codes)) || (c->scales && !aligned4(c->scales)) || !aligned4(b->cu) ||
+        !aligned4(b->lens) || (b->table && !aligned4(b->table)))
+        return TERN_E_ALIGN;
+    return TERN_OK;
+}
+
+tern::KvCache kv_cache(const i8_kv_cache* c) { return {c->codes, c->scales, c->blocks, (int)c->heads}; }
+
+tern::KvBatch kv_batch(const i8_kv_batch* b, int64_t T)
+{
+    return {b->cu, b->lens, b->table, (int)b->nseq, b->table_width, b->table_stride, (int)T};
+}
+
+}  // namespace
+
+extern "C" {
+
+int qk_norm_rope(const tern_qk_transform* f, int64_t T, int64_t D, const void* q, int64_t Hq, int64_t q_stride,
+                 const void* k, int64_t Hk, int64_t k_stride, int in_type, const int32_t* pos, void* q_out,
+                 void* k_out, int out_type, void* stream)
+{
+    if (kv_bad_d(D) || T < 0 || T > kKvMaxRows || Hq < 0 || Hk < 0 || Hq > kKvMaxHeads || Hk > kKvMaxHeads ||
+        kv_bad_type(in_type) || kv_bad_type(out_type) || T * ((Hq + Hk + 15) / 16) > kKvMaxGrid)
+        return TERN_E_SHAPE;
+    if ((Hq > 0 && kv_bad_stride(Hq, D, q_stride, in_type)) || (Hk > 0 && kv_bad_stride(Hk, D, k_stride, in_type)))
+        return TERN_E_SHAPE;
+    if (T == 0 || Hq + Hk == 0) return TERN_OK;
+    int rc = kv_check_transform(f);
+    if (rc) return rc;
+    if ((Hq > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out)) || (f->inv_freq && !pos)) return TERN_E_NULL;
+    if ((Hq > 0 && (!aligned16(q) || !aligned16(q_out))) || (Hk > 0 && (!aligned16(k) || !aligned16(k_out))) ||
+        (f->inv_freq && !aligned4(pos)))
+        return TERN_E_ALIGN;
+    if ((rc = check_device())) return rc;
+    return finish(tern::launch_qk_norm_rope(kv_transform(f), T, D, q, Hq, q_stride, k, Hk, k_stride,
+                                            in_type == TERN_BF16, pos, q_out, k_out, out_type == TERN_BF16,
+                                            (hipStream_t)stream));
+}
+
+int i8_kv_append(const i8_kv_cache* cache, const i8_kv_batch* batch, const tern_qk_transform* f, int64_t T,
+                 const void* q, int64_t Hq, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                 int64_t v_stride, int in_type, const int32_t* pos, uint16_t* q_out, void* stream)
+{
+    bool empty = false;
+    int rc = kv_check_shape(cache, batch, T, &empty);
+    if (rc) return rc;
+    if (kv_bad_type(in_type) || Hq < 0 || Hq > kKvMaxHeads || Hq % cache->heads != 0 ||
+        kv_bad_stride(cache->heads, cache->D, k_stride, in_type) ||
+        kv_bad_stride(cache->heads, cache->D, v_stride, in_type) ||
+        (Hq > 0 && kv_bad_stride(Hq, cache->D, q_stride, in_type)))
+        return TERN_E_SHAPE;
+    if (empty) return TERN_OK;
+    if ((rc = kv_check_transform(f)) || (rc = kv_check_pointers(cache, batch))) return rc;
+    if (!k || !v || (Hq > 0 && (!q || !q_out))) return TERN_E_NULL;
+    if (!aligned16(k) || !aligned16(v) || (Hq > 0 && (!aligned16(q) || !aligned16(q_out))) || (pos && !aligned4(pos)))
+        return TERN_E_ALIGN;
+    if ((rc = check_device())) return rc;
+    return finish(tern::launch_kv_append(kv_cache(cache), kv_batch(batch, T), cache->D, kv_transform(f), q, Hq,
+                                         q_stride, k, k_stride, v, v_stride, in_type == TERN_BF16, pos, q_out,
+                                         (hipStream_t)stream));
+}
+
+int i8_kv_read(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, void* k_out, void* v_out, int out_type,
+               void* stream)
+{
+    bool empty = false;
+    int rc = kv_check_shape(cache, batch, T, &empty);
+    if (rc) return rc;
+    if (kv_bad_type(out_type)) return TERN_E_SHAPE;
+    if (empty) return TERN_OK;
+    if ((rc = kv_check_pointers(cache, batch))) return rc;
+    if (!k_out || !v_out) return TERN_E_NULL;
+    if (!aligned16(k_out) || !aligned16(v_out)) return TERN_E_ALIGN;
+    if ((rc = check_device())) return rc;
+    return finish(tern::launch_kv_read(kv_cache(cache), kv_batch(batch, T), cache->D, k_out, v_out,
+                                       out_type == TERN_BF16, (hipStream_t)stream));
+}
+
+int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
+{
+    if (kv_bad_d(D) || T < 0 || T > kKvMaxRows || heads < 1 || heads > kKvMaxHeads || Hq < 1 || Hq > kKvMaxHeads ||
+        Hq % heads != 0 || T * Hq > kKvMaxGrid || nseq < 0 || nseq > kKvMaxRows || max_len < 1 ||
+        max_len > kKvMaxGrid)
+        return -1;
+    if (T == 0 || nseq == 0) return 0;
+    return tern::kv_attend_workspace_bytes(T, Hq, heads, D, nseq, max_len);
+}
+
+int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
+                 int64_t q_stride, float scale, int64_t window, int64_t max_len, uint16_t* out, void* workspace,
+                 void* stream)
+{
+    bool empty = false;
+    int rc = kv_check_shape(cache, batch, T, &empty);
+    if (rc) return rc;
+    const int64_t need = i8_kv_attend_workspace_bytes(T, Hq, cache->heads, cache->D, batch->nseq, max_len);
+    if (need < 0 || window < 0 || !std::isfinite(scale) || kv_bad_stride(Hq, cache->D, q_stride, TERN_BF16))
+        return TERN_E_SHAPE;
+    if (empty) return TERN_OK;
+    if ((rc = kv_check_pointers(cache, batch))) return rc;
+    if (!q || !out || (need > 0 && !workspace)) return TERN_E_NULL;
+    if (!aligned16(q) || !aligned16(out) || (need > 0 && !aligned16(workspace))) return TERN_E_ALIGN;
+    if ((rc = check_device())) return rc;
+    return finish(tern::launch_kv_attend(kv_cache(cache), kv_batch(batch, T), cache->D, q, Hq, q_stride, scale,
+                                         window, max_len, out, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,100 @@
+// tern_kv.h — the paged int8 key/value cache: layout, batch lookup and the
+// arguments that the append, read and attention kernels share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace tern {
+
+constexpr int kKvBlock = 64;   // tokens per cache block: one scale for each block, head and side
+
+struct KvCache {
+    int8_t* codes;             // [blocks][heads][2][64*D]
+    float* scales;             // [blocks][heads][2]
+    int64_t blocks;
+    int heads;
+};
+
+struct KvBatch {
+    const int32_t* cu;
+    const int32_t* lens;
+    const int32_t* table;
+    int nseq;
+    int64_t table_width, table_stride;
+    int T;                     // rows of the per-token tensors
+};
+
+struct QkTransform {
+    const float* q_gain;
+    const float* k_gain;
+    const double* inv_freq;
+    float eps;
+    int interleaved;
+};
+
+// byte of a code inside its (block, head, side): the order of include/tern.h
+template <int D>
+__device__ __forceinline__ int kv_k_byte(int token, int d)
+{
+    return ((((token >> 4) * (D / 64) + (d >> 6)) * 4 + ((d >> 4) & 3)) * 16 + (token & 15)) * 16 + (d & 15);
+}
+
+__device__ __forceinline__ int kv_v_byte(int token, int d)
+{
+    return (((d >> 4) * 4 + ((token >> 2) & 3)) * 16 + (d & 15)) * 16 + ((token >> 4) << 2) + (token & 3);
+}
+
+// One sequence of a batch: its rows [t0, t0 + n) and the position of row t0.
+struct KvSeq {
+    int i, t0, n;
+    int64_t p0;
+};
+
+// Work items of a batch whose row counts only the device knows: sequence i
+// owns the items from cu[i] * mul / div + i * extra on, which leaves it at
+// least ceil(n * mul / div) + extra - 1 items (floor(a + b) - floor(a) >=
+// floor(b)).  Finds the owner of `item` and the item's number inside it; all
+// lanes of a wave call it together (64 entries of cu at a time, so the lookup
+// is one load's latency for up to 64 sequences).  False: no such sequence, or
+// rows outside the tensors.
+__device__ __forceinline__ bool kv_find(const KvBatch& b, int64_t item, int mul, int div, int extra, KvSeq& s,
+                                        int64_t& local)
+{
+    const int lane = threadIdx.x & 63;
+    int owners = 0;
+    for (int c = 0; c < b.nseq; c += 64) {
+        const int i = c + lane;
+        const bool in = i < b.nseq && (int64_t)b.cu[i] * mul / div + (int64_t)i * extra <= item;
+        const int got = __popcll(__ballot(in));
+        owners += got;
+        if (got < 64) break;
+    }
+    if (owners == 0) return false;
+    s.i = owners - 1;
+    s.t0 = b.cu[s.i];
+    const int t1 = b.cu[s.i + 1];
+    s.n = t1 - s.t0;
+    if (s.t0 < 0 || t1 > b.T || s.n <= 0) return false;
+    s.p0 = (int64_t)b.lens[s.i] - s.n;
+    local = item - ((int64_t)s.t0 * mul / div + (int64_t)s.i * extra);
+    return local >= 0;
+}
+
+// Physical block of a sequence's block, -1 where there is none.
+__device__ __forceinline__ int64_t kv_block(const KvBatch& b, const KvCache& c, int seq, int64_t block)
+{
+    if (block < 0 || block >= b.table_width) return -1;
+    const int64_t phys = b.table[(int64_t)seq * b.table_stride + block];
+    return phys >= 0 && phys < c.blocks ? phys : -1;
+}
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
+
+// nearest-even, NaN kept
+__device__ __forceinline__ uint16_t f32_to_bf16(float f)
+{
+    return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
+}  // namespace tern

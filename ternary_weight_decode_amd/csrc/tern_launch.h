@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "tern_kv.h"
 #include "tern_oneshot.h"
 
 namespace tern {
@@ -129,6 +130,20 @@ hipError_t launch_gemv5_bf16(const uint8_t* packed, int64_t N, int64_t K, const 
                              hipStream_t stream);
 hipError_t launch_gemv5_i8(const uint8_t* packed, int64_t N, int64_t K, const int8_t* q, const float* s_x, int64_t M,
                            float* y, int32_t* acc, hipStream_t stream);
+
+// ---- query/key norm with rotation, paged int8 cache and its attention ----
+hipError_t launch_qk_norm_rope(const QkTransform& f, int64_t T, int64_t D, const void* q, int64_t Hq,
+                               int64_t q_stride, const void* k, int64_t Hk, int64_t k_stride, bool in_bf16,
+                               const int32_t* pos, void* q_out, void* k_out, bool out_bf16, hipStream_t stream);
+hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, int64_t D, const QkTransform& f, const void* q,
+                            int64_t Hq, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, bool in_bf16, const int32_t* pos, uint16_t* q_out, hipStream_t stream);
+hipError_t launch_kv_read(const KvCache& c, const KvBatch& b, int64_t D, void* k_out, void* v_out, bool out_bf16,
+                          hipStream_t stream);
+int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len);
+hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
+                            int64_t q_stride, float scale, int64_t window, int64_t max_len, uint16_t* out,
+                            void* workspace, hipStream_t stream);
 
 // ---- matrix-core throughput probe (measurement aid) ----
 double mfma_peak_ops(int kind, int64_t iters, int64_t grid);

@@ -476,7 +476,7 @@ typedef enum { TERN_F32 = 0, TERN_BF16 = 1 } tern_type;
 
 typedef struct i8_kv_cache {
     int8_t* codes;        /* 16-byte aligned */
-    float* scales;        /* 4-byte aligned */
+    float* scales;        /* 8-byte aligned */
     int64_t blocks, heads, D;
 } i8_kv_cache;
 

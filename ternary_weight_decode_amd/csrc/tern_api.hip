@@ -657,7 +657,7 @@ int kv_check_pointers(const i8_kv_cache* c, const i8_kv_batch* b)
 {
     if ((c->blocks > 0 && (!c->codes || !c->scales)) || !b->cu || !b->lens || (b->table_width > 0 && !b->table))
         return TERN_E_NULL;
-    if ((c->codes && !aligned16(c->codes)) || (c->scales && !aligned4(c->scales)) || !aligned4(b->cu) ||
+    if ((c->codes && !aligned16(c->codes)) || (c->scales && ((uintptr_t)c->scales & 7u)) || !aligned4(b->cu) ||
         !aligned4(b->lens) || (b->table && !aligned4(b->table)))
         return TERN_E_ALIGN;
     return TERN_OK;
@@ -667,7 +667,7 @@ tern::KvCache kv_cache(const i8_kv_cache* c) { return {c->codes, c->scales, c->b
 
 tern::KvBatch kv_batch(const i8_kv_batch* b, int64_t T)
 {
-    return {b->cu, b->lens, b->table, (int)b->nseq, b->table_width, b->table_stride, (int)T};
+    return {b->cu, b->lens, b->table, (int)b->nseq, (int)b->table_width, b->table_stride, (int)T};
 }
 
 }  // namespace

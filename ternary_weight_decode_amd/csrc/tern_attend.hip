@@ -22,8 +22,14 @@
 //                  its digits); int32 sums, scaled into the fp32 accumulator
 //                  once a block.
 // Every wave walks its own blocks with a running maximum and sum; the waves
-// of a workgroup meet in LDS at the end, the parts of a long sequence in a
-// second kernel.
+// of a workgroup meet in LDS at the end.
+//
+// Long sequences are split.  Only the device knows the lengths (a captured
+// graph follows them), so it also makes the split: the blocks of all units
+// (tile of columns, head) stand in one line, each unit padded to whole turns
+// of a workgroup's waves, and every workgroup takes an equal stretch of it.
+// A unit that lies in one stretch is written at once, the parts of the others
+// are joined by a second kernel.
 #include "tern_device.h"
 #include "tern_kv.h"
 #include "tern_launch.h"
@@ -51,86 +57,130 @@ __device__ __forceinline__ void planes(float a, float b, float c, float d, uint3
     lo = __builtin_amdgcn_perm(cd, ab, 0x06040200u);
 }
 
-// The tile of columns a workgroup or a combining row works on.
+// The tile of columns a workgroup or a joining row works on.
 struct AttTile {
     KvSeq s;
     int col0, cols;            // first column, live columns
-    int64_t b0;                // first block any of them sees
-    int64_t nblk;              // blocks from there to the last one seen
+    int b0;                    // first block any of them sees
+    int nblk;                  // blocks from there to the last one seen
 };
 
-__device__ __forceinline__ int64_t att_first(int64_t pos, int64_t window)
+__device__ __forceinline__ int att_first(int pos, int window)
 {
     return window > 0 && pos >= window ? pos - window + 1 : 0;
 }
 
-__device__ __forceinline__ int64_t att_last(int64_t pos, int64_t limit) { return pos < limit ? pos : limit; }
+__device__ __forceinline__ int att_limit(const KvBatch& b) { return (int)((int64_t)b.table_width * kKvBlock - 1); }
 
-// columns [COLS * tile, + COLS) of the sequence that owns `item`
+__device__ __forceinline__ int att_last(int pos, int limit) { return pos < limit ? pos : limit; }
+
+// columns [COLS * number, + COLS) of a.s
 template <int COLS>
-__device__ __forceinline__ bool att_tile(const KvBatch& b, int64_t item, int G, int64_t window, AttTile& a)
+__device__ __forceinline__ bool att_tile(const KvBatch& b, int number, int G, int window, AttTile& a)
 {
-    int64_t local;
-    if (!kv_find(b, item, G, COLS, 1, a.s, local)) return false;
-    const int64_t total = (int64_t)a.s.n * G;
-    if (local * COLS >= total) return false;
-    a.col0 = (int)(local * COLS);
-    a.cols = (int)(total - a.col0 < COLS ? total - a.col0 : COLS);
-    const int64_t limit = b.table_width * kKvBlock - 1;
-    const int64_t lo = att_first(a.s.p0 + a.col0 / G, window);
-    const int64_t hi = att_last(a.s.p0 + (a.col0 + a.cols - 1) / G, limit);
+    const int64_t total = (int64_t)a.s.n * G, col0 = (int64_t)number * COLS;
+    if (col0 >= total || col0 > INT32_MAX - COLS) return false;
+    a.col0 = (int)col0;
+    a.cols = (int)(total - col0 < COLS ? total - col0 : COLS);
+    const int lo = att_first(a.s.p0 + a.col0 / G, window);
+    const int hi = att_last(a.s.p0 + (a.col0 + a.cols - 1) / G, att_limit(b));
     a.b0 = lo / kKvBlock;
     a.nblk = hi < lo ? 0 : hi / kKvBlock - a.b0 + 1;
     return true;
 }
 
+// A sequence's share of the line: its tiles, and the blocks that each of its
+// units takes there (padded; no tile of the sequence sees more).  None for a
+// sequence without rows.
+struct AttShare {
+    uint32_t tiles, len;
+};
+
+// Values equal in all lanes of a wave, held in scalar registers.
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ void att_uniform(AttTile& a)
+{
+    a.s.i = uni(a.s.i);
+    a.s.t0 = uni(a.s.t0);
+    a.s.n = uni(a.s.n);
+    a.s.p0 = uni(a.s.p0);
+    a.col0 = uni(a.col0);
+    a.cols = uni(a.cols);
+    a.b0 = uni(a.b0);
+    a.nblk = uni(a.nblk);
+}
+
+template <int COLS>
+__device__ __forceinline__ AttShare att_share(const KvBatch& b, int i, int G, int window, KvSeq& s)
+{
+    s.i = i;
+    s.t0 = b.cu[i];
+    const int t1 = b.cu[i + 1];
+    s.n = t1 - s.t0;
+    s.p0 = kv_length(b, i) - s.n;
+    AttShare r = {0, kAttWaves};
+    if (s.t0 < 0 || t1 > b.T || s.n <= 0) return r;
+    r.tiles = (uint32_t)(((int64_t)s.n * G + COLS - 1) / COLS);
+    const int last = att_last(s.p0 + s.n - 1, att_limit(b));
+    uint32_t blocks = last < 0 ? 1 : last / kKvBlock + 1;
+    if (window > 0) {          // a tile spans window + its rows - 1 keys
+        const uint32_t most = ((uint32_t)window + COLS / G + 1) / kKvBlock + 2;
+        blocks = blocks < most ? blocks : most;
+    }
+    r.len = (blocks + kAttWaves - 1) / kAttWaves * kAttWaves;
+    return r;
+}
+
 struct AttArgs {
     const uint16_t* q;
     uint16_t* out;
-    float* part;               // [items][heads][slots][COLS][D] unnormalised sums, then their (max, sum)
+    float* part;               // [workgroups][2][COLS][D] unnormalised sums, then their (max, sum)
     float2* stat;
+    uint32_t* start;           // [nseq] where each sequence starts in the line, then the total
     int64_t q_stride;
-    int64_t window;
+    int window;
     float scale;
     int G;
-    int chunk, slots;          // blocks per workgroup, workgroups along a sequence
+    int groups;                // workgroups that share the line; 0: one workgroup for each unit
 };
 
+// blocks of the line for each of `groups` workgroups
+__device__ __forceinline__ uint32_t att_stretch(uint32_t total, int groups)
+{
+    const uint32_t turn = (uint32_t)groups * kAttWaves;
+    return (total + turn - 1) / turn * kAttWaves;
+}
+
+// blocks [begin, end) of one unit; whole: the result is written, else it is
+// part `slot` of the unit
 template <int D, int CT>
-__global__ __launch_bounds__(64 * kAttWaves) void kv_attend_i8_kernel(KvCache c, KvBatch b, AttArgs a)
+__device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b, const AttArgs& a,
+                                              const AttTile& tile, int h, int begin, int end, bool whole,
+                                              uint32_t slot)
 {
     constexpr int S = D / 64, U = D / 16, COLS = 16 * CT;
     constexpr int kPad = D + 4;
     __shared__ float sacc[kAttWaves][COLS][kPad];
     __shared__ float2 sstat[kAttWaves][COLS];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    // slots fastest: neighbouring workgroups read neighbouring parts of one sequence
-    const int slot = blockIdx.x % a.slots;
-    const int h = blockIdx.x / a.slots % c.heads;
-    const int64_t item = blockIdx.x / a.slots / c.heads;
-    AttTile tile;
-    if (!att_tile<COLS>(b, item, a.G, a.window, tile)) return;
-    const int64_t begin = (int64_t)slot * a.chunk;
-    // the last slot takes what is left (lengths above the caller's bound)
-    const int64_t end = slot == a.slots - 1 || begin + a.chunk > tile.nblk ? tile.nblk : begin + a.chunk;
-    if (begin >= end && slot > 0) return;
 
     // this lane's columns: q as planes, the factor of its scores, the keys it sees
-    const int64_t limit = b.table_width * kKvBlock - 1;
+    const int limit = att_limit(b);
     u32x4 qhi[CT][S], qlo[CT][S];
     float rowf[CT];
-    int64_t first[CT], last[CT];
+    int first[CT], last[CT];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const int col = 16 * ct + n;
         const bool live = col < tile.cols;
         const int cc = tile.col0 + (live ? col : 0);
         const int j = cc / a.G;
-        const uint16_t* row = a.q + (tile.s.t0 + j) * a.q_stride + (int64_t)(h * a.G + cc % a.G) * D;
-        const int64_t pos = tile.s.p0 + j;
+        const uint16_t* row = a.q + (int64_t)(tile.s.t0 + j) * a.q_stride + (int64_t)(h * a.G + cc - j * a.G) * D;
+        const int pos = tile.s.p0 + j;
         first[ct] = live ? att_first(pos, a.window) : 0;
-        last[ct] = live ? att_last(pos, limit) : INT64_MAX;
+        last[ct] = live ? att_last(pos, limit) : INT32_MAX;
         u32x4 raw[S][2];
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -180,31 +230,47 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attend_i8_kernel(KvCache c,
         for (int u = 0; u < U; ++u) acc[ct][u] = f32x4{0, 0, 0, 0};
     }
 
-    for (int64_t seg = begin; seg < end; seg += 64) {
+    for (int seg = begin; seg < end; seg += 64) {
         // lane i looks up block seg + i: its place and scales
-        const int count = (int)(end - seg < 64 ? end - seg : 64);
+        const int count = end - seg < 64 ? end - seg : 64;
         int mine = -1;
         float2 sc = make_float2(0.0f, 0.0f);
         if (lane < count) {
-            mine = (int)kv_block(b, c, tile.s.i, tile.b0 + seg + lane);
+            mine = kv_block(b, c, tile.s.i, tile.b0 + seg + lane);
             if (mine >= 0) sc = *(const float2*)(c.scales + ((int64_t)mine * c.heads + h) * 2);
         }
-        for (int i = wave; i < count; i += kAttWaves) {
-            const int phys = __builtin_amdgcn_readlane(mine, i);
-            if (phys < 0) continue;
-            const float sk = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sc.x), i));
-            const float sv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sc.y), i));
-            const int8_t* kc = c.codes + ((int64_t)phys * c.heads + h) * 2 * (kKvBlock * D);
-            const u32x4* kp = (const u32x4*)kc + lane;
-            const u32x4* vp = (const u32x4*)(kc + kKvBlock * D) + lane;
-            u32x4 kr[4][S], vr[U];
+        // this wave's blocks among those that are there
+        uint64_t todo = __ballot(mine >= 0) & (0x1111111111111111ull << wave);
+        const auto codes = [&](int i) {
+            const int64_t phys = __builtin_amdgcn_readlane(mine, i);
+            return c.codes + (phys * c.heads + h) * 2 * (kKvBlock * D);
+        };
+        // the lane's 16 bytes of a KiB behind a scalar address
+        const uint32_t own = lane * 16;
+        const auto load = [&](const int8_t* p, int byte) { return *(const u32x4*)(p + byte + own); };
+        u32x4 kr[4][S], vr[U];
+        if (todo) {
+            const int8_t* p = codes(__builtin_ctzll(todo));
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int s = 0; s < S; ++s) kr[t][s] = kp[64 * (t * S + s)];
+                for (int s = 0; s < S; ++s) kr[t][s] = load(p, 1024 * (t * S + s));
+            __builtin_amdgcn_sched_barrier(0);           // keys first: they are waited for first
 #pragma unroll
-            for (int u = 0; u < U; ++u) vr[u] = vp[64 * u];
-            const int64_t at = (tile.b0 + seg + i) * kKvBlock;
+            for (int u = 0; u < U; ++u) vr[u] = load(p, 1024 * (U + u));
+        }
+        while (todo) {
+            const int i = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            const float sk = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sc.x), i));
+            const float sv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sc.y), i));
+            // The next block's keys are asked for before this one's softmax, its
+            // values behind this one's; never behind a branch, or the waits
+            // would be for all of them.  Without a next block one KiB of this
+            // one is read 16 times.
+            const int8_t* next = codes(todo ? __builtin_ctzll(todo) : i);
+            const int kib = todo ? 1024 : 0;
+            const int at = (tile.b0 + seg + i) * kKvBlock;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 float x[16];
@@ -219,12 +285,19 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attend_i8_kernel(KvCache c,
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[4 * t + e] = (float)(hi[e] * 256 + lo[e]) * f;
+                    asm volatile("" : "+v"(x[4 * t]), "+v"(x[4 * t + 1]), "+v"(x[4 * t + 2]), "+v"(x[4 * t + 3]));
+                }
+                if (ct == CT - 1) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int s = 0; s < S; ++s) kr[t][s] = load(next, kib * (t * S + s));
                 }
                 const bool sees = first[ct] <= at + 63 && last[ct] >= at;
                 if (__any(first[ct] > at || last[ct] < at + 63)) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int64_t p = at + 16 * (e >> 2) + 4 * g + (e & 3);
+                        const int p = at + 16 * (e >> 2) + 4 * g + (e & 3);
                         x[e] = p >= first[ct] && p <= last[ct] ? x[e] : -INFINITY;
                     }
                 }
@@ -263,8 +336,12 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attend_i8_kernel(KvCache c,
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         acc[ct][u][e] = fmaf((float)(hi[e] * 256 + lo[e]), fv, acc[ct][u][e] * keep);
+                    // in this order: or all sums wait in registers behind the loads below
+                    asm volatile("" : "+v"(acc[ct][u]));
                 }
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) vr[u] = load(next, kib * (U + u));
         }
     }
 
@@ -299,9 +376,9 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attend_i8_kernel(KvCache c,
             sum += st.y * (st.x == top ? 1.0f : exp2_fast(st.x - top));
             o += *(const f32x4*)&sacc[w][col][d];
         }
-        if (a.slots > 1) {
-            const int64_t at = ((item * c.heads + h) * a.slots + slot) * COLS + col;
-            *(f32x4*)(a.part + at * D + d) = o;
+        if (!whole) {
+            const uint32_t at = slot * COLS + col;
+            *(f32x4*)(a.part + (int64_t)at * D + d) = o;
             if (d == 0) a.stat[at] = make_float2(top, sum);
         } else {
             const int cc = tile.col0 + col;
@@ -316,110 +393,218 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attend_i8_kernel(KvCache c,
     }
 }
 
-// Joins the parts of every column: one workgroup per column, its waves take
-// the parts in turn.
-constexpr int kJoinWaves = 8;
-
-template <int D, int COLS>
-__global__ __launch_bounds__(64 * kJoinWaves) void kv_attend_join_kernel(KvCache c, KvBatch b, AttArgs a)
+template <int D, int CT>
+__global__ __launch_bounds__(64 * kAttWaves, CT == 1 ? 3 : 2) void kv_attend_i8_kernel(KvCache c, KvBatch b,
+                                                                                       AttArgs a)
 {
-    __shared__ float so[kJoinWaves][D], sf[kJoinWaves][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int col = blockIdx.x % COLS, h = blockIdx.x / COLS % c.heads;
-    const int64_t item = blockIdx.x / COLS / c.heads;
+    constexpr int COLS = 16 * CT;
+    const int lane = threadIdx.x & 63;
     AttTile tile;
-    if (!att_tile<COLS>(b, item, a.G, a.window, tile) || col >= tile.cols) return;
-    int64_t used = (tile.nblk + a.chunk - 1) / a.chunk;
-    used = used < 1 ? 1 : used > a.slots ? a.slots : used;
-    const int64_t at = (item * c.heads + h) * a.slots * COLS + col;
-    const float2* stat = a.stat + at;
-    const float* part = a.part + at * D + lane;
-    float top = -INFINITY;
-    for (int64_t s = lane; s < used; s += 64) top = fmaxf(top, stat[s * COLS].x);
-    for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
-    float sum = 0.0f, o[D / 64] = {};
-    for (int64_t seg = 0; seg < used; seg += 64) {
-        const int count = (int)(used - seg < 64 ? used - seg : 64);
-        float f = 0.0f;
-        if (lane < count) {
-            const float2 st = stat[(seg + lane) * COLS];
-            f = st.x == top ? 1.0f : exp2_fast(st.x - top);
-            sum += st.y * f;
+    AttShare r = {0, 1};
+    uint32_t x = 0, x0 = 0, x1 = 1, at = 0;
+    int i = 0;
+    if (a.groups > 0) {
+        // the line: every lane sums the shares of a run of sequences
+        const int run = (b.nseq + 63) / 64;
+        uint32_t mine = 0;
+        for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
+            r = att_share<COLS>(b, k, a.G, a.window, tile.s);
+            mine += r.tiles * c.heads * r.len;
         }
-        sf[wave][lane] = f;              // 0 behind the last part
-        __builtin_amdgcn_wave_barrier();
-        // eight loads in flight; behind the last part its values are read again and weigh 0
-#pragma unroll
-        for (int r = 0; r < 64 / kJoinWaves; ++r) {
-            const int i = wave + kJoinWaves * r, ic = i < count ? i : count - 1;
-            const float fi = sf[wave][i];
-#pragma unroll
-            for (int u = 0; u < D / 64; ++u) {
-                const float x = part[(seg + ic) * COLS * D + u * 64];
-                o[u] = i < count ? fmaf(x, fi, o[u]) : o[u];
+        uint32_t upto = mine;
+        if (b.nseq > 1)
+            for (int off = 1; off < 64; off <<= 1) {
+                const uint32_t o = __shfl(upto, lane - off);
+                if (lane >= off) upto += o;
             }
+        const uint32_t total = __builtin_amdgcn_readlane(upto, b.nseq > 1 ? 63 : 0);
+        if (blockIdx.x == 0 && threadIdx.x < 64) {           // for the joining kernel
+            uint32_t from = upto - mine;
+            for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
+                KvSeq s;
+                const AttShare o = att_share<COLS>(b, k, a.G, a.window, s);
+                a.start[k] = from;
+                from += o.tiles * c.heads * o.len;
+            }
+            if (lane == 0) a.start[b.nseq] = total;
         }
-        __builtin_amdgcn_wave_barrier();
+        const uint32_t per = att_stretch(total, a.groups);
+        if (per > total && blockIdx.x > 0) return;            // the products below stay in 32 bits
+        x0 = x = blockIdx.x * per;
+        x1 = x > total || total - x < per ? total : x + per;
+        if (x >= x1) return;
+        // the lane whose run holds x, then the sequence inside the run
+        const int owner = b.nseq > 1 ? __popcll(__ballot(upto <= x)) : 0;
+        at = __builtin_amdgcn_readlane(upto - mine, owner);
+        i = uni(owner * run);
+        r = att_share<COLS>(b, i, a.G, a.window, tile.s);
+        r = {(uint32_t)uni(r.tiles), (uint32_t)uni(r.len)};
     }
-    for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) so[wave][u * 64 + lane] = o[u];
-    __syncthreads();
-    const int d = threadIdx.x;
-    if (d >= D) return;
-    float y = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJoinWaves; ++w) y += so[w][d];
-    const int cc = tile.col0 + col;
-    a.out[((int64_t)(tile.s.t0 + cc / a.G) * c.heads * a.G + h * a.G + cc % a.G) * D + d] =
-        f32_to_bf16(sum == 0.0f ? 0.0f : y / sum);
+    while (true) {
+        int h, number, begin = 0, end = INT32_MAX;
+        bool whole = true, any;
+        uint32_t slot = 0;
+        if (a.groups == 0) {
+            const uint32_t item = blockIdx.x / c.heads;
+            int64_t local;
+            any = kv_find(b, item, a.G, COLS, 1, tile.s, local);
+            number = any ? uni((int)local) : 0;
+            h = blockIdx.x - item * c.heads;
+            x = x1;
+        } else {
+            while (x - at >= r.tiles * c.heads * r.len) {     // ends: x < total
+                at += r.tiles * c.heads * r.len;
+                r = att_share<COLS>(b, ++i, a.G, a.window, tile.s);
+                r = {(uint32_t)uni(r.tiles), (uint32_t)uni(r.len)};
+            }
+            const uint32_t unit = (x - at) / r.len, from = x - at - unit * r.len;
+            const uint32_t len = r.len - from < x1 - x ? r.len - from : x1 - x;
+            h = (int)(unit / r.tiles);
+            number = (int)(unit - h * r.tiles);
+            begin = (int)from;
+            end = (int)(from + len);
+            whole = len == r.len;
+            slot = blockIdx.x * 2 + (x > x0);
+            x += len;
+            any = true;
+        }
+        if (any && att_tile<COLS>(b, number, a.G, a.window, tile)) {
+            att_uniform(tile);
+            end = end < tile.nblk ? end : tile.nblk;
+            if (begin < end || begin == 0) attend_blocks<D, CT>(c, b, a, tile, h, begin, end, whole, slot);
+        }
+        if (x >= x1) break;
+        __syncthreads();                                      // LDS is used again
+    }
 }
 
-// How a call is cut: columns per workgroup, blocks per workgroup, workgroups
-// along a sequence.
+// Joins the parts of every row and query head that lie in more than one
+// stretch.  JW waves take one row's parts in turn, eight loads each in
+// flight; with one wave a workgroup holds four rows.
+template <int D, int COLS, int JW>
+__global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel(KvCache c, KvBatch b, AttArgs a)
+{
+    constexpr int kRows = JW == 1 ? 4 : 1;
+    __shared__ float so[JW][D];
+    const int lane = threadIdx.x & 63, wave = JW == 1 ? 0 : threadIdx.x >> 6;
+    const uint32_t Hq = c.heads * a.G, id = blockIdx.x * kRows + (JW == 1 ? threadIdx.x >> 6 : 0);
+    const uint32_t t = id / Hq;
+    const int hq = id - t * Hq, h = hq / a.G;
+    AttTile tile;
+    int64_t j;
+    if (t >= (uint32_t)b.T || !kv_find(b, t, 1, 1, 0, tile.s, j) || j >= tile.s.n) return;
+    const uint32_t total = a.start[b.nseq], start = a.start[tile.s.i];
+    const AttShare r = att_share<COLS>(b, tile.s.i, a.G, a.window, tile.s);
+    const int64_t cc = j * a.G + (hq - h * a.G);
+    const int number = (int)(cc / COLS), col = (int)(cc % COLS);
+    if (!att_tile<COLS>(b, number, a.G, a.window, tile)) return;
+    const uint32_t per = att_stretch(total, a.groups);
+    const uint32_t u0 = start + (h * r.tiles + number) * r.len, w0 = u0 / per;
+    if ((u0 + r.len - 1) / per == w0) return;                       // whole: written already
+    const int used = (int)((u0 + (tile.nblk > 0 ? tile.nblk : 1) - 1) / per - w0) + 1;   // parts with blocks seen
+    // part s > 0 starts its stretch, part 0 may start inside one
+    const auto place = [&](int s) { return (2 * (w0 + s) + (s == 0 && u0 > w0 * per)) * COLS + col; };
+    float top = -INFINITY, sum = 0.0f, o[D / 64] = {};
+    for (int seg = 0; seg < used; seg += 8 * JW) {
+        float x[8][D / 64];
+        float2 st[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {               // behind the last part its values are read again, unused
+            const int s = seg + wave + JW * k;
+            const uint32_t at = place(s < used ? s : used - 1);
+            st[k] = a.stat[at];
+            if (s >= used) st[k] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) x[k][u] = a.part[(int64_t)at * D + u * 64 + lane];
+        }
+        float now = top;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) now = fmaxf(now, st[k].x);
+        const float keep = top == now ? 1.0f : exp2_fast(top - now);
+        top = now;
+        sum *= keep;
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) o[u] *= keep;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float f = st[k].x == top ? 1.0f : exp2_fast(st[k].x - top);
+            sum = fmaf(st[k].y, f, sum);
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) o[u] = seg + wave + JW * k < used ? fmaf(x[k][u], f, o[u]) : o[u];
+        }
+    }
+    uint16_t* dst = a.out + (int64_t)id * D;
+    if constexpr (JW == 1) {
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) dst[u * 64 + lane] = f32_to_bf16(sum == 0.0f ? 0.0f : o[u] / sum);
+    } else {
+        __shared__ float2 sst[JW];
+        if (lane == 0) sst[wave] = make_float2(top, sum);
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) so[wave][u * 64 + lane] = o[u];
+        __syncthreads();
+        const int d = threadIdx.x;
+        if (d >= D) return;
+        float y = 0.0f;
+        sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < JW; ++w) top = fmaxf(top, sst[w].x);
+#pragma unroll
+        for (int w = 0; w < JW; ++w) {
+            const float f = sst[w].x == top ? 1.0f : exp2_fast(sst[w].x - top);
+            y = fmaf(so[w][d], f, y);
+            sum = fmaf(sst[w].y, f, sum);
+        }
+        dst[d] = f32_to_bf16(sum == 0.0f ? 0.0f : y / sum);
+    }
+}
+
+// How a call is cut: columns per workgroup, tiles at most, workgroups that
+// share the line (0: one for each unit, no second kernel).
 struct AttPlan {
-    int cols, chunk, slots;
+    int cols, groups;
     int64_t items;
-    int64_t part_floats, stats;
+    int64_t part_floats, stats, starts;
 };
+
+constexpr int64_t kAttGroups = 768;          // three workgroups a CU: what registers allow at once
+constexpr int64_t kAttWholeBlocks = 16;      // up to here a unit is not split
 
 static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
 {
-    AttPlan p;
+    AttPlan p{};
     const int64_t G = Hq / heads;
     p.cols = T * G <= 16 * nseq ? 16 : 32;
     p.items = T * G / p.cols + nseq;
-    const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock, base = p.items * heads;
-    int64_t slots = blocks * base / 1024 < 32 ? 1024 / base : (blocks + 31) / 32;
-    const int64_t most = 8192 / base, useful = (blocks + kAttWaves - 1) / kAttWaves;
-    slots = slots > most ? most : slots;
-    slots = slots > useful ? useful : slots;
-    slots = slots < 1 ? 1 : slots;
-    const int64_t chunk = (blocks + slots - 1) / slots;
-    p.chunk = (int)((chunk + kAttWaves - 1) / kAttWaves * kAttWaves);
-    p.slots = (int)((blocks + p.chunk - 1) / p.chunk);
-    const int64_t n = p.slots > 1 ? p.items * heads * p.slots * p.cols : 0;
-    p.part_floats = n * D;
-    p.stats = n;
+    const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock, units = p.items * heads;
+    if (blocks <= kAttWholeBlocks || units >= 2 * kAttGroups) return p;
+    const int64_t turns = (blocks + kAttWaves - 1) / kAttWaves;
+    p.groups = (int)(units > kAttGroups / turns ? kAttGroups : units * turns);
+    p.stats = p.groups * 2 * p.cols;
+    p.part_floats = p.stats * D;
+    p.starts = nseq + 1;
     return p;
 }
 
 int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
 {
     const AttPlan p = att_plan(T, Hq, heads, D, nseq, max_len);
-    return p.part_floats * 4 + p.stats * 8;
+    return p.part_floats * 4 + p.stats * 8 + p.starts * 4;
 }
 
 template <int D, int CT>
 static hipError_t attend_i8(const KvCache& c, const KvBatch& b, const AttArgs& a, const AttPlan& p,
                             hipStream_t stream)
 {
-    const int64_t grid = p.items * c.heads * p.slots;
+    const int64_t grid = a.groups ? a.groups : p.items * c.heads;
     kv_attend_i8_kernel<D, CT><<<(unsigned)grid, 64 * kAttWaves, 0, stream>>>(c, b, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.slots == 1) return e;
-    kv_attend_join_kernel<D, 16 * CT>
-        <<<(unsigned)(p.items * c.heads * 16 * CT), 64 * kJoinWaves, 0, stream>>>(c, b, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.groups == 0) return e;
+    const int64_t rows = (int64_t)b.T * c.heads * a.G;
+    if ((int64_t)b.nseq * c.heads * 8 >= a.groups)      // about eight parts a row or fewer
+        kv_attend_join_kernel<D, 16 * CT, 1><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(c, b, a);
+    else
+        kv_attend_join_kernel<D, 16 * CT, 12><<<(unsigned)rows, 768, 0, stream>>>(c, b, a);
     return hipGetLastError();
 }
 
@@ -432,13 +617,15 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const
     a.q = q;
     a.out = out;
     a.part = (float*)workspace;
-    a.stat = (float2*)((float*)workspace + p.part_floats);
+    a.stat = (float2*)(a.part + p.part_floats);
+    a.start = (uint32_t*)(a.stat + p.stats);
     a.q_stride = q_stride;
-    a.window = window;
+    a.window = window < INT32_MAX ? (int)window : 0;      // one that nothing is as far as
     a.scale = scale;
     a.G = (int)(Hq / c.heads);
-    a.chunk = p.chunk;
-    a.slots = p.slots;
+    // the line is counted in 32 bits; a batch that could pass that has units enough
+    const int64_t line = p.items * c.heads * ((int64_t)b.table_width + kAttWaves);
+    a.groups = line < (1ll << 31) ? p.groups : 0;
     if (D == 128) return p.cols == 16 ? attend_i8<128, 1>(c, b, a, p, stream) : attend_i8<128, 2>(c, b, a, p, stream);
     return p.cols == 16 ? attend_i8<64, 1>(c, b, a, p, stream) : attend_i8<64, 2>(c, b, a, p, stream);
 }

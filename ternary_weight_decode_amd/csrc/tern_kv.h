@@ -21,7 +21,8 @@ struct KvBatch {
     const int32_t* lens;
     const int32_t* table;
     int nseq;
-    int64_t table_width, table_stride;
+    int table_width;           // at most 2^31 / 64: positions are 32-bit
+    int64_t table_stride;
     int T;                     // rows of the per-token tensors
 };
 
@@ -47,9 +48,11 @@ __device__ __forceinline__ int kv_v_byte(int token, int d)
 
 // One sequence of a batch: its rows [t0, t0 + n) and the position of row t0.
 struct KvSeq {
-    int i, t0, n;
-    int64_t p0;
+    int i, t0, n, p0;
 };
+
+// a negative length is one of 0
+__device__ __forceinline__ int kv_length(const KvBatch& b, int i) { return b.lens[i] > 0 ? b.lens[i] : 0; }
 
 // Work items of a batch whose row counts only the device knows: sequence i
 // owns the items from cu[i] * mul / div + i * extra on, which leaves it at
@@ -76,17 +79,37 @@ __device__ __forceinline__ bool kv_find(const KvBatch& b, int64_t item, int mul,
     const int t1 = b.cu[s.i + 1];
     s.n = t1 - s.t0;
     if (s.t0 < 0 || t1 > b.T || s.n <= 0) return false;
-    s.p0 = (int64_t)b.lens[s.i] - s.n;
+    s.p0 = kv_length(b, s.i) - s.n;
     local = item - ((int64_t)s.t0 * mul / div + (int64_t)s.i * extra);
     return local >= 0;
 }
 
 // Physical block of a sequence's block, -1 where there is none.
-__device__ __forceinline__ int64_t kv_block(const KvBatch& b, const KvCache& c, int seq, int64_t block)
+__device__ __forceinline__ int kv_block(const KvBatch& b, const KvCache& c, int seq, int block)
 {
     if (block < 0 || block >= b.table_width) return -1;
-    const int64_t phys = b.table[(int64_t)seq * b.table_stride + block];
+    const int phys = b.table[(int64_t)seq * b.table_stride + block];
     return phys >= 0 && phys < c.blocks ? phys : -1;
+}
+
+// The rows of a sequence that fall into its `local`-th touched block.
+struct KvSpan {
+    int block;                 // the block's number in the sequence, below 0 in front of it
+    int slot, n;               // first slot, rows
+    int64_t row;               // first row
+};
+
+__device__ __forceinline__ bool kv_span(const KvSeq& s, int64_t local, KvSpan& w)
+{
+    const int64_t block = (s.p0 >> 6) + local;                     // floor: p0 may be negative
+    const int64_t from = block * kKvBlock, end = (int64_t)s.p0 + s.n;
+    const int64_t lo = s.p0 > from ? s.p0 : from, hi = end < from + kKvBlock ? end : from + kKvBlock;
+    if (lo >= hi) return false;
+    w.block = (int)block;
+    w.slot = (int)(lo - from);
+    w.n = (int)(hi - lo);
+    w.row = s.t0 + (lo - s.p0);
+    return true;
 }
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }

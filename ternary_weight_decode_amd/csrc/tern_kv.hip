@@ -192,21 +192,18 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvBatch b, Qk
     KvSeq s;
     int64_t local;
     if (!kv_find(b, blockIdx.x / c.heads, 1, kKvBlock, 2, s, local)) return;
-    const int64_t blk = (s.p0 >> 6) + local;                       // floor: p0 may be negative
-    const int64_t lo = s.p0 > blk * kKvBlock ? s.p0 : blk * kKvBlock;
-    const int64_t end = s.p0 + s.n;
-    const int64_t hi = end < (blk + 1) * kKvBlock ? end : (blk + 1) * kKvBlock;
-    if (lo >= hi) return;
-    const int nt = (int)(hi - lo), o = (int)(lo - blk * kKvBlock);
-    const int64_t t0 = s.t0 + (lo - s.p0);                          // first row
-    const int64_t phys = kv_block(b, c, s.i, blk);
+    KvSpan w;
+    if (!kv_span(s, local, w)) return;
+    const int nt = w.n, o = w.slot;
+    const int64_t t0 = w.row;
+    const int64_t phys = kv_block(b, c, s.i, w.block);
 
     if (threadIdx.x < 2) top[threadIdx.x] = 0;
     if (f.inv_freq)
         for (int i = threadIdx.x; i < nt * (D / 2); i += 256) {
             const int t = i / (D / 2), p = i % (D / 2);
             float cc, ss;
-            turn(pos ? pos[t0 + t] : (int)(lo + t), f.inv_freq[p], cc, ss);
+            turn(pos ? pos[t0 + t] : w.block * kKvBlock + o + t, f.inv_freq[p], cc, ss);
             cs[i] = make_float2(cc, ss);
         }
     __syncthreads();
@@ -299,14 +296,11 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, KvBatch b, TO* 
     KvSeq s;
     int64_t local;
     if (!kv_find(b, blockIdx.x / c.heads, 1, kKvBlock, 2, s, local)) return;
-    const int64_t blk = (s.p0 >> 6) + local;
-    const int64_t lo = s.p0 > blk * kKvBlock ? s.p0 : blk * kKvBlock;
-    const int64_t end = s.p0 + s.n;
-    const int64_t hi = end < (blk + 1) * kKvBlock ? end : (blk + 1) * kKvBlock;
-    if (lo >= hi) return;
-    const int nt = (int)(hi - lo), o = (int)(lo - blk * kKvBlock);
-    const int64_t t0 = s.t0 + (lo - s.p0);
-    const int64_t phys = kv_block(b, c, s.i, blk);
+    KvSpan w;
+    if (!kv_span(s, local, w)) return;
+    const int nt = w.n, o = w.slot;
+    const int64_t t0 = w.row;
+    const int64_t phys = kv_block(b, c, s.i, w.block);
     const float* scales = c.scales + (phys * c.heads + h) * 2;
     const int8_t* kc = c.codes + (phys * c.heads + h) * 2 * (kKvBlock * D);
     const int8_t* vc = kc + kKvBlock * D;

@@ -393,9 +393,265 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
     }
 }
 
+// kv_attend_f16: 128 columns per workgroup, 32 a wave, for prompts and long
+// drafts.  A block's codes are turned into fp16 once for all four waves, on
+// their way into LDS (exact: |code| <= 127); the sums stay in the fp32
+// accumulators of the fp16 matrix cores, so the vector units are left with
+// about eight operations per score instead of sixteen.
+//   S^T = K Q^T   32 tokens x 32 columns x 16 dims; q divided by the power of
+//                 two below its row's largest value, exact to 2^-25 of that.
+//   weights       2^(9 + x - m + log2(s_V / ref)) in fp16: the values' scale
+//                 rides in the exponent, relative to a power of two at least
+//                 as large as every scale so far, and leaves the sum of
+//                 weights again with one product a block.  m, the running
+//                 maximum, may lag by up to 6, so weights stay below 2^15
+//                 and tails keep their digits down to 2^-33 of the largest.
+//   O^T = V^T P^T the lane's weights are the B operand as they stand; V lies
+//                 in LDS in their order.
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kF16Up = 9.0f, kF16Lag = 6.0f;
+
+__device__ __forceinline__ f32x16 mfma_f16(u32x4 a, u32x4 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+// four codes to fp16: 1024 + (code + 128) as bits, minus 1152
+__device__ __forceinline__ u32x2 codes_f16(uint32_t x)
+{
+    const uint32_t u = x ^ 0x80808080u;
+    const f16x2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
+    u32x2 r;
+    r[0] = __builtin_bit_cast(
+        uint32_t, (f16x2)(__builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - off));
+    r[1] = __builtin_bit_cast(
+        uint32_t, (f16x2)(__builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - off));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b)
+{
+    const f16x2 h = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, h);
+}
+
+template <int D>
+__device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch& b, const AttArgs& a,
+                                                const AttTile& tile, int h, int begin, int end, bool whole,
+                                                uint32_t slot)
+{
+    constexpr int S = D / 64, ST = D / 16, DT = D / 32, COLS = 32 * kAttWaves;
+    constexpr int KC = D / 64;                        // K chunks of 16 bytes per thread
+    __shared__ u32x4 kbuf[2][kKvBlock * D / 8], vbuf[2][kKvBlock * D / 8];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+    const int half = lane >> 5;
+
+    // this lane's column
+    const int col = 32 * wave + (lane & 31);
+    const bool live = col < tile.cols;
+    const int cc = tile.col0 + (live ? col : 0), j = cc / a.G;
+    const uint16_t* row = a.q + (int64_t)(tile.s.t0 + j) * a.q_stride + (int64_t)(h * a.G + cc - j * a.G) * D;
+    const int pos = tile.s.p0 + j;
+    const int first = live ? att_first(pos, a.window) : 0;
+    const int last = live ? att_last(pos, att_limit(b)) : INT32_MAX;
+    u32x4 q[ST];
+    uint32_t qtop = 0;
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+        q[s] = *(const u32x4*)(row + 16 * s + 8 * half);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t x0 = (q[s][e] << 16) & 0x7FFF0000u, x1 = q[s][e] & 0x7FFF0000u;
+            qtop = x0 > qtop ? x0 : qtop;
+            qtop = x1 > qtop ? x1 : qtop;
+        }
+    }
+    const uint32_t other = (uint32_t)__shfl_xor((int)qtop, 32);
+    qtop = other > qtop ? other : qtop;
+    const bool scored = live && qtop >= 0x0D800000u && qtop < 0x7F800000u;    // 2^-100 <= max |q| < inf
+    // the power of two below max |q| and its inverse; the sign of the scale goes into q
+    const float size = __builtin_bit_cast(float, qtop >= 0x7F800000u ? qtop : qtop & 0x7F800000u);
+    const float inv =
+        scored ? copysignf(fmaxf(__builtin_bit_cast(float, 0x7F000000u - (qtop & 0x7F800000u)), 0x1p-127f), a.scale)
+               : 0.0f;
+    const float rowf = size * (fabsf(a.scale) * kLog2e);
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t w = q[s][e];
+            q[s][e] = scored ? pack_f16(__builtin_bit_cast(float, w << 16) * inv,
+                                        __builtin_bit_cast(float, w & 0xFFFF0000u) * inv)
+                             : 0u;
+        }
+
+    // this thread's part in filling LDS
+    int kat[KC];
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+        const int id = tid + 256 * k, r = id & 15, g = (id >> 4) & 3, s = (id >> 6) % S, t = (id >> 6) / S;
+        kat[k] = ((t >> 1) * ST + s * 4 + g) * 64 + (t & 1) * 16 + r;
+    }
+    const bool fills_v = tid < 2 * D;
+    const int vd = (tid >> 5) * 16 + (tid & 15), vh = (tid >> 4) & 1;
+    const int vfrom = fills_v ? ((tid >> 5) * 4 + vh) * 16 + (tid & 15) : 0;      // chunk of group vh; vh + 2 is 32 on
+    const int vat = (vd >> 5) * 256 + vh * 32 + (vd & 31);
+
+    float m = -INFINITY, l = 0.0f, ref = 0.0f;
+    f32x16 acc[DT];
+#pragma unroll
+    for (int u = 0; u < DT; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[u][e] = 0.0f;
+
+    for (int seg = begin; seg < end; seg += 64) {
+        const int count = end - seg < 64 ? end - seg : 64;
+        int mine = -1;
+        float2 sc = make_float2(0.0f, 0.0f);
+        if (lane < count) {
+            mine = kv_block(b, c, tile.s.i, tile.b0 + seg + lane);
+            if (mine >= 0) sc = *(const float2*)(c.scales + ((int64_t)mine * c.heads + h) * 2);
+        }
+        uint64_t todo = __ballot(mine >= 0);
+        u32x4 kraw[KC], vraw[2];
+        const auto fetch = [&](int i) {
+            const int64_t phys = __builtin_amdgcn_readlane(mine, i);
+            const int8_t* p = c.codes + (phys * c.heads + h) * 2 * (kKvBlock * D);
+#pragma unroll
+            for (int k = 0; k < KC; ++k) kraw[k] = *(const u32x4*)(p + (tid + 256 * k) * 16);
+            vraw[0] = *(const u32x4*)(p + kKvBlock * D + vfrom * 16);
+            vraw[1] = *(const u32x4*)(p + kKvBlock * D + vfrom * 16 + 512);
+        };
+        const auto fill = [&](int buf) {
+#pragma unroll
+            for (int k = 0; k < KC; ++k) {
+                const u32x2 x0 = codes_f16(kraw[k][0]), x1 = codes_f16(kraw[k][1]);
+                const u32x2 x2 = codes_f16(kraw[k][2]), x3 = codes_f16(kraw[k][3]);
+                kbuf[buf][kat[k]] = u32x4{x0[0], x0[1], x1[0], x1[1]};
+                kbuf[buf][kat[k] + 32] = u32x4{x2[0], x2[1], x3[0], x3[1]};
+            }
+            if (fills_v) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const u32x2 x0 = codes_f16(vraw[0][t]), x1 = codes_f16(vraw[1][t]);
+                    vbuf[buf][vat + 64 * t] = u32x4{x0[0], x0[1], x1[0], x1[1]};
+                }
+            }
+        };
+        if (todo) {
+            fetch(__builtin_ctzll(todo));
+            fill(0);
+        }
+        int buf = 0;
+        while (todo) {
+            const int i = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            const float sk = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sc.x), i));
+            const float sv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sc.y), i));
+            fetch(todo ? __builtin_ctzll(todo) : i);
+            __syncthreads();         // this buffer is full, the other one no longer read
+            const int at = (tile.b0 + seg + i) * kKvBlock;
+
+            f32x16 x[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[t][e] = 0.0f;
+#pragma unroll
+                for (int s = 0; s < ST; ++s) x[t] = mfma_f16(kbuf[buf][(t * ST + s) * 64 + lane], q[s], x[t]);
+            }
+            // token of x[t][e]: at + 32 t + 8 (e / 4) + 4 half + e % 4
+            const bool sees = first <= at + 63 && last >= at;
+            if (__any(first > at || last < at + 63)) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int p = at + 32 * t + 8 * (e >> 2) + 4 * half + (e & 3);
+                        x[t][e] = p >= first && p <= last ? x[t][e] : -INFINITY;
+                    }
+            }
+            float top = fmaxf(x[0][0], x[1][0]);
+#pragma unroll
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(x[0][e], x[1][e]));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // never 0, or a masked -inf would become a NaN on its way; 1e-30 of
+            // a score (below 2^23) is nothing
+            const float f = rowf * sk < 1e-30f ? 1e-30f : rowf * sk;
+            top *= f;
+            // the scale of the values relative to ref, and what leaves the sum
+            // of weights again; 2^-60 stands for less than that, and for 0
+            float shrink = 1.0f;
+            if (sv > ref && sv < INFINITY) {
+                const float up = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, sv) & 0x7F800000u) + 0x00800000u);
+                shrink = ref == 0.0f ? 1.0f : ref / up;
+                ref = up;
+            }
+            const float ratio = ref == 0.0f ? 0x1p-60f : fmaxf(sv / ref, 0x1p-60f);
+            const float lr = sv < INFINITY ? __log2f(ratio) : NAN, back = exp2_fast(-lr);
+            const bool grow = sees && top > m + kF16Lag;  // from -inf: any score
+            if (__any(grow) || shrink != 1.0f) {
+                const float keep = grow ? exp2_fast(m - top) : 1.0f;
+                m = grow ? top : m;
+                l *= keep;
+#pragma unroll
+                for (int u = 0; u < DT; ++u)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[u][e] *= keep * shrink;
+            }
+            // a row that sees nothing here is spared a scale that is not finite
+            const float base = sees ? kF16Up + lr - (m == -INFINITY ? 0.0f : m) : 0.0f, fs = sees ? f : 1.0f;
+            float sum = 0.0f;
+            u32x4 w[4];              // the B operands of 16 tokens each
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float w0 = exp2_fast(fmaf(x[t][e], fs, base)), w1 = exp2_fast(fmaf(x[t][e + 1], fs, base));
+                    sum += w0;
+                    sum += w1;
+                    w[2 * t + (e >> 3)][(e >> 1) & 3] = pack_f16(w0, w1);
+                }
+            l += sees ? sum * back : 0.0f;
+#pragma unroll
+            for (int u = 0; u < DT; ++u)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) acc[u] = mfma_f16(vbuf[buf][(u * 4 + t) * 64 + lane], w[t], acc[u]);
+            buf ^= 1;
+            fill(buf);
+        }
+        __syncthreads();             // before the next blocks, or the next unit, use LDS
+    }
+    l += __shfl_xor(l, 32);
+    if (!live) return;
+    const float r = whole ? (l == 0.0f ? 0.0f : ref / l) : ref;
+    typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+    uint16_t* dst = a.out + ((int64_t)(tile.s.t0 + j) * c.heads * a.G + h * a.G + cc - j * a.G) * D + 4 * half;
+    const uint32_t place = slot * COLS + col;
+    float* part = a.part + (int64_t)place * D + 4 * half;
+    if (!whole && half == 0) a.stat[place] = make_float2(m, l);
+#pragma unroll
+    for (int u = 0; u < DT; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            f32x4 o;
+            u16x4 y;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                o[k] = l == 0.0f ? 0.0f : acc[u][e + k] * r;
+                y[k] = f32_to_bf16(o[k]);
+            }
+            if (whole) *(u16x4*)(dst + 32 * u + 2 * e) = y;
+            else *(f32x4*)(part + 32 * u + 2 * e) = o;
+        }
+}
+
 template <int D, int CT>
-__global__ __launch_bounds__(64 * kAttWaves, CT == 1 ? 3 : 2) void kv_attend_i8_kernel(KvCache c, KvBatch b,
-                                                                                       AttArgs a)
+__global__ __launch_bounds__(64 * kAttWaves, CT == 1 ? 3 : 2) void kv_attend_kernel(KvCache c, KvBatch b, AttArgs a)
 {
     constexpr int COLS = 16 * CT;
     const int lane = threadIdx.x & 63;
@@ -445,11 +701,13 @@ __global__ __launch_bounds__(64 * kAttWaves, CT == 1 ? 3 : 2) void kv_attend_i8_
         bool whole = true, any;
         uint32_t slot = 0;
         if (a.groups == 0) {
-            const uint32_t item = blockIdx.x / c.heads;
+            // heads fastest (a head's workgroups meet in one XCD's L2 where heads are a
+            // multiple of 8), the last tiles, with the most to see, first
+            const uint32_t item = (gridDim.x - 1 - blockIdx.x) / c.heads;
             int64_t local;
             any = kv_find(b, item, a.G, COLS, 1, tile.s, local);
             number = any ? uni((int)local) : 0;
-            h = blockIdx.x - item * c.heads;
+            h = gridDim.x - 1 - blockIdx.x - item * c.heads;
             x = x1;
         } else {
             while (x - at >= r.tiles * c.heads * r.len) {     // ends: x < total
@@ -471,7 +729,10 @@ __global__ __launch_bounds__(64 * kAttWaves, CT == 1 ? 3 : 2) void kv_attend_i8_
         if (any && att_tile<COLS>(b, number, a.G, a.window, tile)) {
             att_uniform(tile);
             end = end < tile.nblk ? end : tile.nblk;
-            if (begin < end || begin == 0) attend_blocks<D, CT>(c, b, a, tile, h, begin, end, whole, slot);
+            if (begin < end || begin == 0) {
+                if constexpr (CT <= 2) attend_blocks<D, CT>(c, b, a, tile, h, begin, end, whole, slot);
+                else attend_tile_f16<D>(c, b, a, tile, h, begin, end, whole, slot);
+            }
         }
         if (x >= x1) break;
         __syncthreads();                                      // LDS is used again
@@ -567,19 +828,20 @@ struct AttPlan {
     int64_t part_floats, stats, starts;
 };
 
-constexpr int64_t kAttGroups = 768;          // three workgroups a CU: what registers allow at once
+constexpr int64_t kAttGroups = 768;          // three workgroups a CU (two with more columns): what registers allow
 constexpr int64_t kAttWholeBlocks = 16;      // up to here a unit is not split
 
 static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
 {
     AttPlan p{};
     const int64_t G = Hq / heads;
-    p.cols = T * G <= 16 * nseq ? 16 : 32;
+    p.cols = T * G <= 16 * nseq ? 16 : T * G <= 32 * nseq ? 32 : 128;
     p.items = T * G / p.cols + nseq;
     const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock, units = p.items * heads;
-    if (blocks <= kAttWholeBlocks || units >= 2 * kAttGroups) return p;
+    const int64_t most = p.cols == 16 ? kAttGroups : kAttGroups / 3 * 2;
+    if (blocks <= kAttWholeBlocks || units >= 2 * most) return p;
     const int64_t turns = (blocks + kAttWaves - 1) / kAttWaves;
-    p.groups = (int)(units > kAttGroups / turns ? kAttGroups : units * turns);
+    p.groups = (int)(units > most / turns ? most : units * turns);
     p.stats = p.groups * 2 * p.cols;
     p.part_floats = p.stats * D;
     p.starts = nseq + 1;
@@ -593,11 +855,11 @@ int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t 
 }
 
 template <int D, int CT>
-static hipError_t attend_i8(const KvCache& c, const KvBatch& b, const AttArgs& a, const AttPlan& p,
+static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, const AttPlan& p,
                             hipStream_t stream)
 {
     const int64_t grid = a.groups ? a.groups : p.items * c.heads;
-    kv_attend_i8_kernel<D, CT><<<(unsigned)grid, 64 * kAttWaves, 0, stream>>>(c, b, a);
+    kv_attend_kernel<D, CT><<<(unsigned)grid, 64 * kAttWaves, 0, stream>>>(c, b, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.groups == 0) return e;
     const int64_t rows = (int64_t)b.T * c.heads * a.G;
@@ -626,8 +888,13 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const
     // the line is counted in 32 bits; a batch that could pass that has units enough
     const int64_t line = p.items * c.heads * ((int64_t)b.table_width + kAttWaves);
     a.groups = line < (1ll << 31) ? p.groups : 0;
-    if (D == 128) return p.cols == 16 ? attend_i8<128, 1>(c, b, a, p, stream) : attend_i8<128, 2>(c, b, a, p, stream);
-    return p.cols == 16 ? attend_i8<64, 1>(c, b, a, p, stream) : attend_i8<64, 2>(c, b, a, p, stream);
+    if (D == 128)
+        return p.cols == 16   ? attend<128, 1>(c, b, a, p, stream)
+               : p.cols == 32 ? attend<128, 2>(c, b, a, p, stream)
+                              : attend<128, 8>(c, b, a, p, stream);
+    return p.cols == 16   ? attend<64, 1>(c, b, a, p, stream)
+           : p.cols == 32 ? attend<64, 2>(c, b, a, p, stream)
+                          : attend<64, 8>(c, b, a, p, stream);
 }
 
 }  // namespace tern

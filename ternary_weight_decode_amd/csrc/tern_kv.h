@@ -65,21 +65,25 @@ __device__ __forceinline__ bool kv_find(const KvBatch& b, int64_t item, int mul,
                                         int64_t& local)
 {
     const int lane = threadIdx.x & 63;
-    int owners = 0;
+    int owners = 0, cu0 = 0, cu1 = 0, len = 0;
     for (int c = 0; c < b.nseq; c += 64) {
-        const int i = c + lane;
-        const bool in = i < b.nseq && (int64_t)b.cu[i] * mul / div + (int64_t)i * extra <= item;
+        const int i = c + lane < b.nseq ? c + lane : b.nseq - 1;
+        const int r0 = b.cu[i], r1 = b.cu[i + 1], r2 = kv_length(b, i);
+        const bool in = c + lane < b.nseq && (int64_t)r0 * mul / div + (int64_t)i * extra <= item;
         const int got = __popcll(__ballot(in));
+        if (got == 0) break;
         owners += got;
+        cu0 = __builtin_amdgcn_readlane(r0, got - 1);
+        cu1 = __builtin_amdgcn_readlane(r1, got - 1);
+        len = __builtin_amdgcn_readlane(r2, got - 1);
         if (got < 64) break;
     }
     if (owners == 0) return false;
     s.i = owners - 1;
-    s.t0 = b.cu[s.i];
-    const int t1 = b.cu[s.i + 1];
-    s.n = t1 - s.t0;
-    if (s.t0 < 0 || t1 > b.T || s.n <= 0) return false;
-    s.p0 = kv_length(b, s.i) - s.n;
+    s.t0 = cu0;
+    s.n = cu1 - cu0;
+    if (s.t0 < 0 || cu1 > b.T || s.n <= 0) return false;
+    s.p0 = len - s.n;
     local = item - ((int64_t)s.t0 * mul / div + (int64_t)s.i * extra);
     return local >= 0;
 }

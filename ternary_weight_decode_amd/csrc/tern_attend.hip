@@ -413,6 +413,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kF16Up = 9.0f, kF16Lag = 6.0f;
+constexpr int kAhead = 4;                    // LDS operands under way to the matrix cores
 
 __device__ __forceinline__ f32x16 mfma_f16(u32x4 a, u32x4 b, f32x16 c)
 {
@@ -556,14 +557,28 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
             __syncthreads();         // this buffer is full, the other one no longer read
             const int at = (tile.b0 + seg + i) * kKvBlock;
 
+            // Four operands ahead of the matrix cores (alone, the compiler reads
+            // one at a time and waits for it); the two token tiles in turn, so
+            // that neighbouring products do not wait for each other.
             f32x16 x[2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int e = 0; e < 16; ++e) x[0][e] = x[1][e] = 0.0f;
+            u32x4 ahead[kAhead];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[t][e] = 0.0f;
+            for (int k = 0; k < kAhead; ++k) ahead[k] = kbuf[buf][((k & 1) * ST + (k >> 1)) * 64 + lane];
 #pragma unroll
-                for (int s = 0; s < ST; ++s) x[t] = mfma_f16(kbuf[buf][(t * ST + s) * 64 + lane], q[s], x[t]);
+            for (int k = 0; k < 2 * ST; ++k) {
+                x[k & 1] = mfma_f16(ahead[k % kAhead], q[k >> 1], x[k & 1]);
+                const int o = k + kAhead;
+                if (o < 2 * ST) ahead[k % kAhead] = kbuf[buf][((o & 1) * ST + (o >> 1)) * 64 + lane];
             }
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int k = 0; k < 2 * ST - kAhead; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
             // token of x[t][e]: at + 32 t + 8 (e / 4) + 4 half + e % 4
             const bool sees = first <= at + 63 && last >= at;
             if (__any(first > at || last < at + 63)) {
@@ -618,9 +633,20 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
                 }
             l += sees ? sum * back : 0.0f;
 #pragma unroll
-            for (int u = 0; u < DT; ++u)
+            for (int k = 0; k < kAhead; ++k) ahead[k] = vbuf[buf][((k % DT) * 4 + k / DT) * 64 + lane];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) acc[u] = mfma_f16(vbuf[buf][(u * 4 + t) * 64 + lane], w[t], acc[u]);
+            for (int k = 0; k < 4 * DT; ++k) {
+                acc[k % DT] = mfma_f16(ahead[k % kAhead], w[k / DT], acc[k % DT]);
+                const int o = k + kAhead;
+                if (o < 4 * DT) ahead[k % kAhead] = vbuf[buf][((o % DT) * 4 + o / DT) * 64 + lane];
+            }
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 1);
+#pragma unroll
+            for (int k = 0; k < 4 * DT - kAhead; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 1);
             buf ^= 1;
             fill(buf);
         }
@@ -628,26 +654,35 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
     }
     l += __shfl_xor(l, 32);
     if (!live) return;
-    const float r = whole ? (l == 0.0f ? 0.0f : ref / l) : ref;
-    typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-    uint16_t* dst = a.out + ((int64_t)(tile.s.t0 + j) * c.heads * a.G + h * a.G + cc - j * a.G) * D + 4 * half;
-    const uint32_t place = slot * COLS + col;
-    float* part = a.part + (int64_t)place * D + 4 * half;
-    if (!whole && half == 0) a.stat[place] = make_float2(m, l);
+    const bool none = l == 0.0f;
+    if (whole) {
+        typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+        const float r = none ? 0.0f : ref / l;
+        uint16_t* dst =
+            a.out + ((int64_t)(tile.s.t0 + j) * c.heads * a.G + h * a.G + cc - j * a.G) * D + 4 * half;
 #pragma unroll
-    for (int u = 0; u < DT; ++u)
+        for (int u = 0; u < DT; ++u)
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            f32x4 o;
-            u16x4 y;
+            for (int e = 0; e < 16; e += 4) {
+                u16x4 y;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                o[k] = l == 0.0f ? 0.0f : acc[u][e + k] * r;
-                y[k] = f32_to_bf16(o[k]);
+                for (int k = 0; k < 4; ++k) y[k] = none ? (uint16_t)0 : f32_to_bf16(acc[u][e + k] * r);
+                *(u16x4*)(dst + 32 * u + 2 * e) = y;
             }
-            if (whole) *(u16x4*)(dst + 32 * u + 2 * e) = y;
-            else *(f32x4*)(part + 32 * u + 2 * e) = o;
-        }
+    } else {
+        const uint32_t place = slot * COLS + col;
+        float* part = a.part + (int64_t)place * D + 4 * half;
+        if (half == 0) a.stat[place] = make_float2(m, l);
+#pragma unroll
+        for (int u = 0; u < DT; ++u)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                f32x4 o;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = none ? 0.0f : acc[u][e + k] * ref;
+                *(f32x4*)(part + 32 * u + 2 * e) = o;
+            }
+    }
 }
 
 template <int D, int CT>
@@ -863,7 +898,7 @@ static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, c
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.groups == 0) return e;
     const int64_t rows = (int64_t)b.T * c.heads * a.G;
-    if ((int64_t)b.nseq * c.heads * 8 >= a.groups)      // about eight parts a row or fewer
+    if ((int64_t)b.nseq * c.heads * 8 >= a.groups || rows >= 2048)      // about eight parts a row or fewer, or rows enough
         kv_attend_join_kernel<D, 16 * CT, 1><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(c, b, a);
     else
         kv_attend_join_kernel<D, 16 * CT, 12><<<(unsigned)rows, 768, 0, stream>>>(c, b, a);

@@ -393,26 +393,35 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
     }
 }
 
-// kv_attend_f16: 128 columns per workgroup, 32 a wave, for prompts and long
-// drafts.  A block's codes are turned into fp16 once for all four waves, on
-// their way into LDS (exact: |code| <= 127); the sums stay in the fp32
-// accumulators of the fp16 matrix cores, so the vector units are left with
-// about eight operations per score instead of sixteen.
+// The fp16 tile: 256 columns per workgroup, 32 for each of eight waves, for
+// prompts.  A block's codes are turned into fp16 once for all waves, on their
+// way into LDS (exact: |code| <= 127); the sums stay in the fp32 accumulators
+// of the fp16 matrix cores, so the vector units are left with about eight
+// operations per score instead of sixteen.
 //   S^T = K Q^T   32 tokens x 32 columns x 16 dims; q divided by the power of
 //                 two below its row's largest value, exact to 2^-25 of that.
 //   weights       2^(9 + x - m + log2(s_V / ref)) in fp16: the values' scale
 //                 rides in the exponent, relative to a power of two at least
 //                 as large as every scale so far, and leaves the sum of
-//                 weights again with one product a block.  m, the running
-//                 maximum, may lag by up to 6, so weights stay below 2^15
-//                 and tails keep their digits down to 2^-33 of the largest.
+//                 weights again with one product a block.  m, a maximum of
+//                 the scores so far, moves only when a lane's weights sum to
+//                 more than 2^15; tails keep their digits down to 2^-33 of
+//                 the largest.
 //   O^T = V^T P^T the lane's weights are the B operand as they stand; V lies
 //                 in LDS in their order.
+// The matrix cores and the vector units are kept busy at once by the two waves
+// of each SIMD taking turns: while waves 0-3 run one block's products
+// (P V of the block before, then K Q), waves 4-7 run their softmax, then the
+// other way round; a barrier ends every half turn.  Waves 0-3 fill LDS with V,
+// waves 4-7 with K, in their vector half.  In half turns, block j's K is
+// written in 2j - 2 and read in 2j and 2j + 1, its V written in 2j + 1 and read
+// in 2j + 2 and 2j + 3: two buffers of each are enough.
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr float kF16Up = 9.0f, kF16Lag = 6.0f;
+constexpr float kF16Up = 9.0f, kF16Most = 32768.0f;
+constexpr int kTileWaves = 8;
 constexpr int kAhead = 4;                    // LDS operands under way to the matrix cores
 
 __device__ __forceinline__ f32x16 mfma_f16(u32x4 a, u32x4 b, f32x16 c)
@@ -440,25 +449,43 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b)
     return __builtin_bit_cast(uint32_t, h);
 }
 
+__device__ __forceinline__ void half_turn()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 template <int D>
 __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch& b, const AttArgs& a,
                                                 const AttTile& tile, int h, int begin, int end, bool whole,
                                                 uint32_t slot)
 {
-    constexpr int S = D / 64, ST = D / 16, DT = D / 32, COLS = 32 * kAttWaves;
-    constexpr int KC = D / 64;                        // K chunks of 16 bytes per thread
+    constexpr int S = D / 64, ST = D / 16, DT = D / 32, COLS = 32 * kTileWaves;
+    constexpr int CH = D / 64;                        // chunks of 16 bytes per thread: of K, or of V
     __shared__ u32x4 kbuf[2][kKvBlock * D / 8], vbuf[2][kKvBlock * D / 8];
-    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int half = lane >> 5;
+    const bool second = wave >= kTileWaves / 2;      // waves i and i + 4 share a SIMD
+    const int tid = threadIdx.x & 255;
 
     // this lane's column
     const int col = 32 * wave + (lane & 31);
+    const bool works = 32 * wave < tile.cols;         // a wave without columns only fills LDS
     const bool live = col < tile.cols;
     const int cc = tile.col0 + (live ? col : 0), j = cc / a.G;
     const uint16_t* row = a.q + (int64_t)(tile.s.t0 + j) * a.q_stride + (int64_t)(h * a.G + cc - j * a.G) * D;
     const int pos = tile.s.p0 + j;
     const int first = live ? att_first(pos, a.window) : 0;
     const int last = live ? att_last(pos, att_limit(b)) : INT32_MAX;
+    int all_first = first, all_last = last;           // keys that every column sees
+    for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_xor(all_first, off), y = __shfl_xor(all_last, off);
+        all_first = x > all_first ? x : all_first;
+        all_last = y < all_last ? y : all_last;
+    }
+    all_first = uni(all_first);
+    all_last = uni(all_last);
     u32x4 q[ST];
     uint32_t qtop = 0;
 #pragma unroll
@@ -485,22 +512,26 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t w = q[s][e];
-            q[s][e] = scored ? pack_f16(__builtin_bit_cast(float, w << 16) * inv,
-                                        __builtin_bit_cast(float, w & 0xFFFF0000u) * inv)
-                             : 0u;
+            const uint32_t p = pack_f16(__builtin_bit_cast(float, w << 16) * inv,
+                                        __builtin_bit_cast(float, w & 0xFFFF0000u) * inv);
+            q[s][e] = scored ? p : 0u;
         }
 
-    // this thread's part in filling LDS
-    int kat[KC];
+    // this thread's chunks of a block's K (waves 4-7) or V (waves 0-3), and their places in LDS
+    int from[2], to[2];
 #pragma unroll
-    for (int k = 0; k < KC; ++k) {
+    for (int k = 0; k < CH; ++k) {
         const int id = tid + 256 * k, r = id & 15, g = (id >> 4) & 3, s = (id >> 6) % S, t = (id >> 6) / S;
-        kat[k] = ((t >> 1) * ST + s * 4 + g) * 64 + (t & 1) * 16 + r;
+        from[k] = id * 16;
+        to[k] = ((t >> 1) * ST + s * 4 + g) * 64 + (t & 1) * 16 + r;
     }
     const bool fills_v = tid < 2 * D;
-    const int vd = (tid >> 5) * 16 + (tid & 15), vh = (tid >> 4) & 1;
-    const int vfrom = fills_v ? ((tid >> 5) * 4 + vh) * 16 + (tid & 15) : 0;      // chunk of group vh; vh + 2 is 32 on
-    const int vat = (vd >> 5) * 256 + vh * 32 + (vd & 31);
+    if (!second) {
+        const int vd = (tid >> 5) * 16 + (tid & 15), vh = (tid >> 4) & 1;
+        from[0] = kKvBlock * D + (fills_v ? ((tid >> 5) * 4 + vh) * 16 + (tid & 15) : 0) * 16;
+        from[1] = from[0] + 512;                      // groups vh and vh + 2 of one dim
+        to[0] = (vd >> 5) * 256 + vh * 32 + (vd & 31);
+    }
 
     float m = -INFINITY, l = 0.0f, ref = 0.0f;
     f32x16 acc[DT];
@@ -510,6 +541,7 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
         for (int e = 0; e < 16; ++e) acc[u][e] = 0.0f;
 
     for (int seg = begin; seg < end; seg += 64) {
+        // lane i looks up block seg + i; the blocks that are there move to the front
         const int count = end - seg < 64 ? end - seg : 64;
         int mine = -1;
         float2 sc = make_float2(0.0f, 0.0f);
@@ -517,53 +549,66 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
             mine = kv_block(b, c, tile.s.i, tile.b0 + seg + lane);
             if (mine >= 0) sc = *(const float2*)(c.scales + ((int64_t)mine * c.heads + h) * 2);
         }
-        uint64_t todo = __ballot(mine >= 0);
-        u32x4 kraw[KC], vraw[2];
-        const auto fetch = [&](int i) {
-            const int64_t phys = __builtin_amdgcn_readlane(mine, i);
-            const int8_t* p = c.codes + (phys * c.heads + h) * 2 * (kKvBlock * D);
+        const uint64_t there = __ballot(mine >= 0), below = (1ull << lane) - 1;
+        const int blocks = __popcll(there);
+        if (blocks == 0) continue;
+        const int dest = (mine >= 0 ? __popcll(there & below) : blocks + __popcll(~there & below)) * 4;
+        mine = __builtin_amdgcn_ds_permute(dest, mine);
+        const int number = __builtin_amdgcn_ds_permute(dest, tile.b0 + seg + lane);
+        const float sk = __builtin_bit_cast(float, __builtin_amdgcn_ds_permute(dest, __builtin_bit_cast(int, sc.x)));
+        const float sv = __builtin_bit_cast(float, __builtin_amdgcn_ds_permute(dest, __builtin_bit_cast(int, sc.y)));
+        // the values' scales relative to ref, and what takes them out of the
+        // sum of weights; 2^-60 stands for less than that, and for 0
+        float big = lane < blocks && sv < INFINITY ? sv : 0.0f;
+        for (int off = 1; off < 64; off <<= 1) big = fmaxf(big, __shfl_xor(big, off));
+        if (big > ref) {
+            const float up =
+                __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, big) & 0x7F800000u) + 0x00800000u);
+            const float shrink = ref / up;            // 0 at first: nothing is summed yet
 #pragma unroll
-            for (int k = 0; k < KC; ++k) kraw[k] = *(const u32x4*)(p + (tid + 256 * k) * 16);
-            vraw[0] = *(const u32x4*)(p + kKvBlock * D + vfrom * 16);
-            vraw[1] = *(const u32x4*)(p + kKvBlock * D + vfrom * 16 + 512);
+            for (int u = 0; u < DT; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[u][e] *= shrink;
+            ref = up;
+        }
+        const float ratio = ref == 0.0f ? 0x1p-60f : fmaxf(sv / ref, 0x1p-60f);
+        const float lr = sv < INFINITY ? __log2f(ratio) : NAN, back = exp2_fast(-lr);
+        const auto pick = [](float v, int i) {
+            return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), i));
+        };
+
+        u32x4 raw[2];
+        const auto fetch = [&](int i) {
+            const int64_t phys = __builtin_amdgcn_readlane(mine, i < blocks ? i : blocks - 1);
+            const int8_t* p = c.codes + (phys * c.heads + h) * 2 * (kKvBlock * D);
+            raw[0] = *(const u32x4*)(p + from[0]);
+            if (CH == 2 || !second) raw[1] = *(const u32x4*)(p + from[1]);
         };
         const auto fill = [&](int buf) {
+            if (second) {
 #pragma unroll
-            for (int k = 0; k < KC; ++k) {
-                const u32x2 x0 = codes_f16(kraw[k][0]), x1 = codes_f16(kraw[k][1]);
-                const u32x2 x2 = codes_f16(kraw[k][2]), x3 = codes_f16(kraw[k][3]);
-                kbuf[buf][kat[k]] = u32x4{x0[0], x0[1], x1[0], x1[1]};
-                kbuf[buf][kat[k] + 32] = u32x4{x2[0], x2[1], x3[0], x3[1]};
-            }
-            if (fills_v) {
+                for (int k = 0; k < CH; ++k) {
+                    const u32x2 x0 = codes_f16(raw[k][0]), x1 = codes_f16(raw[k][1]);
+                    const u32x2 x2 = codes_f16(raw[k][2]), x3 = codes_f16(raw[k][3]);
+                    kbuf[buf][to[k]] = u32x4{x0[0], x0[1], x1[0], x1[1]};
+                    kbuf[buf][to[k] + 32] = u32x4{x2[0], x2[1], x3[0], x3[1]};
+                }
+            } else if (fills_v) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const u32x2 x0 = codes_f16(vraw[0][t]), x1 = codes_f16(vraw[1][t]);
-                    vbuf[buf][vat + 64 * t] = u32x4{x0[0], x0[1], x1[0], x1[1]};
+                    const u32x2 x0 = codes_f16(raw[0][t]), x1 = codes_f16(raw[1][t]);
+                    vbuf[buf][to[0] + 64 * t] = u32x4{x0[0], x0[1], x1[0], x1[1]};
                 }
             }
         };
-        if (todo) {
-            fetch(__builtin_ctzll(todo));
-            fill(0);
-        }
-        int buf = 0;
-        while (todo) {
-            const int i = __builtin_ctzll(todo);
-            todo &= todo - 1;
-            const float sk = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sc.x), i));
-            const float sv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sc.y), i));
-            fetch(todo ? __builtin_ctzll(todo) : i);
-            __syncthreads();         // this buffer is full, the other one no longer read
-            const int at = (tile.b0 + seg + i) * kKvBlock;
-
-            // Four operands ahead of the matrix cores (alone, the compiler reads
-            // one at a time and waits for it); the two token tiles in turn, so
-            // that neighbouring products do not wait for each other.
-            f32x16 x[2];
+        f32x16 x[2];
+        u32x4 w[4];                  // the weights: B operands of 16 tokens each
+        u32x4 ahead[kAhead];
+        // Four operands ahead of the matrix cores (alone, the compiler reads one
+        // at a time and waits for it), neighbouring products independent.
+        const auto scores = [&](int buf) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[0][e] = x[1][e] = 0.0f;
-            u32x4 ahead[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) ahead[k] = kbuf[buf][((k & 1) * ST + (k >> 1)) * 64 + lane];
 #pragma unroll
@@ -579,59 +624,8 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
             __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
-            // token of x[t][e]: at + 32 t + 8 (e / 4) + 4 half + e % 4
-            const bool sees = first <= at + 63 && last >= at;
-            if (__any(first > at || last < at + 63)) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int p = at + 32 * t + 8 * (e >> 2) + 4 * half + (e & 3);
-                        x[t][e] = p >= first && p <= last ? x[t][e] : -INFINITY;
-                    }
-            }
-            float top = fmaxf(x[0][0], x[1][0]);
-#pragma unroll
-            for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(x[0][e], x[1][e]));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            // never 0, or a masked -inf would become a NaN on its way; 1e-30 of
-            // a score (below 2^23) is nothing
-            const float f = rowf * sk < 1e-30f ? 1e-30f : rowf * sk;
-            top *= f;
-            // the scale of the values relative to ref, and what leaves the sum
-            // of weights again; 2^-60 stands for less than that, and for 0
-            float shrink = 1.0f;
-            if (sv > ref && sv < INFINITY) {
-                const float up = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, sv) & 0x7F800000u) + 0x00800000u);
-                shrink = ref == 0.0f ? 1.0f : ref / up;
-                ref = up;
-            }
-            const float ratio = ref == 0.0f ? 0x1p-60f : fmaxf(sv / ref, 0x1p-60f);
-            const float lr = sv < INFINITY ? __log2f(ratio) : NAN, back = exp2_fast(-lr);
-            const bool grow = sees && top > m + kF16Lag;  // from -inf: any score
-            if (__any(grow) || shrink != 1.0f) {
-                const float keep = grow ? exp2_fast(m - top) : 1.0f;
-                m = grow ? top : m;
-                l *= keep;
-#pragma unroll
-                for (int u = 0; u < DT; ++u)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[u][e] *= keep * shrink;
-            }
-            // a row that sees nothing here is spared a scale that is not finite
-            const float base = sees ? kF16Up + lr - (m == -INFINITY ? 0.0f : m) : 0.0f, fs = sees ? f : 1.0f;
-            float sum = 0.0f;
-            u32x4 w[4];              // the B operands of 16 tokens each
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float w0 = exp2_fast(fmaf(x[t][e], fs, base)), w1 = exp2_fast(fmaf(x[t][e + 1], fs, base));
-                    sum += w0;
-                    sum += w1;
-                    w[2 * t + (e >> 3)][(e >> 1) & 3] = pack_f16(w0, w1);
-                }
-            l += sees ? sum * back : 0.0f;
+        };
+        const auto values = [&](int buf) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) ahead[k] = vbuf[buf][((k % DT) * 4 + k / DT) * 64 + lane];
 #pragma unroll
@@ -647,10 +641,91 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
             }
             __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 1);
-            buf ^= 1;
-            fill(buf);
+        };
+        const auto softmax = [&](int i) {
+            const float f = rowf * pick(sk, i), lri = pick(lr, i);
+            const int at = __builtin_amdgcn_readlane(number, i) * kKvBlock;
+            // exponents against the maximum so far; token of x[t][e]:
+            // at + 32 t + 8 (e / 4) + 4 half + e % 4
+            const float m0 = m == -INFINITY ? 0.0f : m, base = kF16Up + lri - m0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[t][e] = fmaf(x[t][e], f, base);
+            if (all_first > at || all_last < at + 63) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int p = at + 32 * t + 8 * (e >> 2) + 4 * half + (e & 3);
+                        x[t][e] = p >= first && p <= last ? x[t][e] : -INFINITY;
+                    }
+            }
+            float sum;
+            const auto weigh = [&](float by) {
+                float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float w0 = exp2_fast(x[t][e] - by), w1 = exp2_fast(x[t][e + 1] - by);
+                        sum0 += w0;
+                        sum1 += w1;
+                        w[2 * t + (e >> 3)][(e >> 1) & 3] = pack_f16(w0, w1);
+                    }
+                sum = sum0 + sum1;
+            };
+            // The maximum is looked at only when the weights say so: while a
+            // lane's sum stays below 2^15 no weight has left fp16's range.
+            weigh(0.0f);
+            if (__any(sum > kF16Most || m == -INFINITY)) {
+                float top = fmaxf(x[0][0], x[1][0]);
+#pragma unroll
+                for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(x[0][e], x[1][e]));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float over = top - (kF16Up + lri);
+                const bool grow = m == -INFINITY ? over > -INFINITY : over > 0.0f;
+                const float by = grow ? over : 0.0f;
+                const float keep = m == -INFINITY ? 0.0f : exp2_fast(-by);
+                m = grow ? m0 + by : m;
+                l *= keep;
+#pragma unroll
+                for (int u = 0; u < DT; ++u)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[u][e] *= keep;
+                weigh(by);
+            }
+            // a row that sees nothing here is spared a scale that is not finite
+            l += sum == 0.0f ? 0.0f : sum * pick(back, i);
+        };
+
+        if (second) {
+            fetch(0);
+            fill(0);
+            fetch(1);
+        } else {
+            fetch(0);
         }
-        __syncthreads();             // before the next blocks, or the next unit, use LDS
+        half_turn();
+        if (second) {
+            fill(1);
+            fetch(2);
+            half_turn();
+        }
+        for (int i = 0; i < blocks; ++i) {
+            if (works) {
+                if (i > 0) values((i - 1) & 1);
+                scores(i & 1);
+            }
+            half_turn();
+            if (works) softmax(i);
+            fill(i & 1);             // V of block i, or K of block i + 2
+            fetch(second ? i + 3 : i + 1);
+            half_turn();
+        }
+        if (works) values((blocks - 1) & 1);
+        if (!second) half_turn();
+        half_turn();                 // before the next blocks, or the next unit, use LDS
     }
     l += __shfl_xor(l, 32);
     if (!live) return;
@@ -685,8 +760,12 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
     }
 }
 
+// CT 1 and 2: 16 and 32 columns on the int8 path, CT 16: 256 on the fp16 path
+template <int CT>
+constexpr int att_threads() { return CT <= 2 ? 64 * kAttWaves : 64 * kTileWaves; }
+
 template <int D, int CT>
-__global__ __launch_bounds__(64 * kAttWaves, CT == 1 ? 3 : 2) void kv_attend_kernel(KvCache c, KvBatch b, AttArgs a)
+__global__ __launch_bounds__(att_threads<CT>(), CT == 1 ? 3 : 2) void kv_attend_kernel(KvCache c, KvBatch b, AttArgs a)
 {
     constexpr int COLS = 16 * CT;
     const int lane = threadIdx.x & 63;
@@ -870,10 +949,10 @@ static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t
 {
     AttPlan p{};
     const int64_t G = Hq / heads;
-    p.cols = T * G <= 16 * nseq ? 16 : T * G <= 32 * nseq ? 32 : 128;
+    p.cols = T * G <= 16 * nseq ? 16 : T * G <= 32 * nseq ? 32 : 256;
     p.items = T * G / p.cols + nseq;
     const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock, units = p.items * heads;
-    const int64_t most = p.cols == 16 ? kAttGroups : kAttGroups / 3 * 2;
+    const int64_t most = p.cols == 16 ? kAttGroups : p.cols == 32 ? kAttGroups / 3 * 2 : kAttGroups / 3;
     if (blocks <= kAttWholeBlocks || units >= 2 * most) return p;
     const int64_t turns = (blocks + kAttWaves - 1) / kAttWaves;
     p.groups = (int)(units > most / turns ? most : units * turns);
@@ -894,7 +973,7 @@ static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, c
                             hipStream_t stream)
 {
     const int64_t grid = a.groups ? a.groups : p.items * c.heads;
-    kv_attend_kernel<D, CT><<<(unsigned)grid, 64 * kAttWaves, 0, stream>>>(c, b, a);
+    kv_attend_kernel<D, CT><<<(unsigned)grid, att_threads<CT>(), 0, stream>>>(c, b, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.groups == 0) return e;
     const int64_t rows = (int64_t)b.T * c.heads * a.G;
@@ -926,10 +1005,10 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const
     if (D == 128)
         return p.cols == 16   ? attend<128, 1>(c, b, a, p, stream)
                : p.cols == 32 ? attend<128, 2>(c, b, a, p, stream)
-                              : attend<128, 8>(c, b, a, p, stream);
+                              : attend<128, 16>(c, b, a, p, stream);
     return p.cols == 16   ? attend<64, 1>(c, b, a, p, stream)
            : p.cols == 32 ? attend<64, 2>(c, b, a, p, stream)
-                          : attend<64, 8>(c, b, a, p, stream);
+                          : attend<64, 16>(c, b, a, p, stream);
 }
 
 }  // namespace tern

@@ -462,7 +462,6 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
                                                 uint32_t slot)
 {
     constexpr int S = D / 64, ST = D / 16, DT = D / 32, COLS = 32 * kTileWaves;
-    constexpr int CH = D / 64;                        // chunks of 16 bytes per thread: of K, or of V
     __shared__ u32x4 kbuf[2][kKvBlock * D / 8], vbuf[2][kKvBlock * D / 8];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int half = lane >> 5;
@@ -486,11 +485,14 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
     }
     all_first = uni(all_first);
     all_last = uni(all_last);
+    // step 4 s + e, half: dims 64 s + 16 half + 4 e .. + 3 and 32 further on
     u32x4 q[ST];
     uint32_t qtop = 0;
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
-        q[s] = *(const u32x4*)(row + 16 * s + 8 * half);
+        const uint16_t* p = row + 64 * (s >> 2) + 16 * half + 4 * (s & 3);
+        const u32x2 x = *(const u32x2*)p, y = *(const u32x2*)(p + 32);
+        q[s] = u32x4{x[0], x[1], y[0], y[1]};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t x0 = (q[s][e] << 16) & 0x7FFF0000u, x1 = q[s][e] & 0x7FFF0000u;
@@ -517,21 +519,15 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
             q[s][e] = scored ? p : 0u;
         }
 
-    // this thread's chunks of a block's K (waves 4-7) or V (waves 0-3), and their places in LDS
-    int from[2], to[2];
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-        const int id = tid + 256 * k, r = id & 15, g = (id >> 4) & 3, s = (id >> 6) % S, t = (id >> 6) / S;
-        from[k] = id * 16;
-        to[k] = ((t >> 1) * ST + s * 4 + g) * 64 + (t & 1) * 16 + r;
-    }
-    const bool fills_v = tid < 2 * D;
-    if (!second) {
-        const int vd = (tid >> 5) * 16 + (tid & 15), vh = (tid >> 4) & 1;
-        from[0] = kKvBlock * D + (fills_v ? ((tid >> 5) * 4 + vh) * 16 + (tid & 15) : 0) * 16;
-        from[1] = from[0] + 512;                      // groups vh and vh + 2 of one dim
-        to[0] = (vd >> 5) * 256 + vh * 32 + (vd & 31);
-    }
+    // This thread's two chunks of 16 bytes of a block's K (waves 4-7) or V
+    // (waves 0-3), groups g and g + 2 of one token and 64 dims, or of one dim:
+    // their e-th words, side by side, are what lane half g reads in step e.
+    const bool fills = tid < 2 * D;
+    const int item = fills ? tid : 0, fr = item & 15, fg = (item >> 4) & 1, fu = item >> 5;
+    const int from = (second ? 0 : kKvBlock * D) + ((fu * 4 + fg) * 16 + fr) * 16;
+    // K: fu = 16-token tile and 64 dims, V: fu = 16 dims
+    const int step = second ? ((fu / S >> 1) * ST + fu % S * 4) * 64 + (fu / S & 1) * 16 : (fu >> 1) * 256 + (fu & 1) * 16;
+    u32x4* const to = (second ? kbuf[0] : vbuf[0]) + step + fg * 32 + fr;
 
     float m = -INFINITY, l = 0.0f, ref = 0.0f;
     f32x16 acc[DT];
@@ -581,24 +577,14 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
         const auto fetch = [&](int i) {
             const int64_t phys = __builtin_amdgcn_readlane(mine, i < blocks ? i : blocks - 1);
             const int8_t* p = c.codes + (phys * c.heads + h) * 2 * (kKvBlock * D);
-            raw[0] = *(const u32x4*)(p + from[0]);
-            if (CH == 2 || !second) raw[1] = *(const u32x4*)(p + from[1]);
+            raw[0] = *(const u32x4*)(p + from);
+            raw[1] = *(const u32x4*)(p + from + 512);
         };
         const auto fill = [&](int buf) {
-            if (second) {
 #pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    const u32x2 x0 = codes_f16(raw[k][0]), x1 = codes_f16(raw[k][1]);
-                    const u32x2 x2 = codes_f16(raw[k][2]), x3 = codes_f16(raw[k][3]);
-                    kbuf[buf][to[k]] = u32x4{x0[0], x0[1], x1[0], x1[1]};
-                    kbuf[buf][to[k] + 32] = u32x4{x2[0], x2[1], x3[0], x3[1]};
-                }
-            } else if (fills_v) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const u32x2 x0 = codes_f16(raw[0][t]), x1 = codes_f16(raw[1][t]);
-                    vbuf[buf][to[0] + 64 * t] = u32x4{x0[0], x0[1], x1[0], x1[1]};
-                }
+            for (int e = 0; e < 4; ++e) {
+                const u32x2 x0 = codes_f16(raw[0][e]), x1 = codes_f16(raw[1][e]);
+                if (D == 128 || fills) to[buf * (kKvBlock * D / 8) + 64 * e] = u32x4{x0[0], x0[1], x1[0], x1[1]};
             }
         };
         f32x16 x[2];
@@ -643,7 +629,8 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
             __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 1);
         };
         const auto softmax = [&](int i) {
-            const float f = rowf * pick(sk, i), lri = pick(lr, i);
+            // read with every lane active: a lane's value must not be computed behind a mask
+            const float f = rowf * pick(sk, i), lri = pick(lr, i), backi = pick(back, i);
             const int at = __builtin_amdgcn_readlane(number, i) * kKvBlock;
             // exponents against the maximum so far; token of x[t][e]:
             // at + 32 t + 8 (e / 4) + 4 half + e % 4
@@ -653,12 +640,13 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[t][e] = fmaf(x[t][e], f, base);
             if (all_first > at || all_last < at + 63) {
+                const int lo = first - at - 4 * half, hi = last - at - 4 * half;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int p = at + 32 * t + 8 * (e >> 2) + 4 * half + (e & 3);
-                        x[t][e] = p >= first && p <= last ? x[t][e] : -INFINITY;
+                        const int p = 32 * t + 8 * (e >> 2) + (e & 3);
+                        x[t][e] = p >= lo && p <= hi ? x[t][e] : -INFINITY;
                     }
             }
             float sum;
@@ -696,7 +684,7 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
                 weigh(by);
             }
             // a row that sees nothing here is spared a scale that is not finite
-            l += sum == 0.0f ? 0.0f : sum * pick(back, i);
+            l += sum == 0.0f ? 0.0f : sum * backi;
         };
 
         if (second) {

@@ -6,8 +6,10 @@
 // row c / G under query head h*G + c % G, so a group's G query heads share one
 // pass over the cached bytes.
 //
-// kv_attend_i8_kernel: 16 * CT columns per workgroup, for single tokens and
-// drafts, bound by the cache's bytes.  The codes go from memory to the int8
+// The int8 path: 16 columns per wave, for single tokens and drafts, bound by
+// the cache's bytes.  The four waves of a workgroup are X groups of 16 columns
+// that read the same blocks (from memory once, then from the caches), and
+// 4 / X of each that take blocks in turn.  The codes go from memory to the int8
 // matrix cores as they are:
 //   S^T = K Q^T    A = K (16 tokens x 64 dims, one 16-byte load per lane),
 //                  B = q as two int8 planes, x = 256 hi + lo of
@@ -22,12 +24,12 @@
 //                  its digits); int32 sums, scaled into the fp32 accumulator
 //                  once a block.
 // Every wave walks its own blocks with a running maximum and sum; the waves
-// of a workgroup meet in LDS at the end.
+// of a group meet in LDS at the end.
 //
 // Long sequences are split.  Only the device knows the lengths (a captured
 // graph follows them), so it also makes the split: the blocks of all units
 // (tile of columns, head) stand in one line, each unit padded to whole turns
-// of a workgroup's waves, and every workgroup takes an equal stretch of it.
+// of a group's waves, and every workgroup takes an equal stretch of it.
 // A unit that lies in one stretch is written at once, the parts of the others
 // are joined by a second kernel.
 #include "tern_device.h"
@@ -56,6 +58,10 @@ __device__ __forceinline__ void planes(float a, float b, float c, float d, uint3
     hi = __builtin_amdgcn_perm(cdh, abh, 0x07050301u);
     lo = __builtin_amdgcn_perm(cd, ab, 0x06040200u);
 }
+
+// waves that take the blocks of a tile of COLS columns in turn
+template <int COLS>
+constexpr int att_turn() { return COLS <= 16 * kAttWaves ? 16 * kAttWaves / COLS : 1; }
 
 // The tile of columns a workgroup or a joining row works on.
 struct AttTile {
@@ -119,7 +125,8 @@ __device__ __forceinline__ AttShare att_share(const KvBatch& b, int i, int G, in
     const int t1 = b.cu[i + 1];
     s.n = t1 - s.t0;
     s.p0 = kv_length(b, i) - s.n;
-    AttShare r = {0, kAttWaves};
+    constexpr uint32_t kTurn = att_turn<COLS>();
+    AttShare r = {0, kTurn};
     if (s.t0 < 0 || t1 > b.T || s.n <= 0) return r;
     r.tiles = (uint32_t)(((int64_t)s.n * G + COLS - 1) / COLS);
     const int last = att_last(s.p0 + s.n - 1, att_limit(b));
@@ -128,7 +135,7 @@ __device__ __forceinline__ AttShare att_share(const KvBatch& b, int i, int G, in
         const uint32_t most = ((uint32_t)window + COLS / G + 1) / kKvBlock + 2;
         blocks = blocks < most ? blocks : most;
     }
-    r.len = (blocks + kAttWaves - 1) / kAttWaves * kAttWaves;
+    r.len = (blocks + kTurn - 1) / kTurn * kTurn;
     return r;
 }
 
@@ -146,41 +153,52 @@ struct AttArgs {
 };
 
 // blocks of the line for each of `groups` workgroups
+template <int COLS>
 __device__ __forceinline__ uint32_t att_stretch(uint32_t total, int groups)
 {
-    const uint32_t turn = (uint32_t)groups * kAttWaves;
-    return (total + turn - 1) / turn * kAttWaves;
+    constexpr uint32_t kTurn = att_turn<COLS>();
+    const uint32_t turn = (uint32_t)groups * kTurn;
+    return (total + turn - 1) / turn * kTurn;
+}
+
+// bits 0, N, 2 N, ...
+template <int N>
+constexpr uint64_t every()
+{
+    uint64_t m = 0;
+    for (int i = 0; i < 64; i += N) m |= 1ull << i;
+    return m;
 }
 
 // blocks [begin, end) of one unit; whole: the result is written, else it is
 // part `slot` of the unit
-template <int D, int CT>
+template <int D, int X>
 __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b, const AttArgs& a,
                                               const AttTile& tile, int h, int begin, int end, bool whole,
                                               uint32_t slot)
 {
-    constexpr int S = D / 64, U = D / 16, COLS = 16 * CT;
+    constexpr int S = D / 64, U = D / 16, COLS = 16 * X, kTurn = att_turn<COLS>();
     constexpr int kPad = D + 4;
-    __shared__ float sacc[kAttWaves][COLS][kPad];
-    __shared__ float2 sstat[kAttWaves][COLS];
+    __shared__ float sacc[kAttWaves][16][kPad];
+    __shared__ float2 sstat[kAttWaves][16];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
 
     // this lane's columns: q as planes, the factor of its scores, the keys it sees
     const int limit = att_limit(b);
-    u32x4 qhi[CT][S], qlo[CT][S];
-    float rowf[CT];
-    int first[CT], last[CT];
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        const int col = 16 * ct + n;
+    const int group = wave % X;
+    u32x4 qhi[S], qlo[S];
+    float rowf;
+    int first, last;
+    {
+        const int col = 16 * group + n;
         const bool live = col < tile.cols;
         const int cc = tile.col0 + (live ? col : 0);
         const int j = cc / a.G;
         const uint16_t* row = a.q + (int64_t)(tile.s.t0 + j) * a.q_stride + (int64_t)(h * a.G + cc - j * a.G) * D;
         const int pos = tile.s.p0 + j;
-        first[ct] = live ? att_first(pos, a.window) : 0;
-        last[ct] = live ? att_last(pos, limit) : INT32_MAX;
+        first = live ? att_first(pos, a.window) : 0;
+        last = live ? att_last(pos, limit) : INT32_MAX;
         u32x4 raw[S][2];
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -205,7 +223,7 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
         // rows of nothing but zeros (or less than 2^-100) score 0; a row that
         // is not finite scores 0 * amax = NaN
         const float inv = live && amax >= 0x1p-100f && top < 0x7F800000u ? kPlane / 32767.0f / amax : 0.0f;
-        rowf[ct] = amax * (a.scale * kLog2e / kPlane);
+        rowf = amax * (a.scale * kLog2e / kPlane);
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -215,20 +233,15 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
                 planes(__builtin_bit_cast(float, w0 << 16) * inv, __builtin_bit_cast(float, w0 & 0xFFFF0000u) * inv,
                        __builtin_bit_cast(float, w1 << 16) * inv, __builtin_bit_cast(float, w1 & 0xFFFF0000u) * inv,
                        hi, lo);
-                qhi[ct][s][e] = inv == 0.0f ? 0u : hi;
-                qlo[ct][s][e] = inv == 0.0f ? 0u : lo;
+                qhi[s][e] = inv == 0.0f ? 0u : hi;
+                qlo[s][e] = inv == 0.0f ? 0u : lo;
             }
     }
 
-    float m[CT], l[CT];
-    f32x4 acc[CT][U];
+    float m = -INFINITY, l = 0.0f;
+    f32x4 acc[U];
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        m[ct] = -INFINITY;
-        l[ct] = 0.0f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) acc[ct][u] = f32x4{0, 0, 0, 0};
-    }
+    for (int u = 0; u < U; ++u) acc[u] = f32x4{0, 0, 0, 0};
 
     for (int seg = begin; seg < end; seg += 64) {
         // lane i looks up block seg + i: its place and scales
@@ -239,8 +252,8 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
             mine = kv_block(b, c, tile.s.i, tile.b0 + seg + lane);
             if (mine >= 0) sc = *(const float2*)(c.scales + ((int64_t)mine * c.heads + h) * 2);
         }
-        // this wave's blocks among those that are there
-        uint64_t todo = __ballot(mine >= 0) & (0x1111111111111111ull << wave);
+        // this wave's blocks among those that are there (none for a group without columns)
+        uint64_t todo = 16 * group < tile.cols ? __ballot(mine >= 0) & (every<kTurn>() << (wave / X)) : 0;
         const auto codes = [&](int i) {
             const int64_t phys = __builtin_amdgcn_readlane(mine, i);
             return c.codes + (phys * c.heads + h) * 2 * (kKvBlock * D);
@@ -271,96 +284,87 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
             const int8_t* next = codes(todo ? __builtin_ctzll(todo) : i);
             const int kib = todo ? 1024 : 0;
             const int at = (tile.b0 + seg + i) * kKvBlock;
+            float x[16];
+            const float f = rowf * sk;
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                float x[16];
-                const float f = rowf[ct] * sk;
+            for (int t = 0; t < 4; ++t) {
+                i32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    i32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
-#pragma unroll
-                    for (int s = 0; s < S; ++s) {
-                        hi = mfma_i8(kr[t][s], qhi[ct][s], hi);
-                        lo = mfma_i8(kr[t][s], qlo[ct][s], lo);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[4 * t + e] = (float)(hi[e] * 256 + lo[e]) * f;
-                    asm volatile("" : "+v"(x[4 * t]), "+v"(x[4 * t + 1]), "+v"(x[4 * t + 2]), "+v"(x[4 * t + 3]));
+                for (int s = 0; s < S; ++s) {
+                    hi = mfma_i8(kr[t][s], qhi[s], hi);
+                    lo = mfma_i8(kr[t][s], qlo[s], lo);
                 }
-                if (ct == CT - 1) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
+                for (int e = 0; e < 4; ++e) x[4 * t + e] = (float)(hi[e] * 256 + lo[e]) * f;
+                asm volatile("" : "+v"(x[4 * t]), "+v"(x[4 * t + 1]), "+v"(x[4 * t + 2]), "+v"(x[4 * t + 3]));
+            }
 #pragma unroll
-                        for (int s = 0; s < S; ++s) kr[t][s] = load(next, kib * (t * S + s));
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int s = 0; s < S; ++s) kr[t][s] = load(next, kib * (t * S + s));
+            const bool sees = first <= at + 63 && last >= at;
+            if (__any(first > at || last < at + 63)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int p = at + 16 * (e >> 2) + 4 * g + (e & 3);
+                    x[e] = p >= first && p <= last ? x[e] : -INFINITY;
                 }
-                const bool sees = first[ct] <= at + 63 && last[ct] >= at;
-                if (__any(first[ct] > at || last[ct] < at + 63)) {
+            }
+            float top = x[0];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int p = at + 16 * (e >> 2) + 4 * g + (e & 3);
-                        x[e] = p >= first[ct] && p <= last[ct] ? x[e] : -INFINITY;
-                    }
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // weights relative to the block's largest, in units of kPlane / 32767
+            const float base = (top == -INFINITY ? 0.0f : top) + 0x1.715664p-7f;   // log2(32767 / 32512)
+            float sum = 0.0f;
+            u32x4 phi, plo;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = exp2_fast(x[4 * t + e] - base);
+                    sum += w[e];
                 }
-                float top = x[0];
+                uint32_t hi, lo;
+                planes(w[0], w[1], w[2], w[3], hi, lo);
+                phi[t] = hi;
+                plo[t] = lo;
+            }
+            const float mn = fmaxf(m, top);
+            const float keep = m == mn ? 1.0f : exp2_fast(m - mn);
+            const float join = top == -INFINITY ? 0.0f : exp2_fast(top - mn);
+            const float fv = sees ? join * sv * (1.0f / 32767.0f) : 0.0f;
+            m = mn;
+            l = l * keep + sum * join;
 #pragma unroll
-                for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                // weights relative to the block's largest, in units of kPlane / 32767
-                const float base = (top == -INFINITY ? 0.0f : top) + 0x1.715664p-7f;   // log2(32767 / 32512)
-                float sum = 0.0f;
-                u32x4 phi, plo;
+            for (int u = 0; u < U; ++u) {
+                const i32x4 zero = {0, 0, 0, 0};
+                const i32x4 hi = mfma_i8(vr[u], phi, zero), lo = mfma_i8(vr[u], plo, zero);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    float w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        w[e] = exp2_fast(x[4 * t + e] - base);
-                        sum += w[e];
-                    }
-                    uint32_t hi, lo;
-                    planes(w[0], w[1], w[2], w[3], hi, lo);
-                    phi[t] = hi;
-                    plo[t] = lo;
-                }
-                const float mn = fmaxf(m[ct], top);
-                const float keep = m[ct] == mn ? 1.0f : exp2_fast(m[ct] - mn);
-                const float join = top == -INFINITY ? 0.0f : exp2_fast(top - mn);
-                const float fv = sees ? join * sv * (1.0f / 32767.0f) : 0.0f;
-                m[ct] = mn;
-                l[ct] = l[ct] * keep + sum * join;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const i32x4 zero = {0, 0, 0, 0};
-                    const i32x4 hi = mfma_i8(vr[u], phi, zero), lo = mfma_i8(vr[u], plo, zero);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[ct][u][e] = fmaf((float)(hi[e] * 256 + lo[e]), fv, acc[ct][u][e] * keep);
-                    // in this order: or all sums wait in registers behind the loads below
-                    asm volatile("" : "+v"(acc[ct][u]));
-                }
+                for (int e = 0; e < 4; ++e)
+                    acc[u][e] = fmaf((float)(hi[e] * 256 + lo[e]), fv, acc[u][e] * keep);
+                // in this order: or all sums wait in registers behind the loads below
+                asm volatile("" : "+v"(acc[u]));
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) vr[u] = load(next, kib * (U + u));
         }
     }
 
-    // the waves meet: common maximum, scaled sums
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        l[ct] += __shfl_xor(l[ct], 16);
-        l[ct] += __shfl_xor(l[ct], 32);
-        if (g == 0) sstat[wave][16 * ct + n] = make_float2(m[ct], l[ct]);
-    }
+    // a group's waves meet: common maximum, scaled sums
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) sstat[wave][n] = make_float2(m, l);
     __syncthreads();
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
+    {
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kAttWaves; ++w) top = fmaxf(top, sstat[w][16 * ct + n].x);
-        const float f = m[ct] == top ? 1.0f : exp2_fast(m[ct] - top);
+        for (int w = 0; w < kTurn; ++w) top = fmaxf(top, sstat[group + X * w][n].x);
+        const float f = m == top ? 1.0f : exp2_fast(m - top);
 #pragma unroll
-        for (int u = 0; u < U; ++u) *(f32x4*)&sacc[wave][16 * ct + n][16 * u + 4 * g] = acc[ct][u] * f;
+        for (int u = 0; u < U; ++u) *(f32x4*)&sacc[wave][n][16 * u + 4 * g] = acc[u] * f;
     }
     __syncthreads();
     constexpr int kPer = D / 4;                     // threads per column, four dims each
@@ -369,12 +373,12 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
         float top = -INFINITY, sum = 0.0f;
         f32x4 o = {0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < kAttWaves; ++w) top = fmaxf(top, sstat[w][col].x);
+        for (int w = 0; w < kTurn; ++w) top = fmaxf(top, sstat[(col >> 4) + X * w][col & 15].x);
 #pragma unroll
-        for (int w = 0; w < kAttWaves; ++w) {
-            const float2 st = sstat[w][col];
+        for (int w = 0; w < kTurn; ++w) {
+            const float2 st = sstat[(col >> 4) + X * w][col & 15];
             sum += st.y * (st.x == top ? 1.0f : exp2_fast(st.x - top));
-            o += *(const f32x4*)&sacc[w][col][d];
+            o += *(const f32x4*)&sacc[(col >> 4) + X * w][col & 15][d];
         }
         if (!whole) {
             const uint32_t at = slot * COLS + col;
@@ -748,14 +752,14 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
     }
 }
 
-// CT 1 and 2: 16 and 32 columns on the int8 path, CT 16: 256 on the fp16 path
-template <int CT>
-constexpr int att_threads() { return CT <= 2 ? 64 * kAttWaves : 64 * kTileWaves; }
+// COLS 16, 32 and 64: the int8 path, 256: the fp16 path
+template <int COLS>
+constexpr int att_threads() { return COLS <= 64 ? 64 * kAttWaves : 64 * kTileWaves; }
 
-template <int D, int CT>
-__global__ __launch_bounds__(att_threads<CT>(), CT == 1 ? 3 : 2) void kv_attend_kernel(KvCache c, KvBatch b, AttArgs a)
+template <int D, int COLS>
+__global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_attend_kernel(KvCache c, KvBatch b,
+                                                                                            AttArgs a)
 {
-    constexpr int COLS = 16 * CT;
     const int lane = threadIdx.x & 63;
     AttTile tile;
     AttShare r = {0, 1};
@@ -786,7 +790,7 @@ __global__ __launch_bounds__(att_threads<CT>(), CT == 1 ? 3 : 2) void kv_attend_
             }
             if (lane == 0) a.start[b.nseq] = total;
         }
-        const uint32_t per = att_stretch(total, a.groups);
+        const uint32_t per = att_stretch<COLS>(total, a.groups);
         if (per > total && blockIdx.x > 0) return;            // the products below stay in 32 bits
         x0 = x = blockIdx.x * per;
         x1 = x > total || total - x < per ? total : x + per;
@@ -832,7 +836,7 @@ __global__ __launch_bounds__(att_threads<CT>(), CT == 1 ? 3 : 2) void kv_attend_
             att_uniform(tile);
             end = end < tile.nblk ? end : tile.nblk;
             if (begin < end || begin == 0) {
-                if constexpr (CT <= 2) attend_blocks<D, CT>(c, b, a, tile, h, begin, end, whole, slot);
+                if constexpr (COLS <= 64) attend_blocks<D, COLS / 16>(c, b, a, tile, h, begin, end, whole, slot);
                 else attend_tile_f16<D>(c, b, a, tile, h, begin, end, whole, slot);
             }
         }
@@ -856,12 +860,13 @@ __global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel
     AttTile tile;
     int64_t j;
     if (t >= (uint32_t)b.T || !kv_find(b, t, 1, 1, 0, tile.s, j) || j >= tile.s.n) return;
-    const uint32_t total = a.start[b.nseq], start = a.start[tile.s.i];
     const AttShare r = att_share<COLS>(b, tile.s.i, a.G, a.window, tile.s);
+    const bool alone = b.nseq == 1;          // one load's latency less
+    const uint32_t total = alone ? r.tiles * c.heads * r.len : a.start[b.nseq], start = alone ? 0 : a.start[tile.s.i];
     const int64_t cc = j * a.G + (hq - h * a.G);
     const int number = (int)(cc / COLS), col = (int)(cc % COLS);
     if (!att_tile<COLS>(b, number, a.G, a.window, tile)) return;
-    const uint32_t per = att_stretch(total, a.groups);
+    const uint32_t per = att_stretch<COLS>(total, a.groups);
     const uint32_t u0 = start + (h * r.tiles + number) * r.len, w0 = u0 / per;
     if ((u0 + r.len - 1) / per == w0) return;                       // whole: written already
     const int used = (int)((u0 + (tile.nblk > 0 ? tile.nblk : 1) - 1) / per - w0) + 1;   // parts with blocks seen
@@ -930,21 +935,32 @@ struct AttPlan {
     int64_t part_floats, stats, starts;
 };
 
-constexpr int64_t kAttGroups = 768;          // three workgroups a CU (two with more columns): what registers allow
+constexpr int64_t kAttGroups = 768;          // three workgroups a CU: what registers allow on the int8 path
+constexpr int64_t kTileGroups = 256;         // one a CU on the fp16 path
 constexpr int64_t kAttWholeBlocks = 16;      // up to here a unit is not split
+// The choice between the paths, measured on eight caches used in turn, 32:8
+// heads of 128 (16 columns a unit / 64 / 256 fp16, us):
+//   17 rows over 4096   21.0 / 22.8 / 24.5     64 rows over 2048   15.6 / 22.9 / 30.9
+//   32 rows over 12345  48.9 / 37.7 / 40.4     256 rows over 4096  47.6 / 48.6 / 42.1
+//   16 x 24 up to 2000  49.9 / 39.7 / 59.9     256 rows over 12345  216 /  104 / 82.9
+constexpr int64_t kAttShared = 4096;         // (block, head) pairs from which tiles of one head share their reads
+constexpr int64_t kAttTileCols = 128;        // columns a sequence from which 256-column tiles pay off,
+constexpr int64_t kAttSmall = 24576;         // unless (unit of 16 columns, block) pairs are at most so many
 
 static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
 {
     AttPlan p{};
-    const int64_t G = Hq / heads;
-    p.cols = T * G <= 16 * nseq ? 16 : T * G <= 32 * nseq ? 32 : 256;
-    p.items = T * G / p.cols + nseq;
-    const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock, units = p.items * heads;
-    const int64_t most = p.cols == 16 ? kAttGroups : p.cols == 32 ? kAttGroups / 3 * 2 : kAttGroups / 3;
-    if (blocks <= kAttWholeBlocks || units >= 2 * most) return p;
-    const int64_t turns = (blocks + kAttWaves - 1) / kAttWaves;
-    p.groups = (int)(units > most / turns ? most : units * turns);
-    p.stats = p.groups * 2 * p.cols;
+    const int64_t cols = T * (Hq / heads), blocks = (max_len + kKvBlock - 1) / kKvBlock;
+    if (cols > kAttTileCols * nseq && (cols / 16 + nseq) * heads * blocks > kAttSmall) p.cols = 256;
+    else if (cols <= 16 * nseq || nseq * heads * blocks < kAttShared) p.cols = 16;
+    else p.cols = cols <= 32 * nseq ? 32 : 64;
+    p.items = cols / p.cols + nseq;
+    const int64_t units = p.items * heads, most = p.cols == 256 ? kTileGroups : 2 * kAttGroups;
+    if (blocks <= kAttWholeBlocks || units >= most) return p;
+    const int64_t turn = p.cols <= 64 ? 64 / p.cols : 1, turns = (blocks + turn - 1) / turn;
+    const int64_t groups = p.cols == 256 ? kTileGroups : kAttGroups;
+    p.groups = (int)(units > groups / turns ? groups : units * turns);
+    p.stats = (int64_t)p.groups * 2 * p.cols;
     p.part_floats = p.stats * D;
     p.starts = nseq + 1;
     return p;
@@ -956,19 +972,22 @@ int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t 
     return p.part_floats * 4 + p.stats * 8 + p.starts * 4;
 }
 
-template <int D, int CT>
+template <int D, int COLS>
 static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, const AttPlan& p,
                             hipStream_t stream)
 {
     const int64_t grid = a.groups ? a.groups : p.items * c.heads;
-    kv_attend_kernel<D, CT><<<(unsigned)grid, att_threads<CT>(), 0, stream>>>(c, b, a);
+    kv_attend_kernel<D, COLS><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.groups == 0) return e;
     const int64_t rows = (int64_t)b.T * c.heads * a.G;
-    if ((int64_t)b.nseq * c.heads * 8 >= a.groups || rows >= 2048)      // about eight parts a row or fewer, or rows enough
-        kv_attend_join_kernel<D, 16 * CT, 1><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(c, b, a);
+    // few rows: their parts to many waves
+    if (rows <= 256)
+        kv_attend_join_kernel<D, COLS, 12><<<(unsigned)rows, 768, 0, stream>>>(c, b, a);
+    else if (rows <= 2048 && (int64_t)b.nseq * c.heads * 8 < a.groups)
+        kv_attend_join_kernel<D, COLS, 4><<<(unsigned)rows, 256, 0, stream>>>(c, b, a);
     else
-        kv_attend_join_kernel<D, 16 * CT, 12><<<(unsigned)rows, 768, 0, stream>>>(c, b, a);
+        kv_attend_join_kernel<D, COLS, 1><<<(unsigned)((rows + 3) / 4), 256, 0, stream>>>(c, b, a);
     return hipGetLastError();
 }
 
@@ -990,13 +1009,20 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const
     // the line is counted in 32 bits; a batch that could pass that has units enough
     const int64_t line = p.items * c.heads * ((int64_t)b.table_width + kAttWaves);
     a.groups = line < (1ll << 31) ? p.groups : 0;
-    if (D == 128)
-        return p.cols == 16   ? attend<128, 1>(c, b, a, p, stream)
-               : p.cols == 32 ? attend<128, 2>(c, b, a, p, stream)
-                              : attend<128, 16>(c, b, a, p, stream);
-    return p.cols == 16   ? attend<64, 1>(c, b, a, p, stream)
-           : p.cols == 32 ? attend<64, 2>(c, b, a, p, stream)
-                          : attend<64, 16>(c, b, a, p, stream);
+    if (D == 128) {
+        switch (p.cols) {
+        case 16: return attend<128, 16>(c, b, a, p, stream);
+        case 32: return attend<128, 32>(c, b, a, p, stream);
+        case 64: return attend<128, 64>(c, b, a, p, stream);
+        default: return attend<128, 256>(c, b, a, p, stream);
+        }
+    }
+    switch (p.cols) {
+    case 16: return attend<64, 16>(c, b, a, p, stream);
+    case 32: return attend<64, 32>(c, b, a, p, stream);
+    case 64: return attend<64, 64>(c, b, a, p, stream);
+    default: return attend<64, 256>(c, b, a, p, stream);
+    }
 }
 
 }  // namespace tern

@@ -748,70 +748,89 @@ def tern_mfma_peak(kind: str, iters: int, grid: int, sink=None, stream=None):
 
 # ---- attention over a paged int8 cache ----
 
+# Per-call costs count here (a decode step's kernels take microseconds), so
+# what torch is asked for per call is kept small: torch and the library's
+# functions are looked up once, devices are compared by index, and the stream
+# is taken as the number that the C ABI wants.
+_torch = None
+_TYPES = {}
+_raw_stream = None
+
+
+def _setup():
+    global _torch, _TYPES, _raw_stream
+    if _torch is None:
+        import torch
+        _TYPES = {torch.float32: 0, torch.bfloat16: 1}
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _torch = torch
+    return _torch
+
+
 def _vec(t, name, dtype, shape, device=None):
     """A contiguous device tensor of one dtype and shape (None: any size)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise RuntimeError(f"{name} must be a CUDA/HIP tensor")
+    if t.shape == shape and t.dtype == dtype and t.get_device() == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise RuntimeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
         raise RuntimeError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if not t.is_contiguous():
         raise RuntimeError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise RuntimeError(f"{name} is on {t.device}, expected {device}")
+    if device is not None and t.get_device() != device:
+        raise RuntimeError(f"{name} is on {t.device}, expected device {device}")
 
 
-def _rows(t, name, dtypes, device=None, heads=None, d=None, tokens=None):
-    """A [T, heads, D] tensor whose rows may be strided and whose heads are contiguous; its row stride."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _rows(t, name, dtype, device, heads, d, tokens):
+    """A [T, heads, D] tensor whose rows may be strided and whose heads are contiguous: (T, heads, row
+    stride).  dtype None: fp32 or bf16; heads or tokens None: any."""
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
         raise RuntimeError(f"{name} must be a CUDA/HIP tensor")
-    if t.dtype not in dtypes:
-        raise RuntimeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() != 3:
+    if t.dtype != dtype if dtype is not None else t.dtype not in _TYPES:
+        raise RuntimeError(f"{name} has dtype {t.dtype}, expected {dtype or 'float32 or bfloat16'}")
+    shape = t.shape
+    if len(shape) != 3:
         raise RuntimeError(f"{name} must be [T, heads, D]")
-    for got, want, what in zip(t.shape, (tokens, heads, d), ("T", "heads", "D")):
-        if want is not None and got != want:
-            raise RuntimeError(f"{name} has {what} = {got}, expected {want}")
-    if device is not None and t.device != device:
-        raise RuntimeError(f"{name} is on {t.device}, expected {device}")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+    n, h, dd = shape
+    if dd != d or (heads is not None and h != heads) or (tokens is not None and n != tokens):
+        raise RuntimeError(f"{name} has shape {tuple(shape)}, expected [{'T' if tokens is None else tokens}, "
+                           f"{'heads' if heads is None else heads}, {d}]")
+    if t.get_device() != device:
+        raise RuntimeError(f"{name} is on {t.device}, expected device {device}")
+    row, head, one = t.stride()
+    if n and h and (one != 1 or (h > 1 and head != d)):
         raise RuntimeError(f"{name}: the heads of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-class _on:
-    """Make a tensor's device the current one for a call (nothing to do where it already is)."""
-
-    def __init__(self, device):
-        import torch
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _device_stream(device, stream):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    return n, h, row if n > 1 else h * d
 
 
 def _new(shape, dtype, device, stream):
     """An output or workspace for one call; memory used on a stream that is not the current one is kept
     from reuse until that stream is done with it."""
-    import torch
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and stream != torch.cuda.current_stream(device):
+    t = _torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and stream != _torch.cuda.current_stream(device):
         t.record_stream(stream)
     return t
+
+
+def _call(name, device, stream, *args):
+    """One library call on a device: made the current one where it is not, on its current stream or the
+    one given."""
+    handle = _raw_stream(device) if stream is None else stream.cuda_stream
+    f = getattr(_lib or lib(), name)
+    if _torch.cuda.current_device() == device:
+        rc = f(*args, handle)
+    else:
+        with _torch.cuda.device(device):
+            rc = f(*args, handle)
+    if rc:
+        _check(name, rc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 class QkTransform:
@@ -819,19 +838,16 @@ class QkTransform:
     style of one layer's query and key heads; None leaves a part out."""
 
     def __init__(self, d: int, q_gain=None, k_gain=None, eps: float = 1e-6, inv_freq=None, interleaved: bool = False):
-        import torch
+        torch = _setup()
         self.d, self.q_gain, self.k_gain, self.inv_freq = d, q_gain, k_gain, inv_freq
-        self.device = None
+        self.device = None               # index; None: holds no tensor
         for t, name, dtype, n in ((q_gain, "q_gain", torch.float32, d), (k_gain, "k_gain", torch.float32, d),
                                   (inv_freq, "inv_freq", torch.float64, d // 2)):
             if t is not None:
                 _vec(t, name, dtype, (n,), self.device)
-                self.device = t.device
+                self.device = t.get_device()
         self.c = _QkTransform(_addr(q_gain), _addr(k_gain), _addr(inv_freq), eps, int(interleaved))
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+        self.ref = ctypes.byref(self.c)
 
 
 class I8KvCache:
@@ -839,7 +855,7 @@ class I8KvCache:
     (one for each block of 64 tokens, head and side K, V).  Allocated here, or over tensors given."""
 
     def __init__(self, blocks: int = 0, heads: int = 0, d: int = 0, device="cuda", codes=None, scales=None):
-        import torch
+        torch = _setup()
         if codes is None:
             codes = torch.zeros((blocks, heads, 2, KV_BLOCK * d), dtype=torch.int8, device=device)
             scales = torch.zeros((blocks, heads, 2), dtype=torch.float32, device=device)
@@ -847,10 +863,11 @@ class I8KvCache:
         blocks, heads, _, width = codes.shape
         if width not in (KV_BLOCK * 64, KV_BLOCK * 128):
             raise RuntimeError(f"codes hold {width} bytes a side, expected 64 * D with D 64 or 128")
-        _vec(scales, "scales", torch.float32, (blocks, heads, 2), codes.device)
-        self.codes, self.scales, self.device = codes, scales, codes.device
+        self.codes, self.scales, self.device = codes, scales, codes.get_device()
+        _vec(scales, "scales", torch.float32, (blocks, heads, 2), self.device)
         self.blocks, self.heads, self.d = blocks, heads, width // KV_BLOCK
         self.c = _KvCache(codes.data_ptr(), scales.data_ptr(), blocks, heads, self.d)
+        self.ref = ctypes.byref(self.c)
 
 
 class I8KvBatch:
@@ -859,125 +876,114 @@ class I8KvBatch:
     The kernels read all three, so they may be changed in place between calls."""
 
     def __init__(self, cu, lens, table):
-        import torch
+        torch = _setup()
         _vec(cu, "cu", torch.int32, (None,))
         nseq = cu.shape[0] - 1
         if nseq < 0:
             raise RuntimeError("cu needs nseq + 1 entries")
-        _vec(lens, "lens", torch.int32, (nseq,), cu.device)
-        if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.device != cu.device:
+        self.device = cu.get_device()
+        _vec(lens, "lens", torch.int32, (nseq,), self.device)
+        if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.get_device() != self.device:
             raise RuntimeError("table must be an int32 tensor on the device of cu")
         if table.dim() != 2 or table.shape[0] != nseq or (table.shape[1] > 1 and table.stride(1) != 1):
             raise RuntimeError(f"table has shape {tuple(table.shape)}, expected ({nseq}, width) with contiguous rows")
-        self.cu, self.lens, self.table, self.device, self.nseq = cu, lens, table, cu.device, nseq
+        self.cu, self.lens, self.table, self.nseq = cu, lens, table, nseq
         self.width = table.shape[1]
         stride = table.stride(0) if nseq > 1 else self.width
         self.c = _KvBatch(cu.data_ptr(), lens.data_ptr(), table.data_ptr(), nseq, self.width, stride)
-
-
-def _kv_types():
-    import torch
-    return {torch.float32: 0, torch.bfloat16: 1}
+        self.ref = ctypes.byref(self.c)
 
 
 def qk_norm_rope(transform, q, k, pos=None, q_out=None, k_out=None, out_dtype=None, stream=None):
     """Norm and rotation of q [T, Hq, D] and k [T, Hk, D] (fp32 or bf16 rows, e.g. parts of one fused
     row; either may be None) at positions pos int32 [T]: (q, k) contiguous, out_dtype bf16 (default) or fp32."""
-    import torch
-    types = _kv_types()
     x = q if q is not None else k
     if x is None:
         raise RuntimeError("qk_norm_rope: q or k is needed")
-    device = x.device
-    args = []
-    outs = []
+    device = transform.device
+    if device is None:
+        device = x.get_device() if isinstance(x, _torch.Tensor) else -1
+    d = transform.d
     if out_dtype is None:
-        out_dtype = q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else torch.bfloat16
-    if out_dtype not in types:
-        raise RuntimeError(f"out_dtype {out_dtype}, expected one of {tuple(types)}")
-    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is None:
-            args += [None, 0, 0]
-            outs.append(None)
-            continue
-        stride = _rows(t, name, (x.dtype,) if x.dtype in types else tuple(types), device, None, transform.d,
-                       x.shape[0])
-        args += [t.data_ptr(), t.shape[1], stride]
-        if out is None:
-            out = _new(t.shape, out_dtype, device, stream)
+        out_dtype = q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else _torch.bfloat16
+    if out_dtype not in _TYPES:
+        raise RuntimeError(f"out_dtype {out_dtype}, expected float32 or bfloat16")
+    tokens = dtype = None
+    hq = qs = hk = ks = 0
+    if q is not None:
+        tokens, hq, qs = _rows(q, "q", None, device, None, d, None)
+        dtype = q.dtype
+        if q_out is None:
+            q_out = _new((tokens, hq, d), out_dtype, device, stream)
         else:
-            _vec(out, f"{name}_out", out_dtype, tuple(t.shape), device)
-        outs.append(out)
-    if transform.device is not None and transform.device != device:
-        raise RuntimeError(f"transform is on {transform.device}, expected {device}")
+            _vec(q_out, "q_out", out_dtype, (tokens, hq, d), device)
+    if k is not None:
+        tokens, hk, ks = _rows(k, "k", dtype, device, None, d, tokens)
+        dtype = k.dtype
+        if k_out is None:
+            k_out = _new((tokens, hk, d), out_dtype, device, stream)
+        else:
+            _vec(k_out, "k_out", out_dtype, (tokens, hk, d), device)
     if pos is not None:
-        _vec(pos, "pos", torch.int32, (x.shape[0],), device)
-    with _on(device):
-        _check("qk_norm_rope", lib().qk_norm_rope(ctypes.byref(transform.c), x.shape[0], transform.d, *args,
-                                                  types[x.dtype], _addr(pos), _addr(outs[0]), _addr(outs[1]),
-                                                  types[out_dtype], _device_stream(device, stream)))
-    return tuple(outs)
+        _vec(pos, "pos", _torch.int32, (tokens,), device)
+    _call("qk_norm_rope", device, stream, transform.ref, tokens, d, _addr(q), hq, qs, _addr(k), hk, ks,
+          _TYPES[dtype], _addr(pos), _addr(q_out) if q is not None else None,
+          _addr(k_out) if k is not None else None, _TYPES[out_dtype])
+    return (q_out if q is not None else None), (k_out if k is not None else None)
 
 
 def _kv_device(cache, batch, transform=None):
     if batch.device != cache.device:
-        raise RuntimeError(f"batch is on {batch.device}, expected {cache.device}")
+        raise RuntimeError(f"batch is on device {batch.device}, expected {cache.device}")
     if transform is not None and transform.device is not None and transform.device != cache.device:
-        raise RuntimeError(f"transform is on {transform.device}, expected {cache.device}")
+        raise RuntimeError(f"transform is on device {transform.device}, expected {cache.device}")
     return cache.device
 
 
 def i8_kv_append(cache, batch, transform, k, v, q=None, pos=None, q_out=None, stream=None):
     """Append k, v [T, heads, D] (fp32 or bf16 rows) to the cache, k normalised and rotated on the way;
     with q [T, Hq, D] also its norm and rotation -> q bf16 [T, Hq, D] (else None)."""
-    import torch
-    types = _kv_types()
-    device = _kv_device(cache, batch, transform)
-    if transform.d != cache.d:
-        raise RuntimeError(f"transform is for D = {transform.d}, the cache for {cache.d}")
-    ks = _rows(k, "k", tuple(types), device, cache.heads, cache.d)
-    tokens = k.shape[0]
-    vs = _rows(v, "v", (k.dtype,), device, cache.heads, cache.d, tokens)
+    device, d = _kv_device(cache, batch, transform), cache.d
+    if transform.d != d:
+        raise RuntimeError(f"transform is for D = {transform.d}, the cache for {d}")
+    tokens, _, ks = _rows(k, "k", None, device, cache.heads, d, None)
+    dtype = k.dtype
+    vs = _rows(v, "v", dtype, device, cache.heads, d, tokens)[2]
     hq = qs = 0
     if q is not None:
-        qs = _rows(q, "q", (k.dtype,), device, None, cache.d, tokens)
-        hq = q.shape[1]
+        _, hq, qs = _rows(q, "q", dtype, device, None, d, tokens)
         if q_out is None:
-            q_out = _new(q.shape, torch.bfloat16, device, stream)
+            q_out = _new((tokens, hq, d), _torch.bfloat16, device, stream)
         else:
-            _vec(q_out, "q_out", torch.bfloat16, tuple(q.shape), device)
+            _vec(q_out, "q_out", _torch.bfloat16, (tokens, hq, d), device)
     elif q_out is not None:
         raise RuntimeError("q_out without q")
     if pos is not None:
-        _vec(pos, "pos", torch.int32, (tokens,), device)
-    with _on(device):
-        _check("i8_kv_append", lib().i8_kv_append(ctypes.byref(cache.c), ctypes.byref(batch.c),
-                                                  ctypes.byref(transform.c), tokens, _addr(q), hq, qs, k.data_ptr(),
-                                                  ks, v.data_ptr(), vs, types[k.dtype], _addr(pos), _addr(q_out),
-                                                  _device_stream(device, stream)))
+        _vec(pos, "pos", _torch.int32, (tokens,), device)
+    _call("i8_kv_append", device, stream, cache.ref, batch.ref, transform.ref, tokens, _addr(q), hq, qs, k.data_ptr(),
+          ks, v.data_ptr(), vs, _TYPES[dtype], _addr(pos), _addr(q_out))
     return q_out
 
 
 def i8_kv_read(cache, batch, tokens: int, dtype=None, k_out=None, v_out=None, stream=None):
     """The batch's tokens (`tokens` rows) read back from the cache: (k, v) [T, heads, D], bf16 or fp32."""
-    import torch
-    types = _kv_types()
     device = _kv_device(cache, batch)
     if dtype is None:
-        dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.bfloat16
-    if dtype not in types:
-        raise RuntimeError(f"dtype {dtype}, expected one of {tuple(types)}")
-    outs = []
-    for out, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if out is None:
-            out = _new((tokens, cache.heads, cache.d), dtype, device, stream)
-        else:
-            _vec(out, name, dtype, (tokens, cache.heads, cache.d), device)
-        outs.append(out)
-    with _on(device):
-        _check("i8_kv_read", lib().i8_kv_read(ctypes.byref(cache.c), ctypes.byref(batch.c), tokens, _addr(outs[0]),
-                                              _addr(outs[1]), types[dtype], _device_stream(device, stream)))
-    return tuple(outs)
+        dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else _torch.bfloat16
+    if dtype not in _TYPES:
+        raise RuntimeError(f"dtype {dtype}, expected float32 or bfloat16")
+    shape = (tokens, cache.heads, cache.d)
+    if k_out is None:
+        k_out = _new(shape, dtype, device, stream)
+    else:
+        _vec(k_out, "k_out", dtype, shape, device)
+    if v_out is None:
+        v_out = _new(shape, dtype, device, stream)
+    else:
+        _vec(v_out, "v_out", dtype, shape, device)
+    _call("i8_kv_read", device, stream, cache.ref, batch.ref, tokens, k_out.data_ptr(), v_out.data_ptr(),
+          _TYPES[dtype])
+    return k_out, v_out
 
 
 def i8_kv_attend_workspace_bytes(tokens: int, hq: int, heads: int, d: int, nseq: int, max_len: int) -> int:
@@ -986,37 +992,32 @@ def i8_kv_attend_workspace_bytes(tokens: int, hq: int, heads: int, d: int, nseq:
 
 def i8_kv_attend_workspace(cache, batch, tokens: int, hq: int, max_len=None):
     """A workspace for i8_kv_attend of `tokens` rows of hq heads (None where none is needed)."""
-    import torch
     nbytes = i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, cache.d, batch.nseq,
                                           max_len or max(1, batch.width * KV_BLOCK))
     if nbytes < 0:
         _check("i8_kv_attend_workspace_bytes", 2)
-    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
+    return _torch.empty(nbytes, dtype=_torch.uint8, device=cache.device) if nbytes else None
 
 
 def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, out=None, workspace=None, stream=None):
     """Attention of q bf16 [T, Hq, D] over the batch's cached tokens, causal, with a sliding window
     where window > 0 -> bf16 [T, Hq, D].  scale: D ** -0.5 by default.  max_len: the longest length
     that batch.lens will hold (default: what the table can hold)."""
-    import torch
-    device = _kv_device(cache, batch)
-    stride = _rows(q, "q", (torch.bfloat16,), device, None, cache.d)
-    tokens, hq = q.shape[0], q.shape[1]
-    max_len = max_len or max(1, batch.width * KV_BLOCK)
+    device, d = _kv_device(cache, batch), cache.d
+    tokens, hq, stride = _rows(q, "q", _torch.bfloat16, device, None, d, None)
+    if max_len is None:
+        max_len = batch.width * KV_BLOCK or 1
     if out is None:
-        out = _new(q.shape, torch.bfloat16, device, stream)
+        out = _new((tokens, hq, d), _torch.bfloat16, device, stream)
     else:
-        _vec(out, "out", torch.bfloat16, tuple(q.shape), device)
-    need = lib().i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, cache.d, batch.nseq, max_len)
+        _vec(out, "out", _torch.bfloat16, (tokens, hq, d), device)
+    need = lib().i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len)
     if workspace is None:
         if need > 0:
-            workspace = _new(need, torch.uint8, device, stream)
-    elif workspace.device != device or not workspace.is_contiguous() or \
+            workspace = _new(need, _torch.uint8, device, stream)
+    elif workspace.get_device() != device or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
-        raise RuntimeError(f"workspace must be a contiguous tensor of at least {need} bytes on {device}")
-    with _on(device):
-        _check("i8_kv_attend", lib().i8_kv_attend(ctypes.byref(cache.c), ctypes.byref(batch.c), tokens, q.data_ptr(),
-                                                  hq, stride, cache.d ** -0.5 if scale is None else scale, window,
-                                                  max_len, out.data_ptr(), _addr(workspace),
-                                                  _device_stream(device, stream)))
+        raise RuntimeError(f"workspace must be a contiguous tensor of at least {need} bytes on device {device}")
+    _call("i8_kv_attend", device, stream, cache.ref, batch.ref, tokens, q.data_ptr(), hq, stride,
+          d ** -0.5 if scale is None else scale, window, max_len, out.data_ptr(), _addr(workspace))
     return out

@@ -614,7 +614,8 @@ namespace {
 
 constexpr int64_t kKvMaxRows = 1 << 24;     // rows of a per-token tensor, sequences of a batch
 constexpr int64_t kKvMaxHeads = 1024;
-constexpr int64_t kKvMaxGrid = 0x7FFFFFFF;  // workgroups of one launch
+constexpr int64_t kKvMaxGrid = (1 << 24) - 1; // workgroups of one launch: 2^32 threads at 256 each
+constexpr int64_t kKvMaxPairs = 1 << 25;      // (row, query head) pairs of one attention call
 
 bool kv_bad_d(int64_t D) { return D != 64 && D != 128; }
 bool kv_bad_type(int t) { return t != TERN_F32 && t != TERN_BF16; }
@@ -643,12 +644,12 @@ tern::QkTransform kv_transform(const tern_qk_transform* f)
 int kv_check_shape(const i8_kv_cache* c, const i8_kv_batch* b, int64_t T, bool* empty)
 {
     if (!c || !b) return TERN_E_NULL;
-    if (kv_bad_d(c->D) || c->heads < 1 || c->heads > kKvMaxHeads || c->blocks < 0 || c->blocks > kKvMaxGrid)
+    if (kv_bad_d(c->D) || c->heads < 1 || c->heads > kKvMaxHeads || c->blocks < 0 || c->blocks > INT32_MAX)
         return TERN_E_SHAPE;
-    if (b->nseq < 0 || b->nseq > kKvMaxRows || b->table_width < 0 || b->table_width > kKvMaxGrid / TERN_KV_BLOCK ||
+    if (b->nseq < 0 || b->nseq > kKvMaxRows || b->table_width < 0 || b->table_width > INT32_MAX / TERN_KV_BLOCK ||
         b->table_stride < b->table_width || T < 0 || T > kKvMaxRows)
         return TERN_E_SHAPE;
-    if ((T / TERN_KV_BLOCK + 2 * b->nseq) * c->heads > kKvMaxGrid) return TERN_E_SHAPE;
+    if ((T / TERN_KV_BLOCK + 2 * b->nseq) * c->heads * tern::kKvRoles > kKvMaxGrid) return TERN_E_SHAPE;
     *empty = T == 0 || b->nseq == 0;
     return TERN_OK;
 }
@@ -738,8 +739,8 @@ int i8_kv_read(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, vo
 int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
 {
     if (kv_bad_d(D) || T < 0 || T > kKvMaxRows || heads < 1 || heads > kKvMaxHeads || Hq < 1 || Hq > kKvMaxHeads ||
-        Hq % heads != 0 || T * Hq > kKvMaxGrid || nseq < 0 || nseq > kKvMaxRows || max_len < 1 ||
-        max_len > kKvMaxGrid)
+        Hq % heads != 0 || T * Hq > kKvMaxPairs || nseq < 0 || nseq > kKvMaxRows || max_len < 1 ||
+        max_len > INT32_MAX)
         return -1;
     if (T == 0 || nseq == 0) return 0;
     return tern::kv_attend_workspace_bytes(T, Hq, heads, D, nseq, max_len);

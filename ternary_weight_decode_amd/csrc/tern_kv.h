@@ -8,6 +8,7 @@
 namespace tern {
 
 constexpr int kKvBlock = 64;   // tokens per cache block: one scale for each block, head and side
+constexpr int kKvRoles = 5;    // workgroups of an append for each touched block and head, at most
 
 struct KvCache {
     int8_t* codes;             // [blocks][heads][2][64*D]

@@ -545,15 +545,18 @@ int i8_kv_read(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, vo
  * the row's q, is not finite.
  *   q bf16 [T] rows (q_stride as above); out bf16 [T][Hq][D]; Hq % heads == 0;
  *   scale finite, window >= 0.
- *   max_len: the longest length that lens will hold (a hint for the split of
- *   long sequences; any length is right, one above max_len slower), > 0.
+ *   max_len: the longest length that lens will hold, > 0; max_rows: the most
+ *   rows that a sequence will have, 0 when not known.  Both are hints for the
+ *   choice of kernels and the split of long sequences: a batch that goes past
+ *   them is slower, and as right.
  *   workspace: i8_kv_attend_workspace_bytes() bytes, 16-byte aligned, NULL when
  *   that is 0; overwritten, so calls that share it must not overlap in time.
  * The sums do not depend on timing: equal calls give equal bytes. */
-int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len);
+int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
+                                     int64_t max_rows);
 int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
-                 int64_t q_stride, float scale, int64_t window, int64_t max_len, uint16_t* out, void* workspace,
-                 void* stream);
+                 int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows, uint16_t* out,
+                 void* workspace, void* stream);
 
 /* ---- launch-configuration introspection (no operation of the method) ----
  *

@@ -150,8 +150,8 @@ def lib():
                                    _p, _p, _p]
         L.i8_kv_read.argtypes = [cache, batch, _i64, _p, _p, ctypes.c_int, _p]
         L.i8_kv_attend_workspace_bytes.restype = _i64
-        L.i8_kv_attend_workspace_bytes.argtypes = [_i64] * 6
-        L.i8_kv_attend.argtypes = [cache, batch, _i64, _p, _i64, _i64, ctypes.c_float, _i64, _i64, _p, _p, _p]
+        L.i8_kv_attend_workspace_bytes.argtypes = [_i64] * 7
+        L.i8_kv_attend.argtypes = [cache, batch, _i64, _p, _i64, _i64, ctypes.c_float, _i64, _i64, _i64, _p, _p, _p]
         for name in _INT_STATUS:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -986,23 +986,26 @@ def i8_kv_read(cache, batch, tokens: int, dtype=None, k_out=None, v_out=None, st
     return k_out, v_out
 
 
-def i8_kv_attend_workspace_bytes(tokens: int, hq: int, heads: int, d: int, nseq: int, max_len: int) -> int:
-    return int(lib().i8_kv_attend_workspace_bytes(tokens, hq, heads, d, nseq, max_len))
+def i8_kv_attend_workspace_bytes(tokens: int, hq: int, heads: int, d: int, nseq: int, max_len: int,
+                                 max_rows: int = 0) -> int:
+    return int(lib().i8_kv_attend_workspace_bytes(tokens, hq, heads, d, nseq, max_len, max_rows))
 
 
-def i8_kv_attend_workspace(cache, batch, tokens: int, hq: int, max_len=None):
+def i8_kv_attend_workspace(cache, batch, tokens: int, hq: int, max_len=None, max_rows: int = 0):
     """A workspace for i8_kv_attend of `tokens` rows of hq heads (None where none is needed)."""
     nbytes = i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, cache.d, batch.nseq,
-                                          max_len or max(1, batch.width * KV_BLOCK))
+                                          max_len or max(1, batch.width * KV_BLOCK), max_rows)
     if nbytes < 0:
         _check("i8_kv_attend_workspace_bytes", 2)
     return _torch.empty(nbytes, dtype=_torch.uint8, device=cache.device) if nbytes else None
 
 
-def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, out=None, workspace=None, stream=None):
+def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, max_rows: int = 0, out=None,
+                 workspace=None, stream=None):
     """Attention of q bf16 [T, Hq, D] over the batch's cached tokens, causal, with a sliding window
-    where window > 0 -> bf16 [T, Hq, D].  scale: D ** -0.5 by default.  max_len: the longest length
-    that batch.lens will hold (default: what the table can hold)."""
+    where window > 0 -> bf16 [T, Hq, D].  scale: D ** -0.5 by default.  Hints: max_len, the longest
+    length that batch.lens will hold (default: what the table can hold), and max_rows, the most rows
+    that a sequence will have (0: not known)."""
     device, d = _kv_device(cache, batch), cache.d
     tokens, hq, stride = _rows(q, "q", _torch.bfloat16, device, None, d, None)
     if max_len is None:
@@ -1011,7 +1014,7 @@ def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, out
         out = _new((tokens, hq, d), _torch.bfloat16, device, stream)
     else:
         _vec(out, "out", _torch.bfloat16, (tokens, hq, d), device)
-    need = lib().i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len)
+    need = lib().i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len, max_rows)
     if workspace is None:
         if need > 0:
             workspace = _new(need, _torch.uint8, device, stream)
@@ -1019,5 +1022,5 @@ def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, out
             workspace.numel() * workspace.element_size() < need:
         raise RuntimeError(f"workspace must be a contiguous tensor of at least {need} bytes on device {device}")
     _call("i8_kv_attend", device, stream, cache.ref, batch.ref, tokens, q.data_ptr(), hq, stride,
-          d ** -0.5 if scale is None else scale, window, max_len, out.data_ptr(), _addr(workspace))
+          d ** -0.5 if scale is None else scale, window, max_len, max_rows, out.data_ptr(), _addr(workspace))
     return out

@@ -736,24 +736,26 @@ int i8_kv_read(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, vo
                                        out_type == TERN_BF16, (hipStream_t)stream));
 }
 
-int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
+int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
+                                     int64_t max_rows)
 {
     if (kv_bad_d(D) || T < 0 || T > kKvMaxRows || heads < 1 || heads > kKvMaxHeads || Hq < 1 || Hq > kKvMaxHeads ||
         Hq % heads != 0 || T * Hq > kKvMaxPairs || nseq < 0 || nseq > kKvMaxRows || max_len < 1 ||
-        max_len > INT32_MAX)
+        max_len > INT32_MAX || max_rows < 0)
         return -1;
     if (T == 0 || nseq == 0) return 0;
-    return tern::kv_attend_workspace_bytes(T, Hq, heads, D, nseq, max_len);
+    return tern::kv_attend_workspace_bytes(T, Hq, heads, D, nseq, max_len, max_rows);
 }
 
 int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
-                 int64_t q_stride, float scale, int64_t window, int64_t max_len, uint16_t* out, void* workspace,
-                 void* stream)
+                 int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows, uint16_t* out,
+                 void* workspace, void* stream)
 {
     bool empty = false;
     int rc = kv_check_shape(cache, batch, T, &empty);
     if (rc) return rc;
-    const int64_t need = i8_kv_attend_workspace_bytes(T, Hq, cache->heads, cache->D, batch->nseq, max_len);
+    const int64_t need = i8_kv_attend_workspace_bytes(T, Hq, cache->heads, cache->D, batch->nseq, max_len,
+                                                      max_rows);
     if (need < 0 || window < 0 || !std::isfinite(scale) || kv_bad_stride(Hq, cache->D, q_stride, TERN_BF16))
         return TERN_E_SHAPE;
     if (empty) return TERN_OK;
@@ -762,7 +764,7 @@ int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, 
     if (!aligned16(q) || !aligned16(out) || (need > 0 && !aligned16(workspace))) return TERN_E_ALIGN;
     if ((rc = check_device())) return rc;
     return finish(tern::launch_kv_attend(kv_cache(cache), kv_batch(batch, T), cache->D, q, Hq, q_stride, scale,
-                                         window, max_len, out, workspace, (hipStream_t)stream));
+                                         window, max_len, max_rows, out, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -95,9 +95,24 @@ __device__ __forceinline__ bool att_tile(const KvBatch& b, int number, int G, in
     return true;
 }
 
+struct AttArgs {
+    const uint16_t* q;
+    uint16_t* out;
+    float* part;               // [workgroups][2][COLS][D] unnormalised sums, then their (max, sum)
+    float2* stat;
+    uint32_t* start;           // [nseq] where each sequence starts in the line, then the total
+    int64_t q_stride;
+    int window;
+    float scale;
+    int G;
+    int groups;                // workgroups that share the line; 0: one workgroup for each unit
+    int min_cols, max_cols;    // the sequences of this launch, by their columns
+    int by_sequence;           // the joining kernel goes by sequences and columns, not by rows
+};
+
 // A sequence's share of the line: its tiles, and the blocks that each of its
 // units takes there (padded; no tile of the sequence sees more).  None for a
-// sequence without rows.
+// sequence without rows or of another launch.
 struct AttShare {
     uint32_t tiles, len;
 };
@@ -118,7 +133,7 @@ __device__ __forceinline__ void att_uniform(AttTile& a)
 }
 
 template <int COLS>
-__device__ __forceinline__ AttShare att_share(const KvBatch& b, int i, int G, int window, KvSeq& s)
+__device__ __forceinline__ AttShare att_share(const KvBatch& b, int i, const AttArgs& a, KvSeq& s)
 {
     s.i = i;
     s.t0 = b.cu[i];
@@ -128,29 +143,18 @@ __device__ __forceinline__ AttShare att_share(const KvBatch& b, int i, int G, in
     constexpr uint32_t kTurn = att_turn<COLS>();
     AttShare r = {0, kTurn};
     if (s.t0 < 0 || t1 > b.T || s.n <= 0) return r;
-    r.tiles = (uint32_t)(((int64_t)s.n * G + COLS - 1) / COLS);
+    const int64_t cols = (int64_t)s.n * a.G;
+    if (cols < a.min_cols || cols > a.max_cols) return r;
+    r.tiles = (uint32_t)((cols + COLS - 1) / COLS);
     const int last = att_last(s.p0 + s.n - 1, att_limit(b));
     uint32_t blocks = last < 0 ? 1 : last / kKvBlock + 1;
-    if (window > 0) {          // a tile spans window + its rows - 1 keys
-        const uint32_t most = ((uint32_t)window + COLS / G + 1) / kKvBlock + 2;
+    if (a.window > 0) {        // a tile spans window + its rows - 1 keys
+        const uint32_t most = ((uint32_t)a.window + COLS / a.G + 1) / kKvBlock + 2;
         blocks = blocks < most ? blocks : most;
     }
     r.len = (blocks + kTurn - 1) / kTurn * kTurn;
     return r;
 }
-
-struct AttArgs {
-    const uint16_t* q;
-    uint16_t* out;
-    float* part;               // [workgroups][2][COLS][D] unnormalised sums, then their (max, sum)
-    float2* stat;
-    uint32_t* start;           // [nseq] where each sequence starts in the line, then the total
-    int64_t q_stride;
-    int window;
-    float scale;
-    int G;
-    int groups;                // workgroups that share the line; 0: one workgroup for each unit
-};
 
 // blocks of the line for each of `groups` workgroups
 template <int COLS>
@@ -770,7 +774,7 @@ __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_at
         const int run = (b.nseq + 63) / 64;
         uint32_t mine = 0;
         for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
-            r = att_share<COLS>(b, k, a.G, a.window, tile.s);
+            r = att_share<COLS>(b, k, a, tile.s);
             mine += r.tiles * c.heads * r.len;
         }
         uint32_t upto = mine;
@@ -784,7 +788,7 @@ __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_at
             uint32_t from = upto - mine;
             for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
                 KvSeq s;
-                const AttShare o = att_share<COLS>(b, k, a.G, a.window, s);
+                const AttShare o = att_share<COLS>(b, k, a, s);
                 a.start[k] = from;
                 from += o.tiles * c.heads * o.len;
             }
@@ -799,7 +803,7 @@ __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_at
         const int owner = b.nseq > 1 ? __popcll(__ballot(upto <= x)) : 0;
         at = __builtin_amdgcn_readlane(upto - mine, owner);
         i = uni(owner * run);
-        r = att_share<COLS>(b, i, a.G, a.window, tile.s);
+        r = att_share<COLS>(b, i, a, tile.s);
         r = {(uint32_t)uni(r.tiles), (uint32_t)uni(r.len)};
     }
     while (true) {
@@ -812,13 +816,15 @@ __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_at
             const uint32_t item = (gridDim.x - 1 - blockIdx.x) / c.heads;
             int64_t local;
             any = kv_find(b, item, a.G, COLS, 1, tile.s, local);
+            const int64_t cols = any ? (int64_t)tile.s.n * a.G : 0;
+            any = any && cols >= a.min_cols && cols <= a.max_cols;
             number = any ? uni((int)local) : 0;
             h = gridDim.x - 1 - blockIdx.x - item * c.heads;
             x = x1;
         } else {
             while (x - at >= r.tiles * c.heads * r.len) {     // ends: x < total
                 at += r.tiles * c.heads * r.len;
-                r = att_share<COLS>(b, ++i, a.G, a.window, tile.s);
+                r = att_share<COLS>(b, ++i, a, tile.s);
                 r = {(uint32_t)uni(r.tiles), (uint32_t)uni(r.len)};
             }
             const uint32_t unit = (x - at) / r.len, from = x - at - unit * r.len;
@@ -855,15 +861,29 @@ __global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel
     __shared__ float so[JW][D];
     const int lane = threadIdx.x & 63, wave = JW == 1 ? 0 : threadIdx.x >> 6;
     const uint32_t Hq = c.heads * a.G, id = blockIdx.x * kRows + (JW == 1 ? threadIdx.x >> 6 : 0);
-    const uint32_t t = id / Hq;
-    const int hq = id - t * Hq, h = hq / a.G;
     AttTile tile;
-    int64_t j;
-    if (t >= (uint32_t)b.T || !kv_find(b, t, 1, 1, 0, tile.s, j) || j >= tile.s.n) return;
-    const AttShare r = att_share<COLS>(b, tile.s.i, a.G, a.window, tile.s);
+    AttShare r;
+    int64_t cc;                // column of the sequence
+    int h;
+    if (a.by_sequence) {       // id: sequence, head, column
+        const uint32_t i = id / (c.heads * a.max_cols), rest = id - i * c.heads * a.max_cols;
+        if (i >= (uint32_t)b.nseq) return;
+        r = att_share<COLS>(b, i, a, tile.s);
+        h = rest / a.max_cols;
+        cc = rest - h * a.max_cols;
+        if (cc >= (int64_t)tile.s.n * a.G) return;
+    } else {                   // id: row, query head
+        const uint32_t t = id / Hq;
+        const int hq = id - t * Hq;
+        int64_t j;
+        if (t >= (uint32_t)b.T || !kv_find(b, t, 1, 1, 0, tile.s, j) || j >= tile.s.n) return;
+        r = att_share<COLS>(b, tile.s.i, a, tile.s);
+        h = hq / a.G;
+        cc = j * a.G + (hq - h * a.G);
+    }
+    if (r.tiles == 0) return;
     const bool alone = b.nseq == 1;          // one load's latency less
     const uint32_t total = alone ? r.tiles * c.heads * r.len : a.start[b.nseq], start = alone ? 0 : a.start[tile.s.i];
-    const int64_t cc = j * a.G + (hq - h * a.G);
     const int number = (int)(cc / COLS), col = (int)(cc % COLS);
     if (!att_tile<COLS>(b, number, a.G, a.window, tile)) return;
     const uint32_t per = att_stretch<COLS>(total, a.groups);
@@ -901,7 +921,8 @@ __global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel
             for (int u = 0; u < D / 64; ++u) o[u] = seg + wave + JW * k < used ? fmaf(x[k][u], f, o[u]) : o[u];
         }
     }
-    uint16_t* dst = a.out + (int64_t)id * D;
+    const int row = (int)(cc / a.G);
+    uint16_t* dst = a.out + ((int64_t)(tile.s.t0 + row) * Hq + h * a.G + (cc - (int64_t)row * a.G)) * D;
     if constexpr (JW == 1) {
 #pragma unroll
         for (int u = 0; u < D / 64; ++u) dst[u * 64 + lane] = f32_to_bf16(sum == 0.0f ? 0.0f : o[u] / sum);
@@ -927,12 +948,20 @@ __global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel
     }
 }
 
-// How a call is cut: columns per workgroup, tiles at most, workgroups that
-// share the line (0: one for each unit, no second kernel).
-struct AttPlan {
-    int cols, groups;
+// How a launch is cut: columns per workgroup, tiles at most, workgroups that
+// share the line (0: one for each unit, no second kernel), which sequences.
+struct AttPart {
+    int cols, groups, min_cols, max_cols;
     int64_t items;
     int64_t part_floats, stats, starts;
+    int64_t bytes() const { return part_floats * 4 + stats * 8 + (starts + 3) / 4 * 16; }
+};
+
+// A call is one launch, or two where a batch may hold prompts beside single
+// tokens: only the device knows the rows of each sequence.
+struct AttPlan {
+    AttPart part[2];
+    int parts;
 };
 
 constexpr int64_t kAttGroups = 768;          // three workgroups a CU: what registers allow on the int8 path
@@ -947,40 +976,69 @@ constexpr int64_t kAttShared = 4096;         // (block, head) pairs from which t
 constexpr int64_t kAttTileCols = 128;        // columns a sequence from which 256-column tiles pay off,
 constexpr int64_t kAttSmall = 24576;         // unless (unit of 16 columns, block) pairs are at most so many
 
-static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
+constexpr int64_t kAttMixed = 512;           // columns that one of several sequences may have: then both paths
+
+static void att_cut(AttPart& p, int64_t cols, int64_t heads, int64_t D, int64_t nseq, int64_t blocks, bool line)
 {
-    AttPlan p{};
-    const int64_t cols = T * (Hq / heads), blocks = (max_len + kKvBlock - 1) / kKvBlock;
-    if (cols > kAttTileCols * nseq && (cols / 16 + nseq) * heads * blocks > kAttSmall) p.cols = 256;
-    else if (cols <= 16 * nseq || nseq * heads * blocks < kAttShared) p.cols = 16;
-    else p.cols = cols <= 32 * nseq ? 32 : 64;
     p.items = cols / p.cols + nseq;
     const int64_t units = p.items * heads, most = p.cols == 256 ? kTileGroups : 2 * kAttGroups;
-    if (blocks <= kAttWholeBlocks || units >= most) return p;
+    if (!line && (blocks <= kAttWholeBlocks || units >= most)) return;
     const int64_t turn = p.cols <= 64 ? 64 / p.cols : 1, turns = (blocks + turn - 1) / turn;
     const int64_t groups = p.cols == 256 ? kTileGroups : kAttGroups;
     p.groups = (int)(units > groups / turns ? groups : units * turns);
     p.stats = (int64_t)p.groups * 2 * p.cols;
     p.part_floats = p.stats * D;
     p.starts = nseq + 1;
+}
+
+static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
+                        int64_t max_rows)
+{
+    AttPlan p{};
+    const int64_t G = Hq / heads, cols = T * G, blocks = (max_len + kKvBlock - 1) / kKvBlock;
+    const bool small = (cols / 16 + nseq) * heads * blocks <= kAttSmall;
+    // the most columns that a sequence may have; not told, a batch of few rows
+    // each is taken for one of drafts
+    const int64_t rows = nseq == 1 ? T : max_rows > 0 ? max_rows : T > 16 * nseq ? T - nseq + 1 : 16;
+    const int64_t most = (rows < T ? rows : T) * G;
+    p.parts = 1;
+    for (AttPart& q : p.part) q.max_cols = INT32_MAX;
+    if (!small && nseq > 1 && most > kAttMixed) {
+        p.parts = 2;
+        p.part[0].cols = 256;
+        p.part[0].min_cols = kAttTileCols + 1;
+        p.part[1].cols = 16;
+        p.part[1].max_cols = kAttTileCols;
+        // the second always as a line: a grid by units would be idle in a batch of prompts
+        att_cut(p.part[0], cols, heads, D, nseq, blocks, false);
+        att_cut(p.part[1], cols, heads, D, nseq, blocks, true);
+        return p;
+    }
+    if (!small && cols > kAttTileCols * nseq && most > kAttTileCols) p.part[0].cols = 256;
+    else if (cols <= 16 * nseq || nseq * heads * blocks < kAttShared) p.part[0].cols = 16;
+    else p.part[0].cols = cols <= 32 * nseq ? 32 : 64;
+    att_cut(p.part[0], cols, heads, D, nseq, blocks, false);
     return p;
 }
 
-int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
+int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
+                                  int64_t max_rows)
 {
-    const AttPlan p = att_plan(T, Hq, heads, D, nseq, max_len);
-    return p.part_floats * 4 + p.stats * 8 + p.starts * 4;
+    const AttPlan p = att_plan(T, Hq, heads, D, nseq, max_len, max_rows);
+    int64_t bytes = 0;
+    for (int i = 0; i < p.parts; ++i) bytes += p.part[i].bytes();
+    return bytes;
 }
 
 template <int D, int COLS>
-static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, const AttPlan& p,
-                            hipStream_t stream)
+static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, int64_t items, hipStream_t stream)
 {
-    const int64_t grid = a.groups ? a.groups : p.items * c.heads;
+    const int64_t grid = a.groups ? a.groups : items * c.heads;
     kv_attend_kernel<D, COLS><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.groups == 0) return e;
-    const int64_t rows = (int64_t)b.T * c.heads * a.G;
+    int64_t rows = (int64_t)b.T * c.heads * a.G;
+    if (a.by_sequence) rows = (int64_t)b.nseq * c.heads * a.max_cols;
     // few rows: their parts to many waves
     if (rows <= 256)
         kv_attend_join_kernel<D, COLS, 12><<<(unsigned)rows, 768, 0, stream>>>(c, b, a);
@@ -991,38 +1049,47 @@ static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, c
     return hipGetLastError();
 }
 
-hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
-                            int64_t q_stride, float scale, int64_t window, int64_t max_len, uint16_t* out,
-                            void* workspace, hipStream_t stream)
+template <int D>
+static hipError_t attend_part(const KvCache& c, const KvBatch& b, const AttArgs& a, const AttPart& p,
+                              hipStream_t stream)
 {
-    const AttPlan p = att_plan(b.T, Hq, c.heads, D, b.nseq, max_len);
-    AttArgs a{};
-    a.q = q;
-    a.out = out;
-    a.part = (float*)workspace;
-    a.stat = (float2*)(a.part + p.part_floats);
-    a.start = (uint32_t*)(a.stat + p.stats);
-    a.q_stride = q_stride;
-    a.window = window < INT32_MAX ? (int)window : 0;      // one that nothing is as far as
-    a.scale = scale;
-    a.G = (int)(Hq / c.heads);
-    // the line is counted in 32 bits; a batch that could pass that has units enough
-    const int64_t line = p.items * c.heads * ((int64_t)b.table_width + kAttWaves);
-    a.groups = line < (1ll << 31) ? p.groups : 0;
-    if (D == 128) {
-        switch (p.cols) {
-        case 16: return attend<128, 16>(c, b, a, p, stream);
-        case 32: return attend<128, 32>(c, b, a, p, stream);
-        case 64: return attend<128, 64>(c, b, a, p, stream);
-        default: return attend<128, 256>(c, b, a, p, stream);
-        }
-    }
     switch (p.cols) {
-    case 16: return attend<64, 16>(c, b, a, p, stream);
-    case 32: return attend<64, 32>(c, b, a, p, stream);
-    case 64: return attend<64, 64>(c, b, a, p, stream);
-    default: return attend<64, 256>(c, b, a, p, stream);
+    case 16: return attend<D, 16>(c, b, a, p.items, stream);
+    case 32: return attend<D, 32>(c, b, a, p.items, stream);
+    case 64: return attend<D, 64>(c, b, a, p.items, stream);
+    default: return attend<D, 256>(c, b, a, p.items, stream);
     }
+}
+
+hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
+                            int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows,
+                            uint16_t* out, void* workspace, hipStream_t stream)
+{
+    const AttPlan plan = att_plan(b.T, Hq, c.heads, D, b.nseq, max_len, max_rows);
+    uint8_t* ws = (uint8_t*)workspace;
+    for (int i = 0; i < plan.parts; ++i) {
+        const AttPart& p = plan.part[i];
+        AttArgs a{};
+        a.q = q;
+        a.out = out;
+        a.part = (float*)ws;
+        a.stat = (float2*)(a.part + p.part_floats);
+        a.start = (uint32_t*)(a.stat + p.stats);
+        ws += p.bytes();
+        a.q_stride = q_stride;
+        a.window = window < INT32_MAX ? (int)window : 0;      // one that nothing is as far as
+        a.scale = scale;
+        a.G = (int)(Hq / c.heads);
+        a.min_cols = p.min_cols;
+        a.max_cols = p.max_cols;
+        a.by_sequence = p.max_cols < INT32_MAX && (int64_t)b.nseq * p.max_cols < (int64_t)b.T * a.G;
+        // the line is counted in 32 bits; a batch that could pass that has units enough
+        const int64_t line = p.items * c.heads * ((int64_t)b.table_width + kAttWaves);
+        a.groups = line < (1ll << 31) ? p.groups : 0;
+        const hipError_t e = D == 128 ? attend_part<128>(c, b, a, p, stream) : attend_part<64>(c, b, a, p, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace tern

@@ -422,20 +422,22 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvBatch b, Qk
 // is 16 dims of one token; a chunk of V is one dim of 16 tokens, and four
 // neighbouring lanes exchange theirs so that each has four dims of four
 // tokens.
+// 4 N codes as values, in stores of 16 bytes where there are as many
 template <int N, typename TO>
 __device__ __forceinline__ void store_codes(TO* p, const uint32_t* w, float scale)
 {
+    constexpr int kAt = sizeof(TO) == 2 && N > 1 ? 8 : 4;
     float x[4 * N];
 #pragma unroll
     for (int i = 0; i < 4 * N; ++i) x[i] = (float)(int8_t)(w[i / 4] >> 8 * (i % 4)) * scale;
 #pragma unroll
-    for (int i = 0; i < N; ++i) store_run<4>(p + 4 * i, x + 4 * i);
+    for (int i = 0; i < 4 * N; i += kAt) store_run<kAt>(p + i, x + i);
 }
 
 template <int D, typename TO>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, KvBatch b, TO* k_out, TO* v_out)
 {
-    constexpr int S = D / 64, kChunks = kKvBlock * D / 16;
+    constexpr int S = D / 64;                                      // chunks of each side per thread
     const int h = blockIdx.x % c.heads;
     KvSeq s;
     int64_t local;
@@ -445,27 +447,28 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, KvBatch b, TO* 
     const bool there = phys >= 0;
     const int64_t unit = (there ? phys : 0) * c.heads + h;
     const float sk = there ? c.scales[unit * 2] : 0.0f, sv = there ? c.scales[unit * 2 + 1] : 0.0f;
-    const int8_t* kc = c.codes + unit * 2 * (kKvBlock * D);
+    const u32x4* kc = (const u32x4*)(c.codes + unit * 2 * (kKvBlock * D));
     const int64_t stride = (int64_t)c.heads * D;
     TO* const k_row = k_out + w.row * stride + (int64_t)h * D;     // of the block's slot w.slot
     TO* const v_row = v_out + w.row * stride + (int64_t)h * D;
-    u32x4 kx[kChunks / 256], vx[kChunks / 256];
+    // K: a wave has 64 dims of 16 tokens; V: 64 dims of a quarter of the tokens
+    // (16 t + 4 wave + i), so that either stores 64 dims of a row side by side
+    const int wave = threadIdx.x >> 6, r = threadIdx.x & 15, quarter = threadIdx.x >> 4 & 3, quad = threadIdx.x & 3;
+    u32x4 kx[S], vx[S];
 #pragma unroll
-    for (int n = 0; n < kChunks / 256; ++n) {
+    for (int n = 0; n < S; ++n) {
         kx[n] = vx[n] = u32x4{0, 0, 0, 0};
         if (there) {
-            kx[n] = *(const u32x4*)(kc + (threadIdx.x + 256 * n) * 16);
-            vx[n] = *(const u32x4*)(kc + kKvBlock * D + (threadIdx.x + 256 * n) * 16);
+            kx[n] = kc[threadIdx.x + 256 * n];
+            vx[n] = kc[kKvBlock * D / 16 + ((4 * n + quarter) * 4 + wave) * 16 + r];
         }
     }
-    const int quad = threadIdx.x & 3;
 #pragma unroll
-    for (int n = 0; n < kChunks / 256; ++n) {
-        const int i = threadIdx.x + 256 * n, r = i & 15, g = i >> 4 & 3, hi = i >> 6;
-        const int kt = hi / S * 16 + r - w.slot;
+    for (int n = 0; n < S; ++n) {
+        const int hi = wave + 4 * n, kt = hi / S * 16 + r - w.slot;
         if (kt >= 0 && kt < w.n) {
             const uint32_t x[4] = {kx[n][0], kx[n][1], kx[n][2], kx[n][3]};
-            store_codes<4>(k_row + kt * stride + hi % S * 64 + g * 16, x, sk);
+            store_codes<4>(k_row + kt * stride + hi % S * 64 + quarter * 16, x, sk);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -476,8 +479,9 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, KvBatch b, TO* 
             const uint32_t u = __shfl_xor(z, 2);
             const uint32_t word = quad & 2 ? __builtin_amdgcn_perm(z, u, 0x07060302u)
                                            : __builtin_amdgcn_perm(u, z, 0x05040100u);
-            const int vt = 16 * t + 4 * g + quad - w.slot;
-            if (vt >= 0 && vt < w.n) store_codes<1>(v_row + vt * stride + hi * 16 + (r & ~3), &word, sv);
+            const int vt = 16 * t + 4 * wave + quad - w.slot;
+            if (vt >= 0 && vt < w.n)
+                store_codes<1>(v_row + vt * stride + (4 * n + quarter) * 16 + (r & ~3), &word, sv);
         }
     }
 }

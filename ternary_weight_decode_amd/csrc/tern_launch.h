@@ -140,10 +140,11 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, int64_t D, const
                             int64_t v_stride, bool in_bf16, const int32_t* pos, uint16_t* q_out, hipStream_t stream);
 hipError_t launch_kv_read(const KvCache& c, const KvBatch& b, int64_t D, void* k_out, void* v_out, bool out_bf16,
                           hipStream_t stream);
-int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len);
+int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
+                                  int64_t max_rows);
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
-                            int64_t q_stride, float scale, int64_t window, int64_t max_len, uint16_t* out,
-                            void* workspace, hipStream_t stream);
+                            int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows,
+                            uint16_t* out, void* workspace, hipStream_t stream);
 
 // ---- matrix-core throughput probe (measurement aid) ----
 double mfma_peak_ops(int kind, int64_t iters, int64_t grid);

@@ -281,13 +281,14 @@ def test_read(tw, d, heads, new, prev):
 
 
 # ---- attention ----
-def check_attend(tw, s, q, window=0, scale=None, max_len=None):
+def check_attend(tw, s, q, window=0, scale=None, max_len=None, max_rows=0):
     """Within half a bf16 step of the exact value and the oracle's bound for the narrower operands;
     bf16's rounding alone is at most 2^-8 / sqrt(3) = 2^-8.79 of the value in the mean, so the root mean
     square of all errors is asked to stay below 2^-8 of the output's."""
     import torch
     c, b = s.device()
-    got = host(tw.i8_kv_attend(c, b, dev(q, torch.bfloat16), scale=scale, window=window, max_len=max_len))
+    got = host(tw.i8_kv_attend(c, b, dev(q, torch.bfloat16), scale=scale, window=window, max_len=max_len,
+                               max_rows=max_rows))
     want, bound = kv.attend(kv.Cache(s.codes, s.scales), s.cu, s.lens, s.table, q,
                             s.d ** -0.5 if scale is None else scale, window)
     rows = slice(0, int(s.cu[-1]))
@@ -336,6 +337,17 @@ def test_attend_long(tw, new, max_len):
     """Long enough to be split; max_len is a hint, right or wrong."""
     s = Case(tw, 53, 128, 1, [new, new], [9001, 1200])
     check_attend(tw, s, queries(s, 4), max_len=max_len)
+
+
+@pytest.mark.parametrize("new, prev, max_rows", [
+    ([200, 1, 1, 150, 3, 0, 32, 33], [900, 2000, 5, 0, 1300, 3, 700, 40], 0),      # both paths, either side of 128 columns
+    ([1, 1, 400], [3000, 70, 1200], 0), ([1, 1, 400], [3000, 70, 1200], 400), ([1, 1, 400], [3000, 70, 1200], 1),
+    ([300, 300], [1200, 64], 0), ([2] * 20 + [140], [1500] * 20 + [2], 140),
+])
+@pytest.mark.parametrize("d, heads, hq, window", [(128, 8, 32, 0), (64, 4, 16, 500)])
+def test_attend_prompts_beside_single_tokens(tw, new, prev, max_rows, d, heads, hq, window):
+    s = Case(tw, 109 + len(new), d, heads, new, prev)
+    check_attend(tw, s, queries(s, hq), window=window, max_rows=max_rows)
 
 
 @pytest.mark.parametrize("new", [1, 3, 50])

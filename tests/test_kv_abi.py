@@ -39,9 +39,9 @@ def read(c=None, b=None, T=1, ko=P, vo=P, ot=BF16):
     return tw.lib().i8_kv_read(ctypes.byref(c or cache()), ctypes.byref(b or batch()), T, ko, vo, ot, None)
 
 
-def attend(c=None, b=None, T=1, q=P, hq=4, qs=512, scale=0.1, window=0, max_len=256, out=P, ws=P):
+def attend(c=None, b=None, T=1, q=P, hq=4, qs=512, scale=0.1, window=0, max_len=256, max_rows=0, out=P, ws=P):
     return tw.lib().i8_kv_attend(ctypes.byref(c or cache()), ctypes.byref(b or batch()), T, q, hq, qs, scale, window,
-                                 max_len, out, ws, None)
+                                 max_len, max_rows, out, ws, None)
 
 
 @pytest.mark.parametrize("kw, rc", [
@@ -85,6 +85,7 @@ def test_read_refuses(kw, rc):
 @pytest.mark.parametrize("kw, rc", [
     (dict(c=cache(d=256)), E_SHAPE), (dict(hq=5), E_SHAPE), (dict(hq=0), E_SHAPE), (dict(qs=504), E_SHAPE),
     (dict(qs=516), E_SHAPE), (dict(window=-1), E_SHAPE), (dict(max_len=0), E_SHAPE),
+    (dict(max_rows=-1), E_SHAPE),
     (dict(scale=float("nan")), E_SHAPE), (dict(scale=float("inf")), E_SHAPE), (dict(T=-1), E_SHAPE),
     (dict(q=None), E_NULL), (dict(out=None), E_NULL), (dict(q=ODD), E_ALIGN), (dict(out=ODD), E_ALIGN),
     (dict(b=batch(lens=P + 1)), E_ALIGN), (dict(T=0, q=None), E_OK), (dict(b=batch(nseq=0)), E_OK),
@@ -94,8 +95,13 @@ def test_attend_refuses(kw, rc):
 
 
 def test_workspace_sizes():
-    ws = tw.i8_kv_attend_workspace_bytes
+    ws = tw.i8_kv_attend_workspace_bytes        # max_rows 0: not known
     assert ws(1, 4, 3, 128, 1, 64) == -1 and ws(1, 4, 2, 96, 1, 64) == -1 and ws(-1, 4, 2, 128, 1, 64) == -1
     assert ws(1, 4, 2, 128, 1, 0) == -1 and ws(1, 0, 2, 128, 1, 64) == -1
     assert ws(0, 4, 2, 128, 1, 64) == 0 and ws(5, 4, 2, 128, 0, 64) == 0
-    assert ws(1, 32, 8, 128, 1, 40960) >= 0
+    assert ws(1, 4, 2, 128, 1, 64, -1) == -1 and ws(1 << 24, 4, 2, 128, 1, 64) == -1
+    assert ws(1, 32, 8, 128, 1, 40960) > 0 and ws(1, 32, 8, 128, 1, 512) == 0
+    # a batch that may hold prompts beside single tokens works in two launches, told otherwise in one
+    assert ws(2111, 32, 8, 128, 64, 8192) > ws(2111, 32, 8, 128, 64, 8192, 16)
+    # the split is bounded, whatever the hint
+    assert ws(4096, 32, 8, 128, 4096, 10 ** 6) < 1 << 30

@@ -339,6 +339,89 @@ def test_attend_long(tw, new, max_len):
     check_attend(tw, s, queries(s, 4), max_len=max_len)
 
 
+@pytest.mark.parametrize("seqs, rows", [(70, 1), (130, 1), (70, 5)])
+def test_attend_many_long_sequences(tw, seqs, rows):
+    """More sequences than lanes, long enough to be split, some without rows."""
+    s = Case(tw, 113 + seqs, 64, 1, [rows if i % 7 else 0 for i in range(seqs)], [(i * 311) % 2500 for i in range(seqs)])
+    check_attend(tw, s, queries(s, 2))
+
+
+@pytest.mark.parametrize("new", [1, 5, 150])
+def test_rows_in_front_of_the_first_sequence(tw, new):
+    """cu need not start at 0: rows in front of cu[0] are neither read nor written."""
+    import torch
+    s = Case(tw, 127, 64, 2, [new, new], [1200, 3])
+    q = queries(s, 4)
+    c, b = s.device()
+    want = host(tw.i8_kv_attend(c, b, dev(q, torch.bfloat16)))
+    late = tw.I8KvBatch(b.cu + 3, b.lens, b.table)
+    pad = torch.full((3, 4, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out = torch.full((s.tokens + 3, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    tw.i8_kv_attend(c, late, torch.cat([pad, dev(q, torch.bfloat16)]), out=out)
+    assert np.array_equal(host(out[3:]), want) and np.all(host(out[:3]) == 9)
+    k = dev(s.rng.normal(size=(s.tokens, 2, 64)).astype(np.float32))
+    other = tw.I8KvCache(codes=c.codes.clone(), scales=c.scales.clone())
+    tw.i8_kv_append(c, b, tw.QkTransform(64), k, k)
+    tw.i8_kv_append(other, late, tw.QkTransform(64), torch.cat([pad[:, :2].float(), k]),
+                    torch.cat([pad[:, :2].float(), k]))
+    assert torch.equal(c.codes, other.codes) and torch.equal(c.scales, other.scales)
+
+
+def test_one_workspace_for_calls_in_turn(tw):
+    """A workspace carries nothing from call to call: different batches through one, and through graphs
+    that share it, give what they give alone."""
+    import torch
+    cases = [Case(tw, 131 + i, 128, 2, new, prev) for i, (new, prev) in
+             enumerate([([1], [5000]), ([1, 3, 200], [3000, 10, 1500]), ([12], [2000]), ([400], [900])])]
+    parts = [(*s.device(), dev(queries(s, 8), torch.bfloat16)) for s in cases]
+    alone = [tw.i8_kv_attend(*p) for p in parts]
+    sizes = [tw.i8_kv_attend_workspace(c, b, len(q), 8) for c, b, q in parts]
+    ws = torch.full((max(w.numel() for w in sizes if w is not None),), 255, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(a) for a in alone]
+    graphs = []
+    for (c, b, q), out in zip(parts, outs):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            tw.i8_kv_attend(c, b, q, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tw.i8_kv_attend(c, b, q, out=out, workspace=ws)
+        graphs.append(g)
+    for order in ((0, 1, 2, 3), (3, 1, 0, 2), (2, 2, 1, 0)):
+        for i in order:
+            outs[i].zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i], alone[i])
+            assert torch.equal(tw.i8_kv_attend(*parts[i], workspace=ws), alone[i])
+
+
+def test_calls_overlap_on_two_streams(tw):
+    """Appends to two caches and attention over them, on two streams at once."""
+    import torch
+    s = [Case(tw, 137 + i, 128, 2, [33, 1], [1000, 40 + i]) for i in range(2)]
+    parts = [x.device() for x in s]
+    k = [dev(x.rng.normal(size=(x.tokens, 2, 128)).astype(np.float32)) for x in s]
+    q = [dev(queries(x, 8), torch.bfloat16) for x in s]
+    f = tw.QkTransform(128)
+    want = []
+    for i in range(2):
+        c = tw.I8KvCache(codes=parts[i][0].codes.clone(), scales=parts[i][0].scales.clone())
+        tw.i8_kv_append(c, parts[i][1], f, k[i], k[i])
+        want.append(tw.i8_kv_attend(c, parts[i][1], q[i]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = []
+        for i in range(2):
+            tw.i8_kv_append(*parts[i], f, k[i], k[i], stream=streams[i])
+            got.append(tw.i8_kv_attend(*parts[i], q[i], stream=streams[i]))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("new, prev, max_rows", [
     ([200, 1, 1, 150, 3, 0, 32, 33], [900, 2000, 5, 0, 1300, 3, 700, 40], 0),      # both paths, either side of 128 columns
     ([1, 1, 400], [3000, 70, 1200], 0), ([1, 1, 400], [3000, 70, 1200], 400), ([1, 1, 400], [3000, 70, 1200], 1),

@@ -175,8 +175,8 @@ constexpr uint64_t every()
 }
 
 // blocks [begin, end) of one unit; whole: the result is written, else it is
-// part `slot` of the unit
-template <int D, int X>
+// part `slot` of the unit.  STREAM: codes are read past the caches.
+template <int D, int X, bool STREAM>
 __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b, const AttArgs& a,
                                               const AttTile& tile, int h, int begin, int end, bool whole,
                                               uint32_t slot)
@@ -264,7 +264,9 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
         };
         // the lane's 16 bytes of a KiB behind a scalar address
         const uint32_t own = lane * 16;
-        const auto load = [&](const int8_t* p, int byte) { return *(const u32x4*)(p + byte + own); };
+        const auto load = [&](const int8_t* p, int byte) {
+            return STREAM ? ld_nt16(p + byte + own) : *(const u32x4*)(p + byte + own);
+        };
         u32x4 kr[4][S], vr[U];
         if (todo) {
             const int8_t* p = codes(__builtin_ctzll(todo));
@@ -760,7 +762,7 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
 template <int COLS>
 constexpr int att_threads() { return COLS <= 64 ? 64 * kAttWaves : 64 * kTileWaves; }
 
-template <int D, int COLS>
+template <int D, int COLS, bool STREAM>
 __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_attend_kernel(KvCache c, KvBatch b,
                                                                                             AttArgs a)
 {
@@ -842,7 +844,7 @@ __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_at
             att_uniform(tile);
             end = end < tile.nblk ? end : tile.nblk;
             if (begin < end || begin == 0) {
-                if constexpr (COLS <= 64) attend_blocks<D, COLS / 16>(c, b, a, tile, h, begin, end, whole, slot);
+                if constexpr (COLS <= 64) attend_blocks<D, COLS / 16, STREAM>(c, b, a, tile, h, begin, end, whole, slot);
                 else attend_tile_f16<D>(c, b, a, tile, h, begin, end, whole, slot);
             }
         }
@@ -952,6 +954,7 @@ __global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel
 // share the line (0: one for each unit, no second kernel), which sequences.
 struct AttPart {
     int cols, groups, min_cols, max_cols;
+    bool streams;
     int64_t items;
     int64_t part_floats, stats, starts;
     int64_t bytes() const { return part_floats * 4 + stats * 8 + (starts + 3) / 4 * 16; }
@@ -976,11 +979,16 @@ constexpr int64_t kAttShared = 4096;         // (block, head) pairs from which t
 constexpr int64_t kAttTileCols = 128;        // columns a sequence from which 256-column tiles pay off,
 constexpr int64_t kAttSmall = 24576;         // unless (unit of 16 columns, block) pairs are at most so many
 
+// Caches that pass the last-level cache (256 MB) are read past it: 64 streams
+// up to 16000 (2.1 GB at most, 483 MB) 95 us against 107; below, the plain
+// loads are faster, one stream over 40960 (84 MB) 23.8 us against 25.2.
+constexpr int64_t kAttStream = 256ll << 20;
 constexpr int64_t kAttMixed = 512;           // columns that one of several sequences may have: then both paths
 
 static void att_cut(AttPart& p, int64_t cols, int64_t heads, int64_t D, int64_t nseq, int64_t blocks, bool line)
 {
     p.items = cols / p.cols + nseq;
+    p.streams = nseq * heads * blocks * 2 * kKvBlock * D > kAttStream;
     const int64_t units = p.items * heads, most = p.cols == 256 ? kTileGroups : 2 * kAttGroups;
     if (!line && (blocks <= kAttWholeBlocks || units >= most)) return;
     const int64_t turn = p.cols <= 64 ? 64 / p.cols : 1, turns = (blocks + turn - 1) / turn;
@@ -1031,10 +1039,14 @@ int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t 
 }
 
 template <int D, int COLS>
-static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, int64_t items, hipStream_t stream)
+static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, int64_t items, bool streams,
+                         hipStream_t stream)
 {
     const int64_t grid = a.groups ? a.groups : items * c.heads;
-    kv_attend_kernel<D, COLS><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
+    if (COLS <= 64 && streams)
+        kv_attend_kernel<D, COLS, COLS <= 64><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
+    else
+        kv_attend_kernel<D, COLS, false><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.groups == 0) return e;
     int64_t rows = (int64_t)b.T * c.heads * a.G;
@@ -1054,10 +1066,10 @@ static hipError_t attend_part(const KvCache& c, const KvBatch& b, const AttArgs&
                               hipStream_t stream)
 {
     switch (p.cols) {
-    case 16: return attend<D, 16>(c, b, a, p.items, stream);
-    case 32: return attend<D, 32>(c, b, a, p.items, stream);
-    case 64: return attend<D, 64>(c, b, a, p.items, stream);
-    default: return attend<D, 256>(c, b, a, p.items, stream);
+    case 16: return attend<D, 16>(c, b, a, p.items, p.streams, stream);
+    case 32: return attend<D, 32>(c, b, a, p.items, p.streams, stream);
+    case 64: return attend<D, 64>(c, b, a, p.items, p.streams, stream);
+    default: return attend<D, 256>(c, b, a, p.items, p.streams, stream);
     }
 }
 

@@ -447,7 +447,7 @@ int fv5b_embed(const int8_t* W, const float* S, int64_t V, int64_t K, const int3
  * Cache: a block holds TERN_KV_BLOCK = 64 consecutive tokens of one sequence.
  * For each block, key/value head and side (0 = K, 1 = V) there are 64*D int8
  * codes and one fp32 scale; a cached value is code * scale.
- *   codes  int8 [blocks][heads][2][64*D], scales fp32 [blocks][heads][2]
+ *   codes  int8 [blocks][heads][2][64*D], scales fp32 [blocks][heads][2], >= 0
  *   order of the codes inside a block (an int8 matrix-core operand is one
  *   16-byte load, and softmax weights meet V without leaving their lane):
  *     K of token 16t + r, dim 64s + 16g + b:  (((t*(D/64) + s)*4 + g)*16 + r)*16 + b
@@ -525,8 +525,9 @@ int qk_norm_rope(const tern_qk_transform* f, int64_t T, int64_t D, const void* q
  * With Hq > 0 the rows of q (Hq heads) are normalised and rotated in the same
  * launch into q_out, bf16 [T][Hq][D].  pos NULL takes a token's position in
  * its sequence, else pos int32 [T] is what the rotation uses.
- * A block must not be written by two sequences of one call, nor by two calls
- * that overlap in time; blocks that are only read may be shared.
+ * A block must not be written twice in one call (by two sequences, or through
+ * a table that names it twice for one), nor by two calls that overlap in time;
+ * blocks that are only read may be shared.
  * Hq % heads == 0. */
 int i8_kv_append(const i8_kv_cache* cache, const i8_kv_batch* batch, const tern_qk_transform* f, int64_t T,
                  const void* q, int64_t Hq, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -551,7 +552,11 @@ int i8_kv_read(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, vo
  *   them is slower, and as right.
  *   workspace: i8_kv_attend_workspace_bytes() bytes, 16-byte aligned, NULL when
  *   that is 0; overwritten, so calls that share it must not overlap in time.
- * The sums do not depend on timing: equal calls give equal bytes. */
+ * The sums do not depend on timing: equal calls give equal bytes.
+ * Accuracy, against exact arithmetic over the cached values: the output's
+ * rounding to bf16, and below it what the operands of the matrix cores leave
+ * out: q to 2^-16 of its row's largest value, weights to 2^-16 of the largest
+ * of their 64 tokens (few columns) or to 2^-11 of themselves (prompts). */
 int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
                                      int64_t max_rows);
 int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,

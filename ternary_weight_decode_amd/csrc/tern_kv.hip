@@ -103,7 +103,10 @@ __device__ __forceinline__ void rotate(float* x, int j, bool interleaved, CS cs)
 
 // ---- norm + rotation -------------------------------------------------------
 // One workgroup per token and 16 heads; the token's D/2 angles are computed
-// once per workgroup.
+// once per workgroup.  One token of 32:8 heads takes 2.2 us, an empty kernel
+// 1.95; bound by the rows from a few hundred tokens on: 4096 tokens, fp32 in
+// and bf16 out (126 MB), 19.5 us, 6.5 TB/s (the rows just written come in part
+// from the last-level cache; a plain copy of as many bytes reaches 4.9).
 template <int D, typename TI, typename TO>
 __global__ __launch_bounds__(256) void norm_rope_kernel(QkTransform f, const TI* q, int Hq, int64_t q_stride,
                                                         const TI* k, int Hk, int64_t k_stride, const int32_t* pos,
@@ -141,11 +144,15 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(QkTransform f, const TI*
 // For every (sequence, touched block, key/value head) one workgroup has K and V
 // of all the block's new tokens (the block's scale needs the maximum over
 // them, and nothing else writes the block); the queries of their rows are its
-// too where tokens are few, and in prompts have four workgroups of their own.  Loads are issued before the tokens' angles are computed,
+// too where tokens are few, have a workgroup of their own where those are too
+// few for the card (a single token 5.6 us in a graph, 5.8 in one workgroup), and
+// four in prompts.  Loads are issued before the tokens' angles are computed,
 // once per workgroup, into LDS; up to four K and four V vectors (or four
-// queries) of each 16-lane group wait in registers.  Bound by the rows read;
-// 4131 tokens of 32:8 heads of 128 (144 MB) take 32 us of the 29 that a copy
-// of those bytes takes.
+// queries) of each 16-lane group wait in registers.  Single tokens are bound by
+// the chain cu -> table -> rows -> scale -> codes: 5.6 us for one in a graph,
+// 7.7 for 48, an empty kernel 1.95.  Prompts are bound by the rows read: 4131
+// tokens of 32:8 heads of 128 (144 MB) take 33 us, 4.4 TB/s, where a plain copy
+// of those bytes takes 29 (without the angles' arithmetic 31.5).
 
 // the scale after values of magnitude `top` (bits, so that inf < NaN) join;
 // shift: doublings that the old codes have to follow, 31 where they vanish
@@ -221,11 +228,14 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvBatch b, Qk
     constexpr int E = D / 32;
     __shared__ float2 cs[kKvBlock * D / 2];
     __shared__ uint32_t tops[2][4];
-    const int role = blockIdx.x % roles, h = blockIdx.x / roles % c.heads;
+    // keys and values, with the most to do, start first (the prompt above takes
+    // 37 us with a block's roles side by side)
+    const uint32_t items = gridDim.x / roles, role = blockIdx.x / items, item = blockIdx.x - role * items;
+    const int h = item % c.heads;
     KvSeq s;
     int64_t local;
     KvSpan w;
-    if (!kv_find(b, blockIdx.x / roles / c.heads, 1, kKvBlock, 2, s, local) || !kv_span(s, local, w)) return;
+    if (!kv_find(b, item / c.heads, 1, kKvBlock, 2, s, local) || !kv_span(s, local, w)) return;
     const int j = threadIdx.x & 15, grp = threadIdx.x >> 4;
     const int at = w.block * kKvBlock + w.slot;                    // position of the first token
     const bool inter = f.interleaved != 0;
@@ -258,17 +268,20 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvBatch b, Qk
         }
     }
 
-    // queries: tokens [from, from + nt) of the block's rows, G heads each; a
-    // workgroup of its own takes a slice, one that has K and V too takes all
-    const int slices = roles > 1 ? roles - 1 : 1;
-    const int from = role > 0 ? w.n * (role - 1) / slices : 0;
-    const int nt = (role > 0 ? w.n * role / slices : w.n) - from;
-    const int count = role > 0 || roles == 1 ? nt * G : 0;
+    // queries: tokens [from, from + nt) of the block's rows, heads [qh, qh + qn)
+    // of each: G heads of all tokens, or in prompts all heads of a slice of the
+    // tokens, so that their angles are computed once for all query heads
+    const bool sliced = roles > 2;
+    const int slices = sliced ? (roles - 1) * c.heads : 1, slice = sliced ? h * (roles - 1) + (int)role - 1 : 0;
+    const int from = role > 0 ? w.n * slice / slices : 0;
+    const int nt = (role > 0 ? w.n * (slice + 1) / slices : w.n) - from;
+    const int qh = sliced ? 0 : h * G, qn = sliced ? G * c.heads : G;
+    const int count = role > 0 || roles == 1 ? nt * qn : 0;
     const int64_t row = w.row + from;
     const auto query = [&](int i, auto use) {
-        const int t = i / G;
-        use(t, q + (row + t) * q_stride + ((int64_t)h * G + i - t * G) * D,
-            q_out + ((row + t) * ((int64_t)c.heads * G) + (int64_t)h * G + i - t * G) * D);
+        const int t = i / qn;
+        const int64_t hq = qh + i - t * qn;
+        use(t, q + (row + t) * q_stride + hq * D, q_out + ((row + t) * ((int64_t)c.heads * G) + hq) * D);
     };
     float x[4][2 * E];
     const auto load_queries = [&](int base) {
@@ -421,7 +434,10 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvBatch b, Qk
 // One workgroup per (sequence, block, head); 16 bytes a thread.  A chunk of K
 // is 16 dims of one token; a chunk of V is one dim of 16 tokens, and four
 // neighbouring lanes exchange theirs so that each has four dims of four
-// tokens.
+// tokens.  Bound by what it writes: eight contexts of 2500 to 9000 tokens, 8
+// heads of 128, to bf16 (270 MB, two thirds of them written) take 43 us, 6.2
+// TB/s; 777 tokens 3.4 us.
+
 // 4 N codes as values, in stores of 16 bytes where there are as many
 template <int N, typename TO>
 __device__ __forceinline__ void store_codes(TO* p, const uint32_t* w, float scale)

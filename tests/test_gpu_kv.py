@@ -339,6 +339,17 @@ def test_attend_long(tw, new, max_len):
     check_attend(tw, s, queries(s, 4), max_len=max_len)
 
 
+@pytest.mark.parametrize("new, prev", [
+    ([700], [0]), ([256], [900]), ([257], [63]), ([600], [1500]), ([300, 257, 513], [100, 0, 700]),
+    ([300] * 70, [40] * 70), ([1200], [5]),
+])
+@pytest.mark.parametrize("d, heads, hq, window", [(64, 2, 6, 0), (128, 1, 1, 0), (128, 1, 8, 0), (64, 1, 5, 333)])
+def test_attend_prompts_split_where_a_stretch_ends(tw, new, prev, d, heads, hq, window):
+    # told of long caches, the tiles of all prompts are cut into equal stretches
+    s = Case(tw, 131, d, heads, new, prev)
+    check_attend(tw, s, queries(s, hq), window, max_len=10 ** 6)
+
+
 @pytest.mark.parametrize("seqs, rows", [(70, 1), (130, 1), (70, 5)])
 def test_attend_many_long_sequences(tw, seqs, rows):
     """More sequences than lanes, long enough to be split, some without rows."""

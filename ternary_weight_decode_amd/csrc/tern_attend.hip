@@ -969,30 +969,41 @@ struct AttPlan {
 
 constexpr int64_t kAttGroups = 768;          // three workgroups a CU: what registers allow on the int8 path
 constexpr int64_t kTileGroups = 256;         // one a CU on the fp16 path
-constexpr int64_t kAttWholeBlocks = 16;      // up to here a unit is not split
-// The choice between the paths, measured on eight caches used in turn, 32:8
-// heads of 128 (16 columns a unit / 64 / 256 fp16, us):
-//   17 rows over 4096   21.0 / 22.8 / 24.5     64 rows over 2048   15.6 / 22.9 / 30.9
-//   32 rows over 12345  48.9 / 37.7 / 40.4     256 rows over 4096  47.6 / 48.6 / 42.1
-//   16 x 24 up to 2000  49.9 / 39.7 / 59.9     256 rows over 12345  216 /  104 / 82.9
-constexpr int64_t kAttShared = 4096;         // (block, head) pairs from which tiles of one head share their reads
-constexpr int64_t kAttTileCols = 128;        // columns a sequence from which 256-column tiles pay off,
-constexpr int64_t kAttSmall = 24576;         // unless (unit of 16 columns, block) pairs are at most so many
+
+// The choice of path.  A unit (tile of columns, head) whole in one workgroup
+// needs no second kernel, and the tiles of a head run side by side and share
+// its blocks in L2; split, a long unit does not wait for one workgroup.
+// Measured on caches used in turn, 32:8 heads of 128, lengths evenly spread up
+// to the one given (16 columns whole / 16 split / 64 split / 256 fp16, us):
+//   1 x 1 row up to 1500     10.9 / 11.3 /   -  /   -      up to 3000  17.4 / 12.0 /   -  /   -
+//   16 x 1 up to 3000        20.9 / 22.2 /   -  /   -      up to 4500  29.5 / 27.7 /   -  /   -
+//   64 x 1 up to 3000        42.6 / 45.2 /   -  /   -      up to 16000  194 /  178 /   -  /   -
+//   16 x 7 up to 3000        21.4 / 33.0 / 30.4 / 52.6     up to 4500  29.7 / 39.7 / 36.4 /   -
+//   16 x 16 up to 3000       24.8 / 49.1 / 39.5 / 59.1     up to 12000 80.8 /   -  /   -  / 105
+//   1 x 48 up to 3000        18.5 / 22.0 / 27.1 / 34.3     up to 12000 55.7 / 39.5 / 36.6 / 41.8
+//   8 x 64 up to 3000        32.6 / 79.1 / 51.7 / 54.9     up to 12000  112 /   -  / 122  / 94.2
+//   32 x 128 up to 1500       127 /  -   /  -   / 86.8     up to 12000  672 /   -  /   -  / 447
+// (32 x 128 up to 600: 82.5 with 16 columns, 60.4 with 32, 49.9 with 64.)
+constexpr int64_t kAttWhole = 22;            // blocks up to which a lone unit stays whole
+constexpr int64_t kAttShared = 4096;         // (block, head) pairs from which split tiles of one head share their reads
+constexpr int64_t kAttPair = 2048, kAttQuad = 4096;   // units from which two or four whole tiles share theirs
+constexpr int64_t kAttTileCols = 128;        // columns a sequence from which 256-column tiles are looked at
+constexpr int64_t kAttSmall = 24576;         // (unit of 16 columns, block) pairs up to which split ones do not pay off
+constexpr int64_t kAttMixed = 512;           // columns that one of several sequences may have: then both paths
 
 // Caches that pass the last-level cache (256 MB) are read past it: 64 streams
 // up to 16000 (2.1 GB at most, 483 MB) 95 us against 107; below, the plain
-// loads are faster, one stream over 40960 (84 MB) 23.8 us against 25.2.
+// loads are faster, one stream over 40960 (84 MB) 23.8 us against 25.2.  Not
+// where several tiles read a block (16 x 48 rows up to 12000 217 us against 151).
 constexpr int64_t kAttStream = 256ll << 20;
-constexpr int64_t kAttMixed = 512;           // columns that one of several sequences may have: then both paths
 
-static void att_cut(AttPart& p, int64_t cols, int64_t heads, int64_t D, int64_t nseq, int64_t blocks, bool line)
+static void att_cut(AttPart& p, int64_t cols, int64_t heads, int64_t D, int64_t nseq, int64_t blocks, bool whole)
 {
     p.items = cols / p.cols + nseq;
-    p.streams = nseq * heads * blocks * 2 * kKvBlock * D > kAttStream;
-    const int64_t units = p.items * heads, most = p.cols == 256 ? kTileGroups : 2 * kAttGroups;
-    if (!line && (blocks <= kAttWholeBlocks || units >= most)) return;
+    p.streams = cols <= p.cols * nseq && nseq * heads * blocks * 2 * kKvBlock * D > kAttStream;
+    if (whole) return;
+    const int64_t units = p.items * heads, groups = p.cols == 256 ? kTileGroups : kAttGroups;
     const int64_t turn = p.cols <= 64 ? 64 / p.cols : 1, turns = (blocks + turn - 1) / turn;
-    const int64_t groups = p.cols == 256 ? kTileGroups : kAttGroups;
     p.groups = (int)(units > groups / turns ? groups : units * turns);
     p.stats = (int64_t)p.groups * 2 * p.cols;
     p.part_floats = p.stats * D;
@@ -1003,29 +1014,62 @@ static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t
                         int64_t max_rows)
 {
     AttPlan p{};
+    AttPart &first = p.part[0], &second = p.part[1];
     const int64_t G = Hq / heads, cols = T * G, blocks = (max_len + kKvBlock - 1) / kKvBlock;
     const bool small = (cols / 16 + nseq) * heads * blocks <= kAttSmall;
     // the most columns that a sequence may have; not told, a batch of few rows
     // each is taken for one of drafts
     const int64_t rows = nseq == 1 ? T : max_rows > 0 ? max_rows : T > 16 * nseq ? T - nseq + 1 : 16;
     const int64_t most = (rows < T ? rows : T) * G;
+    const auto units = [&](int64_t c) {
+        const int64_t n = (cols + c - 1) / c;
+        return (n > nseq ? n : nseq) * heads;
+    };
+    const int64_t u16 = units(16), u256 = units(256);
+    // estimates in us from the table's kind of measurements: the longest unit,
+    // and (unit, block) pairs over the card; rows of one sequence see all but
+    // half of themselves; the lengths of several lie between all alike and evenly
+    // spread from none (0.5 of the longest on average)
+    const double mean = nseq == 1 ? (double)(blocks - (T < max_len ? T : max_len) / (2 * kKvBlock)) : 0.75 * blocks;
+    const auto either = [](double a, double b) { return a > b ? a : b; };
+    const double rounds = (double)((u256 + kTileGroups - 1) / kTileGroups);
+    const double int8 = either(5 + 0.28 * blocks, 5 + 0.95e-3 * u16 * mean);
+    const double tile = 1.15 * either(13 + 1.45 * blocks, 5 + 8 * rounds + 7.5e-3 * u256 * mean);
+    const double tile_split = 25 + 1.5e-3 * T * Hq + 8e-3 * u256 * mean;
     p.parts = 1;
-    for (AttPart& q : p.part) q.max_cols = INT32_MAX;
-    if (!small && nseq > 1 && most > kAttMixed) {
-        p.parts = 2;
-        p.part[0].cols = 256;
-        p.part[0].min_cols = kAttTileCols + 1;
-        p.part[1].cols = 16;
-        p.part[1].max_cols = kAttTileCols;
-        // the second always as a line: a grid by units would be idle in a batch of prompts
-        att_cut(p.part[0], cols, heads, D, nseq, blocks, false);
-        att_cut(p.part[1], cols, heads, D, nseq, blocks, true);
-        return p;
+    first.max_cols = second.max_cols = INT32_MAX;
+    bool whole = blocks <= kAttWhole + u16 / (cols > 16 * nseq ? 2 : 8) || u16 >= 2 * kAttGroups;
+    if (nseq > 1 && most > kAttMixed && cols < most * nseq) {
+        // only the prompts' work goes to the tiles, whoever has the longest length
+        const double u = (double)((cols + 255) / 256 * heads);
+        if (!small && int8 > 15 + 8 * (double)(int64_t)(u / kTileGroups + 1) + 8.6e-3 * u * mean) {
+            p.parts = 2;
+            first.cols = 256;
+            first.min_cols = kAttTileCols + 1;
+            second.cols = 16;
+            second.max_cols = kAttTileCols;
+            att_cut(first, cols, heads, D, nseq, blocks, blocks <= 16 || (cols / 256 + nseq) * heads >= kTileGroups);
+            // always split: a grid by units would be idle in a batch of prompts
+            att_cut(second, cols, heads, D, nseq, blocks, false);
+            return p;
+        }
+        whole = whole || !small;
+    } else if (cols > kAttTileCols * nseq && most > kAttTileCols) {
+        const double best = tile < tile_split ? tile : tile_split;
+        whole = int8 <= best && (whole || !small);
+        if (!whole && !small) {
+            first.cols = 256;
+            att_cut(first, cols, heads, D, nseq, blocks, tile <= tile_split);
+            return p;
+        }
     }
-    if (!small && cols > kAttTileCols * nseq && most > kAttTileCols) p.part[0].cols = 256;
-    else if (cols <= 16 * nseq || nseq * heads * blocks < kAttShared) p.part[0].cols = 16;
-    else p.part[0].cols = cols <= 32 * nseq ? 32 : 64;
-    att_cut(p.part[0], cols, heads, D, nseq, blocks, false);
+    if (whole) {
+        const bool pair = u16 >= kAttPair || (u16 >= kAttPair / 2 && blocks <= 16);
+        first.cols = cols > 32 * nseq && u16 >= kAttQuad ? 64 : cols > 16 * nseq && pair ? 32 : 16;
+    } else {
+        first.cols = cols <= 16 * nseq || nseq * heads * blocks < kAttShared ? 16 : cols <= 32 * nseq ? 32 : 64;
+    }
+    att_cut(first, cols, heads, D, nseq, blocks, whole);
     return p;
 }
 

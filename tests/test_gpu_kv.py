@@ -350,6 +350,17 @@ def test_attend_prompts_split_where_a_stretch_ends(tw, new, prev, d, heads, hq, 
     check_attend(tw, s, queries(s, hq), window, max_len=10 ** 6)
 
 
+@pytest.mark.parametrize("new, prev, heads, hq, max_len", [
+    ([5] * 6, [200, 0, 64, 700, 3, 130], 2, 8, 10 ** 6), ([12, 0, 12, 9], [300, 5, 1000, 55], 2, 8, 10 ** 6),   # split
+    ([10] * 80, [3 * i for i in range(80)], 32, 64, None), ([20] * 80, [3 * i for i in range(80)], 32, 64, None),
+    ([7, 0, 20, 1] * 20, [5 * i for i in range(80)], 32, 64, None),                 # two and four tiles a workgroup
+    ([300] * 40, [7] * 40, 8, 8, 10 ** 6), ([300, 1, 0, 2] * 30, list(range(120)), 8, 8, 10 ** 6),  # many 256-column tiles
+])
+def test_attend_batches_of_many_tiles(tw, new, prev, heads, hq, max_len):
+    s = Case(tw, 137, 64, heads, new, prev)
+    check_attend(tw, s, queries(s, hq), max_len=max_len)
+
+
 @pytest.mark.parametrize("seqs, rows", [(70, 1), (130, 1), (70, 5)])
 def test_attend_many_long_sequences(tw, seqs, rows):
     """More sequences than lanes, long enough to be split, some without rows."""

@@ -103,9 +103,9 @@ __device__ __forceinline__ void rotate(float* x, int j, bool interleaved, CS cs)
 
 // ---- norm + rotation -------------------------------------------------------
 // One workgroup per token and 16 heads; the token's D/2 angles are computed
-// once per workgroup.  One token of 32:8 heads takes 2.2 us, an empty kernel
+// once per workgroup.  One token of 32:8 heads takes 2.7 us, an empty kernel
 // 1.95; bound by the rows from a few hundred tokens on: 4096 tokens, fp32 in
-// and bf16 out (126 MB), 19.5 us, 6.5 TB/s (the rows just written come in part
+// and bf16 out (126 MB), 20 us, 6.3 TB/s (the rows just written come in part
 // from the last-level cache; a plain copy of as many bytes reaches 4.9).
 template <int D, typename TI, typename TO>
 __global__ __launch_bounds__(256) void norm_rope_kernel(QkTransform f, const TI* q, int Hq, int64_t q_stride,
@@ -435,8 +435,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvBatch b, Qk
 // is 16 dims of one token; a chunk of V is one dim of 16 tokens, and four
 // neighbouring lanes exchange theirs so that each has four dims of four
 // tokens.  Bound by what it writes: eight contexts of 2500 to 9000 tokens, 8
-// heads of 128, to bf16 (270 MB, two thirds of them written) take 43 us, 6.2
-// TB/s; 777 tokens 3.4 us.
+// heads of 128, to bf16 (254 MB, two thirds of them written) take 43 us, 5.9
+// TB/s; 777 tokens 4.6 us.
 
 // 4 N codes as values, in stores of 16 bytes where there are as many
 template <int N, typename TO>

@@ -992,12 +992,16 @@ constexpr int64_t kTileGroups = 256;         // one a CU on the fp16 path
 //   16 x 1 up to 3000        20.9 / 22.2 /   -  /   -      up to 4500  29.5 / 27.7 /   -  /   -
 //   64 x 1 up to 3000        42.6 / 45.2 /   -  /   -      up to 16000  194 /  178 /   -  /   -
 //   16 x 7 up to 3000        21.4 / 33.0 / 30.4 / 52.6     up to 4500  29.7 / 39.7 / 36.4 /   -
-//   16 x 16 up to 3000       24.8 / 49.1 / 39.5 / 59.1     up to 12000 80.8 /   -  /   -  / 105
+//   16 x 16 up to 3000       24.8 / 49.1 / 39.5 / 59.1     up to 12000 80.8 /   -  / 81.9 / 105
 //   1 x 48 up to 3000        18.5 / 22.0 / 27.1 / 34.3     up to 12000 55.7 / 39.5 / 36.6 / 41.8
 //   8 x 64 up to 3000        32.6 / 79.1 / 51.7 / 54.9     up to 12000  112 /   -  / 122  / 94.2
 //   32 x 128 up to 1500       127 /  -   /  -   / 86.8     up to 12000  672 /   -  /   -  / 447
 // (32 x 128 up to 600: 82.5 with 16 columns, 60.4 with 32, 49.9 with 64.)
 constexpr int64_t kAttWhole = 22;            // blocks up to which a lone unit stays whole
+// one long sequence among many short ones is waited for alone: 64 x 16 rows over 500, one of them over 12000,
+// 110 us whole and 55 split, over 6000 62 and 65; more than 64 columns are several tiles, split or not, and
+// gain more where all are long (32 x 24 rows up to 12000 167 whole, 250 split)
+constexpr int64_t kAttWholeMost = 128;
 constexpr int64_t kAttShared = 4096;         // (block, head) pairs from which split tiles of one head share their reads
 constexpr int64_t kAttPair = 2048, kAttQuad = 4096;   // units from which two or four whole tiles share theirs
 constexpr int64_t kAttTileCols = 128;        // columns a sequence from which 256-column tiles are looked at
@@ -1007,13 +1011,14 @@ constexpr int64_t kAttMixed = 512;           // columns that one of several sequ
 // Caches that pass the last-level cache (256 MB) are read past it: 64 streams
 // up to 16000 (2.1 GB at most, 483 MB) 95 us against 107; below, the plain
 // loads are faster, one stream over 40960 (84 MB) 23.8 us against 25.2.  Not
-// where several tiles read a block (16 x 48 rows up to 12000 217 us against 151).
+// where several waves or tiles read a block (16 x 48 rows up to 12000 217 us
+// against 151, 64 x 16 up to 12000 split 386 against 265).
 constexpr int64_t kAttStream = 256ll << 20;
 
 static void att_cut(AttPart& p, int64_t cols, int64_t heads, int64_t D, int64_t nseq, int64_t blocks, bool whole)
 {
     p.items = cols / p.cols + nseq;
-    p.streams = cols <= p.cols * nseq && nseq * heads * blocks * 2 * kKvBlock * D > kAttStream;
+    p.streams = cols <= 16 * nseq && nseq * heads * blocks * 2 * kKvBlock * D > kAttStream;
     if (whole) return;
     const int64_t units = p.items * heads, groups = p.cols == 256 ? kTileGroups : kAttGroups;
     const int64_t turn = p.cols <= 64 ? 64 / p.cols : 1, turns = (blocks + turn - 1) / turn;
@@ -1051,7 +1056,8 @@ static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t
     const double tile_split = 25 + 1.5e-3 * T * Hq + 8e-3 * u256 * mean;
     p.parts = 1;
     first.max_cols = second.max_cols = INT32_MAX;
-    bool whole = blocks <= kAttWhole + u16 / (cols > 16 * nseq ? 2 : 8) || u16 >= 2 * kAttGroups;
+    bool whole = (blocks <= kAttWhole + u16 / (cols > 16 * nseq ? 2 : 8) || u16 >= 2 * kAttGroups) &&
+                 blocks <= (cols > 64 * nseq ? 2 : 1) * kAttWholeMost;
     if (nseq > 1 && most > kAttMixed && cols < most * nseq) {
         // only the prompts' work goes to the tiles, whoever has the longest length
         const double u = (double)((cols + 255) / 256 * heads);
@@ -1100,8 +1106,8 @@ static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, i
                          hipStream_t stream)
 {
     const int64_t grid = a.groups ? a.groups : items * c.heads;
-    if (COLS <= 64 && streams)
-        kv_attend_kernel<D, COLS, COLS <= 64><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
+    if (COLS == 16 && streams)
+        kv_attend_kernel<D, COLS, COLS == 16><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
     else
         kv_attend_kernel<D, COLS, false><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
     const hipError_t e = hipGetLastError();

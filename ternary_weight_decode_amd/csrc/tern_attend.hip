@@ -978,6 +978,7 @@ struct AttPart {
 struct AttPlan {
     AttPart part[2];
     int parts;
+    int64_t bytes() const { return part[0].bytes() + (parts > 1 ? part[1].bytes() : 0); }
 };
 
 constexpr int64_t kAttGroups = 768;          // three workgroups a CU: what registers allow on the int8 path
@@ -1013,12 +1014,12 @@ constexpr int64_t kAttMixed = 512;           // columns that one of several sequ
 // loads are faster, one stream over 40960 (84 MB) 23.8 us against 25.2.  Not
 // where several waves or tiles read a block (16 x 48 rows up to 12000 217 us
 // against 151, 64 x 16 up to 12000 split 386 against 265).
-constexpr int64_t kAttStream = 256ll << 20;
+constexpr double kAttStream = 256 << 20;
 
 static void att_cut(AttPart& p, int64_t cols, int64_t heads, int64_t D, int64_t nseq, int64_t blocks, bool whole)
 {
     p.items = cols / p.cols + nseq;
-    p.streams = cols <= 16 * nseq && nseq * heads * blocks * 2 * kKvBlock * D > kAttStream;
+    p.streams = cols <= 16 * nseq && (double)(nseq * heads * blocks) * (2 * kKvBlock * D) > kAttStream;
     if (whole) return;
     const int64_t units = p.items * heads, groups = p.cols == 256 ? kTileGroups : kAttGroups;
     const int64_t turn = p.cols <= 64 ? 64 / p.cols : 1, turns = (blocks + turn - 1) / turn;
@@ -1029,11 +1030,15 @@ static void att_cut(AttPart& p, int64_t cols, int64_t heads, int64_t D, int64_t 
 }
 
 static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
-                        int64_t max_rows)
+                        int64_t max_rows, int64_t window)
 {
     AttPlan p{};
     AttPart &first = p.part[0], &second = p.part[1];
-    const int64_t G = Hq / heads, cols = T * G, blocks = (max_len + kKvBlock - 1) / kKvBlock;
+    // blocks that a unit has at most
+    const int64_t G = Hq / heads, cols = T * G, all = (max_len + kKvBlock - 1) / kKvBlock;
+    const int64_t seen = window > 0 ? window / kKvBlock + 256 / kKvBlock + 2 : all;
+    const bool windowed = seen < all;
+    const int64_t blocks = windowed ? seen : all;
     const bool small = (cols / 16 + nseq) * heads * blocks <= kAttSmall;
     // the most columns that a sequence may have; not told, a batch of few rows
     // each is taken for one of drafts
@@ -1048,7 +1053,9 @@ static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t
     // and (unit, block) pairs over the card; rows of one sequence see all but
     // half of themselves; the lengths of several lie between all alike and evenly
     // spread from none (0.5 of the longest on average)
-    const double mean = nseq == 1 ? (double)(blocks - (T < max_len ? T : max_len) / (2 * kKvBlock)) : 0.75 * blocks;
+    const double mean = windowed    ? (double)blocks
+                        : nseq == 1 ? (double)(blocks - (T < max_len ? T : max_len) / (2 * kKvBlock))
+                                    : 0.75 * blocks;
     const auto either = [](double a, double b) { return a > b ? a : b; };
     const double rounds = (double)((u256 + kTileGroups - 1) / kTileGroups);
     const double int8 = either(5 + 0.28 * blocks, 5 + 0.95e-3 * u16 * mean);
@@ -1095,10 +1102,8 @@ static AttPlan att_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t
 int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
                                   int64_t max_rows)
 {
-    const AttPlan p = att_plan(T, Hq, heads, D, nseq, max_len, max_rows);
-    int64_t bytes = 0;
-    for (int i = 0; i < p.parts; ++i) bytes += p.part[i].bytes();
-    return bytes;
+    const AttPlan p = att_plan(T, Hq, heads, D, nseq, max_len, max_rows, 0);
+    return p.bytes();
 }
 
 template <int D, int COLS>
@@ -1140,7 +1145,13 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const
                             int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows,
                             uint16_t* out, void* workspace, hipStream_t stream)
 {
-    const AttPlan plan = att_plan(b.T, Hq, c.heads, D, b.nseq, max_len, max_rows);
+    AttPlan plan = att_plan(b.T, Hq, c.heads, D, b.nseq, max_len, max_rows, 0);
+    if (window > 0) {
+        // what a window leaves to see is often short enough for whole units (64 x 7 rows up to 12000, window
+        // 512: 26 us instead of 42), but the workspace was sized for any window
+        const AttPlan near = att_plan(b.T, Hq, c.heads, D, b.nseq, max_len, max_rows, window);
+        if (near.bytes() <= plan.bytes()) plan = near;
+    }
     uint8_t* ws = (uint8_t*)workspace;
     for (int i = 0; i < plan.parts; ++i) {
         const AttPart& p = plan.part[i];

@@ -319,6 +319,17 @@ def test_attend_window(tw, new, prev, window):
     check_attend(tw, s, queries(s, 8), window=window)
 
 
+@pytest.mark.parametrize("new, prev, window", [
+    ([1], [3900], 2871), ([1, 1], [100, 5000], 2500), ([6], [3900], 2500), ([20, 20, 3], [3000, 10, 2600], 2600),
+    ([300], [4000], 3100), ([280, 1, 260], [3500, 4000, 10], 3333),
+])
+@pytest.mark.parametrize("max_len", [None, 10 ** 6])
+def test_attend_long_window(tw, new, prev, window, max_len):
+    """Windows long enough to be split."""
+    s = Case(tw, 61, 64, 1, new, prev)
+    check_attend(tw, s, queries(s, 4), window, max_len=max_len)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.05, 0.01, 0.3])
 @pytest.mark.parametrize("new, prev", [([1], [300]), ([90], [40])])
 def test_attend_scale(tw, new, prev, scale):

@@ -594,6 +594,19 @@ int tern_gemv_config(int64_t N, int64_t K, int64_t M, int kind, int64_t* out);
  * K % 128 != 0.  Touches no device memory. */
 int tern_prefill_config(int64_t N, int64_t K, int64_t M, int64_t* out);
 
+/* The kernels that i8_kv_attend takes for these arguments (heads and D of the
+ * cache, nseq and table_width of the batch), computed on the host exactly as
+ * the call does: returns the number of launches with a joining one not counted,
+ * 1 or 2 (0 where there is nothing to do), and fills six values of out[12] for
+ * each = {columns (rows x query heads of a group) of a workgroup's tile: 16, 32
+ * or 64 the int8 path, 256 the fp16 path; workgroups that share the blocks of
+ * all tiles evenly, their parts joined by a second kernel, or 0: a workgroup
+ * for each tile and head; workgroups; least and most columns of the sequences
+ * that it takes; codes read past the caches (0/1)}.  -TERN_E_NULL for a NULL
+ * out, -TERN_E_SHAPE for what i8_kv_attend refuses.  Touches no device memory. */
+int i8_kv_attend_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
+                        int64_t window, int64_t max_len, int64_t max_rows, int64_t* out);
+
 /* ---- matrix-core throughput probe (a measurement aid; no operation of the method) ----
  *
  * The contraction of tern_gemm_prefill runs on the int8 matrix cores and the

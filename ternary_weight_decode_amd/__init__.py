@@ -23,7 +23,7 @@ packed int8 head ``i8_head_packed_bytes``, ``i8_head_pack``,
 side of a step ``qk_norm_rope``, ``i8_kv_append``, ``i8_kv_read`` and
 ``i8_kv_attend`` (with the handles ``QkTransform``, ``I8KvCache`` and
 ``I8KvBatch``), and the launch-configuration views
-``tern_gemv_config`` and ``tern_prefill_config``.
+``tern_gemv_config``, ``tern_prefill_config`` and ``i8_kv_attend_config``.
 """
 from __future__ import annotations
 
@@ -42,7 +42,7 @@ SYMBOLS = ("tern_strerror", "tern_last_error", "tern_abi_version", "tern_packed_
            "i8_head_gemv_packed", "i8_head_gemv_packed_i8", "i8_head_argmax_packed", "i8_head_argmax_packed_i8",
            "fv5b_head_gemv_packed", "fv5b_head_gemv_packed_i8", "fv5b_head_argmax_packed",
            "fv5b_head_argmax_packed_i8", "qk_norm_rope", "i8_kv_append", "i8_kv_read",
-           "i8_kv_attend_workspace_bytes", "i8_kv_attend")
+           "i8_kv_attend_workspace_bytes", "i8_kv_attend", "i8_kv_attend_config")
 _INT_STATUS = ("tern_pack", "tern_stats", "tern_quantize_i8", "tern_gemv", "tern_gemv_i8", "i8_head_gemv",
                "i8_head_gemv_i8", "tern_gemm_prefill", "tern_chain_plan", "tern_gemv_chain", "i8_head_argmax",
                "i8_head_argmax_i8", "tern5_pack", "tern5_gemv", "tern5_gemv_i8", "fv5b_head_gemv", "fv5b_head_gemv_i8",
@@ -143,6 +143,8 @@ def lib():
         L.fv5b_head_gemv_packed_i8.argtypes = [_p, _p, _i64, _i64, _p, _p, _i64, _p, _p, _p]
         L.fv5b_head_argmax_packed.argtypes = [_p, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p]
         L.fv5b_head_argmax_packed_i8.argtypes = [_p, _p, _i64, _i64, _p, _p, _i64, _p, _p, _p, _p, _p]
+        L.i8_kv_attend_config.restype = ctypes.c_int
+        L.i8_kv_attend_config.argtypes = [_i64] * 9 + [ctypes.POINTER(_i64)]
         cache, batch, transform = (ctypes.POINTER(t) for t in (_KvCache, _KvBatch, _QkTransform))
         L.qk_norm_rope.argtypes = [transform, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, ctypes.c_int, _p, _p, _p,
                                    ctypes.c_int, _p]
@@ -998,6 +1000,19 @@ def i8_kv_attend_workspace(cache, batch, tokens: int, hq: int, max_len=None, max
     if nbytes < 0:
         _check("i8_kv_attend_workspace_bytes", 2)
     return _torch.empty(nbytes, dtype=_torch.uint8, device=cache.device) if nbytes else None
+
+
+def i8_kv_attend_config(tokens: int, hq: int, heads: int, d: int, nseq: int, width: int, window: int = 0,
+                        max_len=None, max_rows: int = 0):
+    """The launches that i8_kv_attend takes for `tokens` rows of hq heads (host-side, no device needed; width:
+    of the table, max_len by default what that holds): a list of dicts, empty where there is nothing to do."""
+    out = (_i64 * 12)()
+    rc = lib().i8_kv_attend_config(tokens, hq, heads, d, nseq, width, window,
+                                   max(1, width * KV_BLOCK) if max_len is None else max_len, max_rows, out)
+    if rc < 0:
+        _check("i8_kv_attend_config", -rc)
+    keys = ("cols", "groups", "grid", "min_cols", "max_cols", "streams")
+    return [dict(zip(keys, (int(v) for v in out[6 * i:6 * i + 6]))) for i in range(rc)]
 
 
 def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, max_rows: int = 0, out=None,

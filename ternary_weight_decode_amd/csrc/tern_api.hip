@@ -811,6 +811,16 @@ int tern_prefill_config(int64_t N, int64_t K, int64_t M, int64_t* out)
     return 1;
 }
 
+int i8_kv_attend_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
+                        int64_t window, int64_t max_len, int64_t max_rows, int64_t* out)
+{
+    if (!out) return -TERN_E_NULL;
+    const int64_t need = i8_kv_attend_workspace_bytes(T, Hq, heads, D, nseq, max_len, max_rows);
+    if (need < 0 || table_width < 0 || table_width > INT32_MAX / TERN_KV_BLOCK || window < 0) return -TERN_E_SHAPE;
+    if (T == 0 || nseq == 0) return 0;
+    return tern::kv_attend_config(T, Hq, heads, D, nseq, table_width, window, max_len, max_rows, out);
+}
+
 }  // extern "C"
 
 extern "C" {

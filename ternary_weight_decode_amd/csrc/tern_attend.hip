@@ -1141,17 +1141,46 @@ static hipError_t attend_part(const KvCache& c, const KvBatch& b, const AttArgs&
     }
 }
 
+// the plan of one call
+static AttPlan att_choose(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
+                          int64_t window, int64_t max_len, int64_t max_rows)
+{
+    AttPlan plan = att_plan(T, Hq, heads, D, nseq, max_len, max_rows, 0);
+    if (window > 0) {
+        // what a window leaves to see is often short enough for whole units (64 x 7 rows up to 12000, window
+        // 512: 26 us instead of 42), but the workspace was sized for any window
+        const AttPlan near = att_plan(T, Hq, heads, D, nseq, max_len, max_rows, window);
+        if (near.bytes() <= plan.bytes()) plan = near;
+    }
+    for (int i = 0; i < plan.parts; ++i) {
+        // the line is counted in 32 bits; a batch that could pass that has units enough
+        const int64_t line = plan.part[i].items * heads * (table_width + kAttWaves);
+        if (line >= (1ll << 31)) plan.part[i].groups = 0;
+    }
+    return plan;
+}
+
+int kv_attend_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
+                     int64_t window, int64_t max_len, int64_t max_rows, int64_t* out)
+{
+    const AttPlan plan = att_choose(T, Hq, heads, D, nseq, table_width, window, max_len, max_rows);
+    for (int i = 0; i < plan.parts; ++i) {
+        const AttPart& p = plan.part[i];
+        *out++ = p.cols;
+        *out++ = p.groups;
+        *out++ = p.groups ? p.groups : p.items * heads;
+        *out++ = p.min_cols;
+        *out++ = p.max_cols;
+        *out++ = p.cols == 16 && p.streams;
+    }
+    return plan.parts;
+}
+
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
                             int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows,
                             uint16_t* out, void* workspace, hipStream_t stream)
 {
-    AttPlan plan = att_plan(b.T, Hq, c.heads, D, b.nseq, max_len, max_rows, 0);
-    if (window > 0) {
-        // what a window leaves to see is often short enough for whole units (64 x 7 rows up to 12000, window
-        // 512: 26 us instead of 42), but the workspace was sized for any window
-        const AttPlan near = att_plan(b.T, Hq, c.heads, D, b.nseq, max_len, max_rows, window);
-        if (near.bytes() <= plan.bytes()) plan = near;
-    }
+    const AttPlan plan = att_choose(b.T, Hq, c.heads, D, b.nseq, b.table_width, window, max_len, max_rows);
     uint8_t* ws = (uint8_t*)workspace;
     for (int i = 0; i < plan.parts; ++i) {
         const AttPart& p = plan.part[i];
@@ -1169,9 +1198,7 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const
         a.min_cols = p.min_cols;
         a.max_cols = p.max_cols;
         a.by_sequence = p.max_cols < INT32_MAX && (int64_t)b.nseq * p.max_cols < (int64_t)b.T * a.G;
-        // the line is counted in 32 bits; a batch that could pass that has units enough
-        const int64_t line = p.items * c.heads * ((int64_t)b.table_width + kAttWaves);
-        a.groups = line < (1ll << 31) ? p.groups : 0;
+        a.groups = p.groups;
         const hipError_t e = D == 128 ? attend_part<128>(c, b, a, p, stream) : attend_part<64>(c, b, a, p, stream);
         if (e != hipSuccess) return e;
     }

@@ -142,6 +142,8 @@ hipError_t launch_kv_read(const KvCache& c, const KvBatch& b, int64_t D, void* k
                           hipStream_t stream);
 int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
                                   int64_t max_rows);
+int kv_attend_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
+                     int64_t window, int64_t max_len, int64_t max_rows, int64_t* out);
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
                             int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows,
                             uint16_t* out, void* workspace, hipStream_t stream);

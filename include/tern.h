@@ -555,8 +555,13 @@ int i8_kv_read(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, vo
  * The sums do not depend on timing: equal calls give equal bytes.
  * Accuracy, against exact arithmetic over the cached values: the output's
  * rounding to bf16, and below it what the operands of the matrix cores leave
- * out: q to 2^-16 of its row's largest value, weights to 2^-16 of the largest
- * of their 64 tokens (few columns) or to 2^-11 of themselves (prompts). */
+ * out.  Few columns, on the int8 matrix cores: q to 2^-16 of its row's largest
+ * value, weights to 2^-16 of the largest of their 64 tokens.  Prompts, on the
+ * fp16 ones: weights to 2^-11 of themselves, or to 2^-34 of the largest product
+ * of a weight and its block's V scale among the tokens that the row sees, and
+ * 0 for results below 2^-73 (the V scales that it sees lie within 2^120 of each
+ * other).  Which of the two a row gets follows from the sizes of the call and
+ * its hints (i8_kv_attend_config), not from values. */
 int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
                                      int64_t max_rows);
 int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,

@@ -418,13 +418,13 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
 // operations per score instead of sixteen.
 //   S^T = K Q^T   32 tokens x 32 columns x 16 dims; q divided by the power of
 //                 two below its row's largest value, exact to 2^-25 of that.
-//   weights       2^(9 + x - m + log2(s_V / ref)) in fp16: the values' scale
-//                 rides in the exponent, relative to a power of two at least
-//                 as large as every scale so far, and leaves the sum of
-//                 weights again with one product a block.  m, a maximum of
-//                 the scores so far, moves only when a lane's weights sum to
-//                 more than 2^15; tails keep their digits down to 2^-33 of
-//                 the largest.
+//   weights       2^(9 + x + log2 s_V - m) in fp16: the values' scale rides in
+//                 the exponent and leaves the sum of weights again with one
+//                 product a block.  m, the row's own largest x + log2 s_V so
+//                 far (what a row does not see has no say in it), moves only
+//                 when a lane's weights sum to more than 2^15.  fp16 holds
+//                 2^-11 of a weight, and 2^-34 of the row's largest product of
+//                 weight and scale where that is more.
 //   O^T = V^T P^T the lane's weights are the B operand as they stand; V lies
 //                 in LDS in their order.
 // The matrix cores and the vector units are kept busy at once by the two waves
@@ -444,6 +444,10 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kF16Up = 9.0f, kF16Most = 32768.0f;
+// A smaller scale of values than 2^-80, 0 among them, stands for that, so that
+// its logarithm and what takes it out of the sum of weights stay in range;
+// results below what the largest code makes of it are 0.
+constexpr float kF16Least = 0x1p-80f, kF16None = 0x1p-73f;
 constexpr int kTileWaves = 8;
 constexpr int kAhead = 4;                    // LDS operands under way to the matrix cores
 
@@ -470,6 +474,13 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b)
 {
     const f16x2 h = {(_Float16)a, (_Float16)b};
     return __builtin_bit_cast(uint32_t, h);
+}
+
+// a result of the fp16 path (NaN kept)
+template <int COLS>
+__device__ __forceinline__ float none_below(float y)
+{
+    return COLS == 256 && fabsf(y) < kF16None ? 0.0f : y;
 }
 
 __device__ __forceinline__ void half_turn()
@@ -552,7 +563,7 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
     const int step = second ? ((fu / S >> 1) * ST + fu % S * 4) * 64 + (fu / S & 1) * 16 : (fu >> 1) * 256 + (fu & 1) * 16;
     u32x4* const to = (second ? kbuf[0] : vbuf[0]) + step + fg * 32 + fr;
 
-    float m = -INFINITY, l = 0.0f, ref = 0.0f;
+    float m = -INFINITY, l = 0.0f;
     f32x16 acc[DT];
 #pragma unroll
     for (int u = 0; u < DT; ++u)
@@ -576,22 +587,8 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
         const int number = __builtin_amdgcn_ds_permute(dest, tile.b0 + seg + lane);
         const float sk = __builtin_bit_cast(float, __builtin_amdgcn_ds_permute(dest, __builtin_bit_cast(int, sc.x)));
         const float sv = __builtin_bit_cast(float, __builtin_amdgcn_ds_permute(dest, __builtin_bit_cast(int, sc.y)));
-        // the values' scales relative to ref, and what takes them out of the
-        // sum of weights; 2^-60 stands for less than that, and for 0
-        float big = lane < blocks && sv < INFINITY ? sv : 0.0f;
-        for (int off = 1; off < 64; off <<= 1) big = fmaxf(big, __shfl_xor(big, off));
-        if (big > ref) {
-            const float up =
-                __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, big) & 0x7F800000u) + 0x00800000u);
-            const float shrink = ref / up;            // 0 at first: nothing is summed yet
-#pragma unroll
-            for (int u = 0; u < DT; ++u)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[u][e] *= shrink;
-            ref = up;
-        }
-        const float ratio = ref == 0.0f ? 0x1p-60f : fmaxf(sv / ref, 0x1p-60f);
-        const float lr = sv < INFINITY ? __log2f(ratio) : NAN, back = exp2_fast(-lr);
+        // the values' scales as exponents, and what takes them out of the sum of weights
+        const float lv = sv < INFINITY ? __log2f(fmaxf(sv, kF16Least)) : NAN, back = exp2_fast(-lv);
         const auto pick = [](float v, int i) {
             return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), i));
         };
@@ -653,11 +650,11 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
         };
         const auto softmax = [&](int i) {
             // read with every lane active: a lane's value must not be computed behind a mask
-            const float f = rowf * pick(sk, i), lri = pick(lr, i), backi = pick(back, i);
+            const float f = rowf * pick(sk, i), lvi = pick(lv, i), backi = pick(back, i);
             const int at = __builtin_amdgcn_readlane(number, i) * kKvBlock;
             // exponents against the maximum so far; token of x[t][e]:
             // at + 32 t + 8 (e / 4) + 4 half + e % 4
-            const float m0 = m == -INFINITY ? 0.0f : m, base = kF16Up + lri - m0;
+            const float m0 = m == -INFINITY ? 0.0f : m, base = kF16Up + lvi - m0;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -694,7 +691,7 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
 #pragma unroll
                 for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(x[0][e], x[1][e]));
                 top = fmaxf(top, __shfl_xor(top, 32));
-                const float over = top - (kF16Up + lri);
+                const float over = top - kF16Up;
                 const bool grow = m == -INFINITY ? over > -INFINITY : over > 0.0f;
                 const float by = grow ? over : 0.0f;
                 const float keep = m == -INFINITY ? 0.0f : exp2_fast(-by);
@@ -743,7 +740,7 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
     const bool none = l == 0.0f;
     if (whole) {
         typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-        const float r = none ? 0.0f : ref / l;
+        const float r = none ? 0.0f : 1.0f / l;
         uint16_t* dst =
             a.out + ((int64_t)(tile.s.t0 + j) * c.heads * a.G + h * a.G + cc - j * a.G) * D + 4 * half;
 #pragma unroll
@@ -752,7 +749,7 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
             for (int e = 0; e < 16; e += 4) {
                 u16x4 y;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = none ? (uint16_t)0 : f32_to_bf16(acc[u][e + k] * r);
+                for (int k = 0; k < 4; ++k) y[k] = none ? (uint16_t)0 : f32_to_bf16(none_below<COLS>(acc[u][e + k] * r));
                 *(u16x4*)(dst + 32 * u + 2 * e) = y;
             }
     } else {
@@ -765,7 +762,7 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
             for (int e = 0; e < 16; e += 4) {
                 f32x4 o;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = none ? 0.0f : acc[u][e + k] * ref;
+                for (int k = 0; k < 4; ++k) o[k] = acc[u][e + k];
                 *(f32x4*)(part + 32 * u + 2 * e) = o;
             }
     }
@@ -940,7 +937,7 @@ __global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel
     uint16_t* dst = a.out + ((int64_t)(tile.s.t0 + row) * Hq + h * a.G + (cc - (int64_t)row * a.G)) * D;
     if constexpr (JW == 1) {
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) dst[u * 64 + lane] = f32_to_bf16(sum == 0.0f ? 0.0f : o[u] / sum);
+        for (int u = 0; u < D / 64; ++u) dst[u * 64 + lane] = f32_to_bf16(sum == 0.0f ? 0.0f : none_below<COLS>(o[u] / sum));
     } else {
         __shared__ float2 sst[JW];
         if (lane == 0) sst[wave] = make_float2(top, sum);
@@ -959,7 +956,7 @@ __global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel
             y = fmaf(so[w][d], f, y);
             sum = fmaf(sst[w].y, f, sum);
         }
-        dst[d] = f32_to_bf16(sum == 0.0f ? 0.0f : y / sum);
+        dst[d] = f32_to_bf16(sum == 0.0f ? 0.0f : none_below<COLS>(y / sum));
     }
 }
 

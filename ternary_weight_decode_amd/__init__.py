@@ -808,12 +808,17 @@ def _rows(t, name, dtype, device, heads, d, tokens):
     return n, h, row if n > 1 else h * d
 
 
-def _new(shape, dtype, device, stream):
-    """An output or workspace for one call; memory used on a stream that is not the current one is kept
-    from reuse until that stream is done with it."""
-    t = _torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and stream != _torch.cuda.current_stream(device):
-        t.record_stream(stream)
+def _new(shape, dtype, device, stream, returned=True):
+    """An output or a workspace for one call.  The memory comes from the stream that will write it: what
+    the current stream has freed may still be in use there.  An output that is returned is kept from
+    reuse until the current stream, the caller's, is done with it too."""
+    current = None if stream is None else _torch.cuda.current_stream(device)
+    if stream == current:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        t = _torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(current)
     return t
 
 
@@ -1032,7 +1037,7 @@ def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, max
     need = lib().i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len, max_rows)
     if workspace is None:
         if need > 0:
-            workspace = _new(need, _torch.uint8, device, stream)
+            workspace = _new(need, _torch.uint8, device, stream, returned=False)
     elif workspace.get_device() != device or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise RuntimeError(f"workspace must be a contiguous tensor of at least {need} bytes on device {device}")

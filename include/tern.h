@@ -464,7 +464,8 @@ int fv5b_embed(const int8_t* W, const float* S, int64_t V, int64_t K, const int3
  * entry outside [0, blocks), a position below 0 and one past the table's
  * width name no cached token: the append stores nothing there, the read gives
  * zeros and the attention does not see it.  cu must not descend and must end
- * within the T rows; a sequence for which that fails is skipped.
+ * within the T rows: a sequence that leaves the rows is skipped, and where cu
+ * descends every sequence from there on.
  *
  * Per-token tensors hold T rows of heads * D contiguous elements; row t starts
  * at t * stride elements (the q, k and v parts of one fused row are three such

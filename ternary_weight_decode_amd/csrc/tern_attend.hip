@@ -120,7 +120,7 @@ struct AttArgs {
 
 // A sequence's share of the line: its tiles, and the blocks that each of its
 // units takes there (padded; no tile of the sequence sees more).  None for a
-// sequence without rows or of another launch.
+// sequence without rows or of another launch; s.n < 0 where cu descends.
 struct AttShare {
     uint32_t tiles, len;
 };
@@ -146,7 +146,7 @@ __device__ __forceinline__ AttShare att_share(const KvBatch& b, int i, const Att
     s.i = i;
     s.t0 = b.cu[i];
     const int t1 = b.cu[i + 1];
-    s.n = t1 - s.t0;
+    s.n = t1 < s.t0 ? -1 : t1 - s.t0;
     s.p0 = kv_length(b, i) - s.n;
     constexpr uint32_t kTurn = att_turn<COLS>();
     AttShare r = {0, kTurn};
@@ -782,13 +782,20 @@ __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_at
     uint32_t x = 0, x0 = 0, x1 = 1, at = 0;
     int i = 0;
     if (a.groups > 0) {
-        // the line: every lane sums the shares of a run of sequences
+        // the line: every lane sums the shares of a run of sequences, up to the
+        // first descent of cu (so that no rows are counted twice, and the sums
+        // stay in the bits that the launcher has checked)
         const int run = (b.nseq + 63) / 64;
         uint32_t mine = 0;
-        for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
+        bool falls = false;
+        for (int k = lane * run; k < lane * run + run && k < b.nseq && !falls; ++k) {
             r = att_share<COLS>(b, k, a, tile.s);
+            falls = tile.s.n < 0;
             mine += r.tiles * c.heads * r.len;
         }
+        const uint64_t fell = __ballot(falls);
+        const int lanes = fell ? __builtin_ctzll(fell) : 63;  // the last that counts
+        if (lane > lanes) mine = 0;
         uint32_t upto = mine;
         if (b.nseq > 1)
             for (int off = 1; off < 64; off <<= 1) {
@@ -798,10 +805,12 @@ __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_at
         const uint32_t total = __builtin_amdgcn_readlane(upto, b.nseq > 1 ? 63 : 0);
         if (blockIdx.x == 0 && threadIdx.x < 64) {           // for the joining kernel
             uint32_t from = upto - mine;
+            bool counts = lane <= lanes;
             for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
                 KvSeq s;
                 const AttShare o = att_share<COLS>(b, k, a, s);
-                a.start[k] = from;
+                counts = counts && s.n >= 0;
+                a.start[k] = counts ? from : total;
                 from += o.tiles * c.heads * o.len;
             }
             if (lane == 0) a.start[b.nseq] = total;
@@ -896,6 +905,7 @@ __global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel
     if (r.tiles == 0) return;
     const bool alone = b.nseq == 1;          // one load's latency less
     const uint32_t total = alone ? r.tiles * c.heads * r.len : a.start[b.nseq], start = alone ? 0 : a.start[tile.s.i];
+    if (start >= total) return;              // behind a descent of cu
     const int number = (int)(cc / COLS), col = (int)(cc % COLS);
     if (!att_tile<COLS>(b, number, a.G, a.window, tile)) return;
     const uint32_t per = att_stretch<COLS>(total, a.groups);

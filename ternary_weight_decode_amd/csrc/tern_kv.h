@@ -61,7 +61,8 @@ __device__ __forceinline__ int kv_length(const KvBatch& b, int i) { return b.len
 // floor(b)).  Finds the owner of `item` and the item's number inside it; all
 // lanes of a wave call it together (64 entries of cu at a time, so the lookup
 // is one load's latency for up to 64 sequences).  False: no such sequence, or
-// rows outside the tensors.
+// rows outside the tensors.  Sequences from the first descent of cu on own
+// nothing: an item of theirs falls to the one in front, past its end.
 __device__ __forceinline__ bool kv_find(const KvBatch& b, int64_t item, int mul, int div, int extra, KvSeq& s,
                                         int64_t& local)
 {
@@ -70,8 +71,9 @@ __device__ __forceinline__ bool kv_find(const KvBatch& b, int64_t item, int mul,
     for (int c = 0; c < b.nseq; c += 64) {
         const int i = c + lane < b.nseq ? c + lane : b.nseq - 1;
         const int r0 = b.cu[i], r1 = b.cu[i + 1], r2 = kv_length(b, i);
-        const bool in = c + lane < b.nseq && (int64_t)r0 * mul / div + (int64_t)i * extra <= item;
-        const int got = __popcll(__ballot(in));
+        const bool in = c + lane < b.nseq && r1 >= r0 && (int64_t)r0 * mul / div + (int64_t)i * extra <= item;
+        const uint64_t out = ~__ballot(in);
+        const int got = out ? __builtin_ctzll(out) : 64;
         if (got == 0) break;
         owners += got;
         cu0 = __builtin_amdgcn_readlane(r0, got - 1);

@@ -815,8 +815,8 @@ __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_at
             }
             if (lane == 0) a.start[b.nseq] = total;
         }
+        // per <= total (both whole turns), so x passes total, below 2^31, by less than a turn of all workgroups
         const uint32_t per = att_stretch<COLS>(total, a.groups);
-        if (per > total && blockIdx.x > 0) return;            // the products below stay in 32 bits
         x0 = x = blockIdx.x * per;
         x1 = x > total || total - x < per ? total : x + per;
         if (x >= x1) return;

@@ -121,13 +121,10 @@ PROMPT = {"split": 0, "whole": 0, "beside": 1}                  # which sequence
 
 
 # ---- block scales of the values ----
-@pytest.mark.parametrize("k", [20, 24, 30, 36, 60, 100])
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kind, d, k", [(kind, d, k) for kind in KINDS for d in (64, 128) for k in
+                                        ((30, 100) if (kind, d) == ("whole", 128) else (20, 24, 30, 36, 60, 100))])
 def test_larger_values_behind_a_row_do_not_reach_it(kind, d, k):
     """The last block's values are 2^k times the others': rows in front of it are as right as without it."""
-    if d == 128 and kind == "whole" and k not in (30, 100):
-        pytest.skip("two of six are enough at this size")
     s, hq, max_len = make(kind, 200 + k, d)
     i = PROMPT[kind]
     s.scales[s.table[i, (s.lens[i] - 1) // 64], :, 1] *= np.float32(2.0) ** k
@@ -179,3 +176,259 @@ def test_rows_that_see_values_of_nothing(kind, tiny):
     got = check(kind, s, hq, queries(s, hq), max_len=max_len)
     rows = int(last * 64 - (s.lens[0] - s.new[0]))
     assert rows > 0 and np.all(got[:rows] == 0) and np.all(np.abs(got[rows:]).max((1, 2)) > 0)
+
+
+# ---- what a row sees ----
+@pytest.mark.parametrize("kind", KINDS)
+def test_rows_that_see_nothing(kind):
+    """Rows in front of the start give zeros, those behind them what they see; a sequence of length 0 gives
+    zeros; rows of no sequence are left as they were."""
+    import torch
+    if kind == "whole":
+        s, hq, max_len = Case(tw, 340, 64, 16, [600, 500], [1500, 0], spare_rows=3), 64, None
+    else:
+        s, hq, max_len = Case(tw, 340, 64, 2, [200, 170] + ([1, 0, 3] if kind == "beside" else []),
+                              [500, 0] + ([300, 0, 60] if kind == "beside" else []), spare_rows=3), 8, LONG
+    s.lens[:2] = s.new[0] - 77, 0
+    if kind == "beside":
+        s.lens[4] = 1
+    tiles, short = path(s, hq, 0, max_len)
+    assert (tiles["cols"], tiles["groups"] == 0, short["cols"]) == (256, kind == "whole", 16)
+    q = queries(s, hq)
+    c, b = s.device()
+    out = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device="cuda")
+    tw.i8_kv_attend(c, b, dev(q, torch.bfloat16), out=out, max_len=max_len)
+    got, n = host(out), int(s.cu[-1])
+    want, bound = exact(s, q)
+    assert np.all((np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + bound)[:n])
+    assert np.all(got[:77] == 0) and np.all(np.abs(got[77:s.cu[1]]).max(-1) > 0)
+    assert np.all(got[s.cu[1]:s.cu[2]] == 0) and np.all(got[n:] == 9)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_missing_blocks(kind):
+    s, hq, max_len = make(kind, 350, prev=900)
+    i = PROMPT[kind]
+    s.table[i, [0, 3, 4, 5, 7, (s.lens[i] - 1) // 64]] = -1, 10 ** 6, -1, len(s.codes), -2 ** 31, -1
+    check(kind, s, hq, queries(s, hq), max_len=max_len)
+    s.table[i] = -1                                              # none at all: zeros
+    got = check(kind, s, hq, queries(s, hq), max_len=max_len)
+    assert np.all(got[s.cu[i]:s.cu[i + 1]] == 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_table_narrower_than_the_length(kind):
+    """What the table does not hold is not seen; rows past it see all that it holds."""
+    s, hq, max_len = make(kind, 355, prev=500)
+    width = (int(s.lens[PROMPT[kind]]) - int(s.new[PROMPT[kind]]) + 100) // 64
+    s.table = s.table[:, :width].copy()
+    check(kind, s, hq, queries(s, hq), max_len=max_len or int(s.lens.max()))
+
+
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("kind", KINDS)
+def test_scales_that_are_not_finite(kind, bad, side):
+    """NaN in exactly the rows and heads that see the block, the others as without it."""
+    s, hq, max_len = make(kind, 360, prev=700)
+    i = PROMPT[kind]
+    q = queries(s, hq)
+    want, bound = exact(s, q)
+    at = (int(s.lens[i]) - int(s.new[i])) // 64 + 2              # a block in the middle of the rows
+    s.codes[s.table[i, at], -1, side] = 0
+    s.scales[s.table[i, at], -1, side] = bad
+    assert_kind(kind, s, hq, 0, max_len)
+    got = attend(s, q, max_len=max_len)
+    sees = np.zeros(got.shape[:2], bool)
+    row = int(s.cu[i]) + at * 64 - (int(s.lens[i]) - int(s.new[i]))
+    assert s.cu[i] < row < s.cu[i + 1]
+    sees[row:s.cu[i + 1], hq - hq // s.heads:] = True
+    assert np.array_equal(np.isnan(got), np.broadcast_to(sees[..., None], got.shape))
+    ok = ~sees
+    assert np.all((np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + bound)[ok])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_queries_that_are_not_finite(kind):
+    s, hq, max_len = make(kind, 370)
+    q = queries(s, hq)
+    want, bound = exact(s, q)
+    first = int(s.cu[PROMPT[kind]])
+    places = [(first, 0, 3, np.nan), (first + 70, 1, 40, np.inf), (first + 131, hq - 1, 63, -np.inf)]
+    for t, h, d, bad in places:
+        q[t, h, d] = bad
+    assert_kind(kind, s, hq, 0, max_len)
+    got = attend(s, q, max_len=max_len)
+    ok = np.ones(got.shape[:2], bool)
+    for t, h, *_ in places:
+        assert np.isnan(got[t, h]).all()
+        ok[t, h] = False
+    assert np.all((np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + bound)[ok])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_queries_of_any_size(kind):
+    """Rows of zeros, of numbers too small to score, and of large ones (scores stay in range by the scale)."""
+    s, hq, max_len = make(kind, 375)
+    q = queries(s, hq)
+    first = int(s.cu[PROMPT[kind]])
+    q[first:first + 40] = 0
+    q[first + 40:first + 80] *= np.float32(2.0) ** -110
+    q[first + 80:first + 120] *= 2.0 ** -9
+    q[first + 120:first + 130] *= 2.0 ** 5
+    check(kind, s, hq, kv.bf16(q), max_len=max_len)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_what_is_masked_changes_nothing(kind):
+    """Bytes behind the length, unused blocks and table entries behind the length."""
+    s, hq, max_len = make(kind, 380)
+    i = PROMPT[kind]
+    s.table = np.concatenate([s.table, np.full((len(s.table), 2), 10 ** 9, np.int32)], 1)
+    q = queries(s, hq)
+    first = check(kind, s, hq, q, max_len=max_len or int(s.lens.max()))
+    last, left = divmod(int(s.lens[i]) - 1, 64)
+    assert left < 63
+    for side in (0, 1):
+        tail = kv.place(side, s.d)[left + 1:].ravel()
+        s.codes[s.table[i, last], :, side][:, tail] = -127
+    s.scales[np.setdiff1d(np.arange(len(s.codes)), s.table)] = np.nan
+    assert np.array_equal(first, attend(s, q, max_len=max_len or int(s.lens.max())))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 0.01, 0.3])
+@pytest.mark.parametrize("kind", KINDS)
+def test_scale(kind, scale):
+    s, hq, max_len = make(kind, 390)
+    check(kind, s, hq, queries(s, hq), scale=scale, max_len=max_len)
+
+
+@pytest.mark.parametrize("rows", [130, 200])
+def test_flat_tail(rows):
+    """One key far above thousands of equal ones that together weigh as much."""
+    s = Case(tw, 400, 64, 1, [rows], [6000])
+    s.scales[:] = 0.01
+    s.codes[:, :, 0] = 0
+    s.codes[s.table[0, 0], 0, 0][kv.place(0, 64)[5]] = 100
+    check("split", s, 4, np.ones((s.tokens, 4, 64), np.float32), scale=np.log(6000.0) / 64, max_len=LONG)
+
+
+# ---- windows, and units of more blocks than a wave looks up at once ----
+def sampled(s, q, window, max_len, step=37):
+    rows = np.unique(np.concatenate([np.arange(0, s.tokens, step), [s.tokens - 1]]))
+    got = attend(s, q, window, max_len=max_len)
+    want, bound = exact(s, q, window, rows=rows)
+    assert np.all((np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + bound)[rows])
+    return got
+
+
+@pytest.mark.parametrize("new, prev, heads, hq, window, max_len, kind", [
+    ([1000], [0], 8, 64, 70, None, "whole"), ([1000], [0], 16, 64, 200, None, "whole"),
+    ([300], [1500], 16, 128, 1000, None, "whole"), ([2000], [4000], 4, 16, 5000, None, "whole"),
+    ([300] * 70, [40 + i for i in range(70)], 1, 5, 333, LONG, "whole"),
+    ([400, 1, 3, 2], [4500, 300, 60, 0], 16, 64, 3000, LONG, "split"),
+])
+def test_windows(new, prev, heads, hq, window, max_len, kind):
+    s = Case(tw, 410, 64, heads, new, prev)
+    launches = path(s, hq, window, max_len)
+    assert (launches[0]["cols"], launches[0]["groups"] == 0) == (256, kind == "whole")
+    sampled(s, queries(s, hq), window, max_len)
+
+
+@pytest.mark.parametrize("side", [0, 1])
+def test_what_lies_in_front_of_a_window_changes_nothing(side):
+    """Scales that are not finite: NaN in the rows whose window still holds the block, the others as without."""
+    s = Case(tw, 420, 64, 8, [1000], [0])
+    q = queries(s, 64)
+    assert_kind("whole", s, 64, 70, None)
+    want, bound = exact(s, q, 70)
+    s.scales[s.table[0, [2, 6]], :, side] = np.nan
+    got = attend(s, q, 70)
+    p = np.arange(1000)
+    sees = np.zeros(1000, bool)
+    for b in (2, 6):
+        sees |= (p >= 64 * b) & (p - 70 + 1 <= 64 * b + 63)
+    assert np.array_equal(np.isnan(got).all((1, 2)), sees) and np.array_equal(np.isnan(got).any((1, 2)), sees)
+    assert np.all((np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + bound)[~sees])
+
+
+@pytest.mark.parametrize("kind, new, prev, heads, hq, max_len", [
+    ("whole", 600, 4200, 8, 64, None), ("split", 2000, 3000, 8, 32, LONG),
+])
+def test_units_of_many_blocks(kind, new, prev, heads, hq, max_len):
+    """Uneven scales and missing blocks on both sides of the 64 blocks that are looked up together."""
+    s = Case(tw, 430, 64, heads, [new], [prev])
+    s.scales[:, :, 1] *= (2.0 ** s.rng.integers(-20, 20, s.scales.shape[:2])).astype(np.float32)
+    s.table[0, [1, 62, 63, 64, 70]] = -1
+    s.scales[s.table[0, 65]] = 0
+    assert_kind(kind, s, hq, 0, max_len)
+    tiles, most = -(-new * hq // heads // 256), -(-(new + prev) // 64)
+    assert most > 64 and (kind == "whole" or tiles * heads * most > 64 * 256)        # of a unit, of a stretch
+    sampled(s, queries(s, hq), 0, max_len)
+
+
+# ---- calls ----
+@pytest.mark.parametrize("kind", KINDS)
+def test_equal_bytes_on_any_stream(kind):
+    import torch
+    s, hq, max_len = make(kind, 440, 128)
+    assert_kind(kind, s, hq, 0, max_len)
+    c, b = s.device()
+    q = dev(queries(s, hq), torch.bfloat16)
+    first = tw.i8_kv_attend(c, b, q, max_len=max_len)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        got = [tw.i8_kv_attend(c, b, q, max_len=max_len, stream=x) for x in (side, None, side)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(first, x) for x in got)
+
+
+def test_one_workspace_through_calls_and_graphs():
+    import torch
+    parts = []
+    for i, kind in enumerate(KINDS):
+        s, hq, max_len = make(kind, 450 + i)
+        assert_kind(kind, s, hq, 0, max_len)
+        parts.append((*s.device(), dev(queries(s, hq), torch.bfloat16), max_len))
+    alone = [tw.i8_kv_attend(c, b, q, max_len=n) for c, b, q, n in parts]
+    sizes = [tw.i8_kv_attend_workspace(c, b, len(q), q.shape[1], n) for c, b, q, n in parts]
+    ws = torch.full((max(w.numel() for w in sizes if w is not None),), 255, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(a) for a in alone]
+    graphs = []
+    for (c, b, q, n), out in zip(parts, outs):
+        tw.i8_kv_attend(c, b, q, max_len=n, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tw.i8_kv_attend(c, b, q, max_len=n, out=out, workspace=ws)
+        graphs.append(g)
+    for order in ((0, 1, 2), (2, 0, 1), (1, 1, 0)):
+        for i in order:
+            outs[i].zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i], alone[i])
+            c, b, q, n = parts[i]
+            assert torch.equal(tw.i8_kv_attend(c, b, q, max_len=n, workspace=ws), alone[i])
+
+
+def test_far_blocks_of_a_large_cache():
+    """Blocks whose bytes lie past 2^32."""
+    import torch
+    d, heads, hq, rows = 128, 8, 16, 250
+    blocks = 2 ** 32 // (heads * 2 * 64 * d) + 40
+    codes = torch.zeros((blocks, heads, 2, 64 * d), dtype=torch.int8, device="cuda")
+    far = tw.I8KvCache(codes=codes, scales=torch.zeros((blocks, heads, 2), device="cuda"))
+    near = tw.I8KvCache(4, heads, d)
+    rng = np.random.default_rng(460)
+    k, v = dev(rng.normal(size=(2, rows, heads, d)).astype(np.float32))
+    q = dev(rng.normal(size=(rows, hq, d)), torch.bfloat16)
+    cu, lens = dev(np.array([0, rows], np.int32)), dev(np.array([rows], np.int32))
+    assert tw.i8_kv_attend_config(rows, hq, heads, d, 1, 4, max_len=LONG)[0]["cols"] == 256
+    got = []
+    for cache, table in ((far, [blocks - 1, 3, blocks - 7, blocks // 2]), (near, [0, 1, 2, 3])):
+        b = tw.I8KvBatch(cu, lens, torch.tensor([table], dtype=torch.int32, device="cuda"))
+        tw.i8_kv_append(cache, b, tw.QkTransform(d), k, v)
+        got.append(tw.i8_kv_attend(cache, b, q, max_len=LONG))
+    assert torch.equal(*got)

@@ -824,8 +824,13 @@ def _new(shape, dtype, device, stream, returned=True):
 
 def _call(name, device, stream, *args):
     """One library call on a device: made the current one where it is not, on its current stream or the
-    one given."""
-    handle = _raw_stream(device) if stream is None else stream.cuda_stream
+    one given (not one of another device, which the tensors need not be mapped on)."""
+    if stream is None:
+        handle = _raw_stream(device)
+    elif stream.device_index == device:
+        handle = stream.cuda_stream
+    else:
+        raise RuntimeError(f"stream is on device {stream.device_index}, expected {device}")
     f = getattr(_lib or lib(), name)
     if _torch.cuda.current_device() == device:
         rc = f(*args, handle)

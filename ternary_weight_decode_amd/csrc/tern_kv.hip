@@ -145,14 +145,13 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(QkTransform f, const TI*
 // of all the block's new tokens (the block's scale needs the maximum over
 // them, and nothing else writes the block); the queries of their rows are its
 // too where tokens are few, have a workgroup of their own where those are too
-// few for the card (a single token 5.6 us in a graph, 5.8 in one workgroup), and
-// four in prompts.  Loads are issued before the tokens' angles are computed,
+// few for the card, and four in prompts (figures at the launcher).  Loads are issued before the tokens' angles are computed,
 // once per workgroup, into LDS; up to four K and four V vectors (or four
 // queries) of each 16-lane group wait in registers.  Single tokens are bound by
-// the chain cu -> table -> rows -> scale -> codes: 5.6 us for one in a graph,
-// 7.7 for 48, an empty kernel 1.95.  Prompts are bound by the rows read: 4131
-// tokens of 32:8 heads of 128 (144 MB) take 33 us, 4.4 TB/s, where a plain copy
-// of those bytes takes 29 (without the angles' arithmetic 31.5).
+// the chain cu -> table -> rows -> scale -> codes: 5.7 us for one, calls one
+// behind another in a graph, 7.2 for 48, an empty kernel 1.95.  Prompts are bound
+// by the rows read: 4131 tokens of 32:8 heads of 128 (144 MB) take 36 us, 4.0
+// TB/s (34 in a kernel trace), where a plain copy of those bytes takes 29.
 
 // the scale after values of magnitude `top` (bits, so that inf < NaN) join;
 // shift: doublings that the old codes have to follow, 31 where they vanish
@@ -229,7 +228,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvCache c, KvBatch b, Qk
     __shared__ float2 cs[kKvBlock * D / 2];
     __shared__ uint32_t tops[2][4];
     // keys and values, with the most to do, start first (the prompt above takes
-    // 37 us with a block's roles side by side)
+    // 40 us with a block's roles side by side)
     const uint32_t items = gridDim.x / roles, role = blockIdx.x / items, item = blockIdx.x - role * items;
     const int h = item % c.heads;
     KvSeq s;
@@ -540,9 +539,12 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, int64_t D, const
 {
     const int G = (int)(Hq / c.heads);
     // Workgroups for a block and head: one for K and V and four for the queries
-    // in prompts (4131 rows 37 us, against 50 with one), one and one for few
-    // streams (a single token 3.2 us, against 4.8), else one for all (48 streams
-    // 6.4 us, against 9.2).
+    // in prompts, one and one for few streams, else one for all.  Calls one
+    // behind another in a graph, 32:8 heads of 128 (one for all / one and one /
+    // one and four, us):
+    //   4131 rows of two sequences  46.0 / 46.1 / 36.2    16 x 16 rows  9.5 /  7.2 /  7.1
+    //   1 token  5.9 / 5.7 / 5.7    16 streams  6.3 / 6.1 / 6.4    24  6.5 /  6.3 /  9.2
+    //   48 streams  7.2 / 9.0 / 14.2    128  15.9 / 18.6 / 33.9    64 x 8 rows  10.0 / 11.8 / 16.0
     const int roles = G == 0 ? 1 : (int64_t)b.T >= 16 * (int64_t)b.nseq ? kKvRoles : block_items(c, b) <= 256 ? 2 : 1;
 #define TERN_AP(DD, TI)                                                                                      \
     kv_append_kernel<DD, TI><<<block_items(c, b) * roles, 256, 0, stream>>>(                                 \

@@ -202,7 +202,7 @@ def tern_pack(t, scale, out=None, stream=None):
     if nbytes < 0:
         _check("tern_pack", 2)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+        out = _new(nbytes, torch.uint8, t.device, stream)
     _check("tern_pack", lib().tern_pack(_ptr(t), _ptr(scale), n, k, _ptr(out), _stream(stream)))
     return out
 
@@ -211,7 +211,7 @@ def tern_stats(packed, n: int, k: int, out=None, stream=None):
     """-> int64 [3]: nonzero weights, -1 weights, non-canonical sign bits."""
     import torch
     if out is None:
-        out = torch.empty(3, dtype=torch.int64, device=packed.device)
+        out = _new(3, torch.int64, packed.device, stream)
     _check("tern_stats", lib().tern_stats(_ptr(packed), n, k, _ptr(out), _stream(stream)))
     return out
 
@@ -222,9 +222,9 @@ def tern_quantize_i8(x, q=None, s_x=None, stream=None):
     _need(x, "x", (torch.bfloat16, torch.int16, torch.uint16), 2)
     m, k = x.shape
     if q is None:
-        q = torch.empty((m, k), dtype=torch.int8, device=x.device)
+        q = _new((m, k), torch.int8, x.device, stream)
     if s_x is None:
-        s_x = torch.empty(m, dtype=torch.float32, device=x.device)
+        s_x = _new(m, torch.float32, x.device, stream)
     _check("tern_quantize_i8", lib().tern_quantize_i8(_ptr(x), m, k, _ptr(q), _ptr(s_x), _stream(stream)))
     return q, s_x
 
@@ -235,7 +235,7 @@ def tern_gemv(packed, n: int, k: int, x, y=None, stream=None):
     _need(x, "x", (torch.bfloat16, torch.int16, torch.uint16), 2)
     m = x.shape[0]
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float32, device=x.device)
+        y = _new((m, n), torch.float32, x.device, stream)
     _check("tern_gemv", lib().tern_gemv(_ptr(packed), n, k, _ptr(x), m, _ptr(y), _stream(stream)))
     return y
 
@@ -246,7 +246,7 @@ def tern_gemv_i8(packed, n: int, k: int, q, s_x, y=None, acc=None, stream=None):
     _need(q, "q", (torch.int8,), 2)
     m = q.shape[0]
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float32, device=q.device)
+        y = _new((m, n), torch.float32, q.device, stream)
     _check("tern_gemv_i8", lib().tern_gemv_i8(_ptr(packed), n, k, _ptr(q), _ptr(s_x), m, _ptr(y), _ptr(acc),
                                               _stream(stream)))
     return y
@@ -260,7 +260,7 @@ def i8_head_gemv(w, row_scale, x, y=None, stream=None):
     v, k = w.shape
     m = x.shape[0]
     if y is None:
-        y = torch.empty((m, v), dtype=torch.float32, device=x.device)
+        y = _new((m, v), torch.float32, x.device, stream)
     _check("i8_head_gemv", lib().i8_head_gemv(_ptr(w), _ptr(row_scale), v, k, _ptr(x), m, _ptr(y),
                                               _stream(stream)))
     return y
@@ -273,7 +273,7 @@ def i8_head_gemv_i8(w, row_scale, q, s_x, y=None, acc=None, stream=None):
     v, k = w.shape
     m = q.shape[0]
     if y is None:
-        y = torch.empty((m, v), dtype=torch.float32, device=q.device)
+        y = _new((m, v), torch.float32, q.device, stream)
     _check("i8_head_gemv_i8", lib().i8_head_gemv_i8(_ptr(w), _ptr(row_scale), v, k, _ptr(q), _ptr(s_x), m, _ptr(y),
                                                     _ptr(acc), _stream(stream)))
     return y
@@ -292,7 +292,7 @@ def i8_head_pack(w, out=None, stream=None):
     if nbytes < 0:
         _check("i8_head_pack", 2)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.int8, device=w.device)
+        out = _new(nbytes, torch.int8, w.device, stream)
     _check("i8_head_pack", lib().i8_head_pack(_ptr(w), v, k, _ptr(out), _stream(stream)))
     return out
 
@@ -303,7 +303,7 @@ def i8_head_gemv_packed(wp, row_scale, v: int, k: int, x, y=None, stream=None):
     _need(x, "x", (torch.bfloat16, torch.int16, torch.uint16), 2)
     m = x.shape[0]
     if y is None:
-        y = torch.empty((m, v), dtype=torch.float32, device=x.device)
+        y = _new((m, v), torch.float32, x.device, stream)
     _check("i8_head_gemv_packed", lib().i8_head_gemv_packed(_ptr(wp), _ptr(row_scale), v, k, _ptr(x), m, _ptr(y),
                                                             _stream(stream)))
     return y
@@ -314,7 +314,7 @@ def i8_head_gemv_packed_i8(wp, row_scale, v: int, k: int, q, s_x, y=None, acc=No
     _need(q, "q", (torch.int8,), 2)
     m = q.shape[0]
     if y is None:
-        y = torch.empty((m, v), dtype=torch.float32, device=q.device)
+        y = _new((m, v), torch.float32, q.device, stream)
     _check("i8_head_gemv_packed_i8", lib().i8_head_gemv_packed_i8(_ptr(wp), _ptr(row_scale), v, k, _ptr(q),
                                                                   _ptr(s_x), m, _ptr(y), _ptr(acc), _stream(stream)))
     return y
@@ -326,9 +326,9 @@ def i8_head_argmax_packed(wp, row_scale, v: int, k: int, x, workspace=None, logi
     _need(x, "x", (torch.bfloat16, torch.int16, torch.uint16), 2)
     m = x.shape[0]
     if workspace is None:
-        workspace = i8_head_argmax_workspace(v, m, x.device)
-    idx = torch.empty(m, dtype=torch.int32, device=x.device)
-    val = torch.empty(m, dtype=torch.float32, device=x.device)
+        workspace = _new(i8_head_argmax_workspace_bytes(v, m), torch.uint8, x.device, stream, returned=False)
+    idx = _new(m, torch.int32, x.device, stream)
+    val = _new(m, torch.float32, x.device, stream)
     _check("i8_head_argmax_packed", lib().i8_head_argmax_packed(_ptr(wp), _ptr(row_scale), v, k, _ptr(x), m,
                                                                 _ptr(idx), _ptr(val), _ptr(logits),
                                                                 _ptr(workspace), _stream(stream)))
@@ -340,9 +340,9 @@ def i8_head_argmax_packed_i8(wp, row_scale, v: int, k: int, q, s_x, workspace=No
     _need(q, "q", (torch.int8,), 2)
     m = q.shape[0]
     if workspace is None:
-        workspace = i8_head_argmax_workspace(v, m, q.device)
-    idx = torch.empty(m, dtype=torch.int32, device=q.device)
-    val = torch.empty(m, dtype=torch.float32, device=q.device)
+        workspace = _new(i8_head_argmax_workspace_bytes(v, m), torch.uint8, q.device, stream, returned=False)
+    idx = _new(m, torch.int32, q.device, stream)
+    val = _new(m, torch.float32, q.device, stream)
     _check("i8_head_argmax_packed_i8", lib().i8_head_argmax_packed_i8(_ptr(wp), _ptr(row_scale), v, k, _ptr(q),
                                                                       _ptr(s_x), m, _ptr(idx), _ptr(val),
                                                                       _ptr(logits), _ptr(workspace),
@@ -368,9 +368,9 @@ def i8_head_argmax(w, row_scale, x, workspace=None, logits=None, stream=None):
     v, k = w.shape
     m = x.shape[0]
     if workspace is None:
-        workspace = i8_head_argmax_workspace(v, m, x.device)
-    idx = torch.empty(m, dtype=torch.int32, device=x.device)
-    val = torch.empty(m, dtype=torch.float32, device=x.device)
+        workspace = _new(i8_head_argmax_workspace_bytes(v, m), torch.uint8, x.device, stream, returned=False)
+    idx = _new(m, torch.int32, x.device, stream)
+    val = _new(m, torch.float32, x.device, stream)
     _check("i8_head_argmax", lib().i8_head_argmax(_ptr(w), _ptr(row_scale), v, k, _ptr(x), m, _ptr(idx), _ptr(val),
                                                   _ptr(logits), _ptr(workspace), _stream(stream)))
     return idx, val
@@ -398,9 +398,9 @@ def i8_head_argmax_i8(w, row_scale, q, s_x, workspace=None, logits=None, stream=
     v, k = w.shape
     m = q.shape[0]
     if workspace is None:
-        workspace = i8_head_argmax_workspace(v, m, q.device)
-    idx = torch.empty(m, dtype=torch.int32, device=q.device)
-    val = torch.empty(m, dtype=torch.float32, device=q.device)
+        workspace = _new(i8_head_argmax_workspace_bytes(v, m), torch.uint8, q.device, stream, returned=False)
+    idx = _new(m, torch.int32, q.device, stream)
+    val = _new(m, torch.float32, q.device, stream)
     _check("i8_head_argmax_i8", lib().i8_head_argmax_i8(_ptr(w), _ptr(row_scale), v, k, _ptr(q), _ptr(s_x), m,
                                                         _ptr(idx), _ptr(val), _ptr(logits), _ptr(workspace),
                                                         _stream(stream)))
@@ -412,7 +412,7 @@ def tern_gemm_prefill(packed, n: int, k: int, q, s_x, y=None, acc=None, stream=N
     _need(q, "q", (torch.int8,), 2)
     m = q.shape[0]
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float32, device=q.device)
+        y = _new((m, n), torch.float32, q.device, stream)
     _check("tern_gemm_prefill", lib().tern_gemm_prefill(_ptr(packed), n, k, _ptr(q), _ptr(s_x), m, _ptr(y),
                                                         _ptr(acc), _stream(stream)))
     return y
@@ -490,7 +490,7 @@ def tern5_pack(levels, s_lo, s_hi, out=None, stream=None):
     if nbytes < 0:
         _check("tern5_pack", 2)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=levels.device)
+        out = _new(nbytes, torch.uint8, levels.device, stream)
     _check("tern5_pack", lib().tern5_pack(_ptr(levels), _ptr(s_lo), _ptr(s_hi), n, k, _ptr(out), _stream(stream)))
     return out
 
@@ -501,7 +501,7 @@ def tern5_gemv(packed, n: int, k: int, x, y=None, stream=None):
     _need(x, "x", (torch.bfloat16, torch.int16, torch.uint16), 2)
     m = x.shape[0]
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float32, device=x.device)
+        y = _new((m, n), torch.float32, x.device, stream)
     _check("tern5_gemv", lib().tern5_gemv(_ptr(packed), n, k, _ptr(x), m, _ptr(y), _stream(stream)))
     return y
 
@@ -513,7 +513,7 @@ def tern5_gemv_i8(packed, n: int, k: int, q, s_x, y=None, acc=None, stream=None)
     _need(q, "q", (torch.int8,), 2)
     m = q.shape[0]
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float32, device=q.device)
+        y = _new((m, n), torch.float32, q.device, stream)
     _check("tern5_gemv_i8", lib().tern5_gemv_i8(_ptr(packed), n, k, _ptr(q), _ptr(s_x), m, _ptr(y), _ptr(acc),
                                                 _stream(stream)))
     return y
@@ -537,7 +537,7 @@ def fv5b_head_gemv(w, s, x, y=None, stream=None):
     import torch
     v, k, m = _fv5b_args(w, s, x, (torch.bfloat16, torch.int16, torch.uint16))
     if y is None:
-        y = torch.empty((m, v), dtype=torch.float32, device=x.device)
+        y = _new((m, v), torch.float32, x.device, stream)
     _check("fv5b_head_gemv", lib().fv5b_head_gemv(_ptr(w), _ptr(s), v, k, _ptr(x), m, _ptr(y), _stream(stream)))
     return y
 
@@ -547,7 +547,7 @@ def fv5b_head_gemv_i8(w, s, q, s_x, y=None, acc=None, stream=None):
     import torch
     v, k, m = _fv5b_args(w, s, q, (torch.int8,))
     if y is None:
-        y = torch.empty((m, v), dtype=torch.float32, device=q.device)
+        y = _new((m, v), torch.float32, q.device, stream)
     _check("fv5b_head_gemv_i8", lib().fv5b_head_gemv_i8(_ptr(w), _ptr(s), v, k, _ptr(q), _ptr(s_x), m, _ptr(y),
                                                         _ptr(acc), _stream(stream)))
     return y
@@ -558,9 +558,9 @@ def fv5b_head_argmax(w, s, x, workspace=None, logits=None, stream=None):
     import torch
     v, k, m = _fv5b_args(w, s, x, (torch.bfloat16, torch.int16, torch.uint16))
     if workspace is None:
-        workspace = i8_head_argmax_workspace(v, m, x.device)
-    idx = torch.empty(m, dtype=torch.int32, device=x.device)
-    val = torch.empty(m, dtype=torch.float32, device=x.device)
+        workspace = _new(i8_head_argmax_workspace_bytes(v, m), torch.uint8, x.device, stream, returned=False)
+    idx = _new(m, torch.int32, x.device, stream)
+    val = _new(m, torch.float32, x.device, stream)
     _check("fv5b_head_argmax", lib().fv5b_head_argmax(_ptr(w), _ptr(s), v, k, _ptr(x), m, _ptr(idx), _ptr(val),
                                                       _ptr(logits), _ptr(workspace), _stream(stream)))
     return idx, val
@@ -571,9 +571,9 @@ def fv5b_head_argmax_i8(w, s, q, s_x, workspace=None, logits=None, stream=None):
     import torch
     v, k, m = _fv5b_args(w, s, q, (torch.int8,))
     if workspace is None:
-        workspace = i8_head_argmax_workspace(v, m, q.device)
-    idx = torch.empty(m, dtype=torch.int32, device=q.device)
-    val = torch.empty(m, dtype=torch.float32, device=q.device)
+        workspace = _new(i8_head_argmax_workspace_bytes(v, m), torch.uint8, q.device, stream, returned=False)
+    idx = _new(m, torch.int32, q.device, stream)
+    val = _new(m, torch.float32, q.device, stream)
     _check("fv5b_head_argmax_i8", lib().fv5b_head_argmax_i8(_ptr(w), _ptr(s), v, k, _ptr(q), _ptr(s_x), m,
                                                             _ptr(idx), _ptr(val), _ptr(logits), _ptr(workspace),
                                                             _stream(stream)))
@@ -594,7 +594,7 @@ def fv5b_head_gemv_packed(wp, s, v: int, k: int, x, y=None, stream=None):
     import torch
     m = _fv5b_packed_args(s, v, k, x, (torch.bfloat16, torch.int16, torch.uint16))
     if y is None:
-        y = torch.empty((m, v), dtype=torch.float32, device=x.device)
+        y = _new((m, v), torch.float32, x.device, stream)
     _check("fv5b_head_gemv_packed", lib().fv5b_head_gemv_packed(_ptr(wp), _ptr(s), v, k, _ptr(x), m, _ptr(y),
                                                                 _stream(stream)))
     return y
@@ -604,7 +604,7 @@ def fv5b_head_gemv_packed_i8(wp, s, v: int, k: int, q, s_x, y=None, acc=None, st
     import torch
     m = _fv5b_packed_args(s, v, k, q, (torch.int8,))
     if y is None:
-        y = torch.empty((m, v), dtype=torch.float32, device=q.device)
+        y = _new((m, v), torch.float32, q.device, stream)
     _check("fv5b_head_gemv_packed_i8", lib().fv5b_head_gemv_packed_i8(_ptr(wp), _ptr(s), v, k, _ptr(q), _ptr(s_x),
                                                                       m, _ptr(y), _ptr(acc), _stream(stream)))
     return y
@@ -614,9 +614,9 @@ def fv5b_head_argmax_packed(wp, s, v: int, k: int, x, workspace=None, logits=Non
     import torch
     m = _fv5b_packed_args(s, v, k, x, (torch.bfloat16, torch.int16, torch.uint16))
     if workspace is None:
-        workspace = i8_head_argmax_workspace(v, m, x.device)
-    idx = torch.empty(m, dtype=torch.int32, device=x.device)
-    val = torch.empty(m, dtype=torch.float32, device=x.device)
+        workspace = _new(i8_head_argmax_workspace_bytes(v, m), torch.uint8, x.device, stream, returned=False)
+    idx = _new(m, torch.int32, x.device, stream)
+    val = _new(m, torch.float32, x.device, stream)
     _check("fv5b_head_argmax_packed", lib().fv5b_head_argmax_packed(_ptr(wp), _ptr(s), v, k, _ptr(x), m, _ptr(idx),
                                                                     _ptr(val), _ptr(logits), _ptr(workspace),
                                                                     _stream(stream)))
@@ -627,9 +627,9 @@ def fv5b_head_argmax_packed_i8(wp, s, v: int, k: int, q, s_x, workspace=None, lo
     import torch
     m = _fv5b_packed_args(s, v, k, q, (torch.int8,))
     if workspace is None:
-        workspace = i8_head_argmax_workspace(v, m, q.device)
-    idx = torch.empty(m, dtype=torch.int32, device=q.device)
-    val = torch.empty(m, dtype=torch.float32, device=q.device)
+        workspace = _new(i8_head_argmax_workspace_bytes(v, m), torch.uint8, q.device, stream, returned=False)
+    idx = _new(m, torch.int32, q.device, stream)
+    val = _new(m, torch.float32, q.device, stream)
     _check("fv5b_head_argmax_packed_i8", lib().fv5b_head_argmax_packed_i8(_ptr(wp), _ptr(s), v, k, _ptr(q),
                                                                           _ptr(s_x), m, _ptr(idx), _ptr(val),
                                                                           _ptr(logits), _ptr(workspace),
@@ -648,13 +648,13 @@ def fv5b_head_argmax_embed(w, s, x, e, es, workspace=None, logits=None, f32=True
     _need(es, "ES", (torch.float32,), 2)
     ve, ke = e.shape
     if workspace is None:
-        workspace = i8_head_argmax_workspace(v, m, x.device)
-    idx = torch.empty(m, dtype=torch.int32, device=x.device)
-    val = torch.empty(m, dtype=torch.float32, device=x.device)
+        workspace = _new(i8_head_argmax_workspace_bytes(v, m), torch.uint8, x.device, stream, returned=False)
+    idx = _new(m, torch.int32, x.device, stream)
+    val = _new(m, torch.float32, x.device, stream)
     if out is None and f32:
-        out = torch.empty((m, ke), dtype=torch.float32, device=x.device)
+        out = _new((m, ke), torch.float32, x.device, stream)
     if out_bf16 is None and bf16:
-        out_bf16 = torch.empty((m, ke), dtype=torch.bfloat16, device=x.device)
+        out_bf16 = _new((m, ke), torch.bfloat16, x.device, stream)
     _check("fv5b_head_argmax_embed",
            lib().fv5b_head_argmax_embed(_ptr(w), _ptr(s), v, k, _ptr(x), m, _ptr(idx), _ptr(val), _ptr(logits),
                                         _ptr(workspace), _ptr(e), _ptr(es), ve, ke, _ptr(out), _ptr(out_bf16),
@@ -672,9 +672,9 @@ def fv5b_embed(w, s, ids, f32=True, bf16=True, out=None, out_bf16=None, stream=N
     v, k = w.shape
     m = ids.shape[0]
     if out is None and f32:
-        out = torch.empty((m, k), dtype=torch.float32, device=ids.device)
+        out = _new((m, k), torch.float32, ids.device, stream)
     if out_bf16 is None and bf16:
-        out_bf16 = torch.empty((m, k), dtype=torch.bfloat16, device=ids.device)
+        out_bf16 = _new((m, k), torch.bfloat16, ids.device, stream)
     _check("fv5b_embed", lib().fv5b_embed(_ptr(w), _ptr(s), v, k, _ptr(ids), m, _ptr(out), _ptr(out_bf16),
                                           _stream(stream)))
     return out, out_bf16
@@ -722,7 +722,7 @@ def tern_launch_probe(kind: str, grid: int, src=None, sink=None, stream=None):
     at least `grid` floats (allocated when None)."""
     import torch
     if sink is None and kind != "empty":
-        sink = torch.empty(grid, dtype=torch.float32, device="cuda")
+        sink = _new(grid, torch.float32, "cuda", stream)
     nbytes = 0 if src is None else src.numel() * src.element_size()
     _check("tern_launch_probe", lib().tern_launch_probe(LAUNCH_PROBE_KINDS[kind], grid, _ptr(src), nbytes,
                                                          _ptr(sink), _stream(stream)))
@@ -743,7 +743,7 @@ def tern_mfma_peak(kind: str, iters: int, grid: int, sink=None, stream=None):
     if ops < 0:
         _check("tern_mfma_peak", 2)
     if sink is None:
-        sink = torch.empty(int(lib().tern_mfma_peak_sink_bytes(grid)) // 4, dtype=torch.int32, device="cuda")
+        sink = _new(int(lib().tern_mfma_peak_sink_bytes(grid)) // 4, torch.int32, "cuda", stream)
     _check("tern_mfma_peak", lib().tern_mfma_peak(k, iters, grid, _ptr(sink), _stream(stream)))
     return ops
 
@@ -812,11 +812,12 @@ def _new(shape, dtype, device, stream, returned=True):
     """An output or a workspace for one call.  The memory comes from the stream that will write it: what
     the current stream has freed may still be in use there.  An output that is returned is kept from
     reuse until the current stream, the caller's, is done with it too."""
-    current = None if stream is None else _torch.cuda.current_stream(device)
+    torch = _torch or _setup()
+    current = None if stream is None else torch.cuda.current_stream(device)
     if stream == current:
-        return _torch.empty(shape, dtype=dtype, device=device)
-    with _torch.cuda.stream(stream):
-        t = _torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
     if returned:
         t.record_stream(current)
     return t

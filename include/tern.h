@@ -560,8 +560,8 @@ int i8_kv_read(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, vo
  * value, weights to 2^-16 of the largest of their 64 tokens.  Prompts, on the
  * fp16 ones: weights to 2^-11 of themselves, or to 2^-34 of the largest product
  * of a weight and its block's V scale among the tokens that the row sees, and
- * 0 for results below 2^-73 (the V scales that it sees lie within 2^120 of each
- * other).  Which of the two a row gets follows from the sizes of the call and
+ * 0 for results below 2^-73 (a V scale below 2^-80 counts as that, and those
+ * that a row sees lie within 2^120 of each other).  Which of the two a row gets follows from the sizes of the call and
  * its hints (i8_kv_attend_config), not from values. */
 int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len,
                                      int64_t max_rows);

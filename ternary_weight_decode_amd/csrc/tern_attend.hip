@@ -749,7 +749,8 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
             for (int e = 0; e < 16; e += 4) {
                 u16x4 y;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = none ? (uint16_t)0 : f32_to_bf16(none_below<COLS>(acc[u][e + k] * r));
+                for (int k = 0; k < 4; ++k)
+                    y[k] = none ? (uint16_t)0 : f32_to_bf16(none_below<COLS>(acc[u][e + k] * r));
                 *(u16x4*)(dst + 32 * u + 2 * e) = y;
             }
     } else {
@@ -947,7 +948,8 @@ __global__ __launch_bounds__(JW == 1 ? 256 : 64 * JW) void kv_attend_join_kernel
     uint16_t* dst = a.out + ((int64_t)(tile.s.t0 + row) * Hq + h * a.G + (cc - (int64_t)row * a.G)) * D;
     if constexpr (JW == 1) {
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) dst[u * 64 + lane] = f32_to_bf16(sum == 0.0f ? 0.0f : none_below<COLS>(o[u] / sum));
+        for (int u = 0; u < D / 64; ++u)
+            dst[u * 64 + lane] = f32_to_bf16(sum == 0.0f ? 0.0f : none_below<COLS>(o[u] / sum));
     } else {
         __shared__ float2 sst[JW];
         if (lane == 0) sst[wave] = make_float2(top, sum);

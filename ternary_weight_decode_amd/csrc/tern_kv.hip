@@ -142,16 +142,17 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(QkTransform f, const TI*
 
 // ---- append ----------------------------------------------------------------
 // For every (sequence, touched block, key/value head) one workgroup has K and V
-// of all the block's new tokens (the block's scale needs the maximum over
-// them, and nothing else writes the block); the queries of their rows are its
-// too where tokens are few, have a workgroup of their own where those are too
-// few for the card, and four in prompts (figures at the launcher).  Loads are issued before the tokens' angles are computed,
-// once per workgroup, into LDS; up to four K and four V vectors (or four
-// queries) of each 16-lane group wait in registers.  Single tokens are bound by
-// the chain cu -> table -> rows -> scale -> codes: 5.7 us for one, calls one
-// behind another in a graph, 7.2 for 48, an empty kernel 1.95.  Prompts are bound
-// by the rows read: 4131 tokens of 32:8 heads of 128 (144 MB) take 36 us, 4.0
-// TB/s (34 in a kernel trace), where a plain copy of those bytes takes 29.
+// of all the block's new tokens (the block's scale needs the maximum over them,
+// and nothing else writes the block); the queries of their rows are its too where
+// tokens are few, have a workgroup of their own where those are too few for the
+// card, and four in prompts (figures at the launcher).  Loads are issued before
+// the tokens' angles are computed, once per workgroup, into LDS; up to four K and
+// four V vectors (or four queries) of each 16-lane group wait in registers.
+// Single tokens are bound by the chain cu -> table -> rows -> scale -> codes: 5.7
+// us for one, calls one behind another in a graph, 7.2 for 48, an empty kernel
+// 1.95.  Prompts are bound by the rows read: 4131 tokens of 32:8 heads of 128
+// (144 MB) take 36 us, 4.0 TB/s (35 in a kernel trace), where a plain copy of
+// those bytes takes 29.
 
 // the scale after values of magnitude `top` (bits, so that inf < NaN) join;
 // shift: doublings that the old codes have to follow, 31 where they vanish

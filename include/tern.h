@@ -435,6 +435,52 @@ int fv5b_head_argmax_embed(const int8_t* W, const float* S, int64_t V, int64_t K
 int fv5b_embed(const int8_t* W, const float* S, int64_t V, int64_t K, const int32_t* ids, int64_t M, float* out,
                uint16_t* out_bf16, void* stream);
 
+/* ---- 4-bit weights with group scales ----
+ *
+ * A linear of a model that was not trained in a ternary format, such as a
+ * drafter's: rounded to 16 levels, with one scale for 32, 64 or 128 neighbours
+ * of a row (block-wise scaling, [P5] section "어떻게 작동하나"; [P2], the section
+ * that compares with other stacks, sets a 4-bit GEMV beside the ternary one).
+ *   W[n][k] = t[n][k] * scale[n][k / group],  t in [-8, 7], scale fp16
+ * Layout ("4-bit blob", this library's own): K % 128 == 0, rows padded to
+ * Np = 16*ceil(N/16).  With rt = n/16, r = n%16, b = k/128, nb = K/128 and
+ * k % 128 = 32c + 8g + i: t is the four bits (two's complement) from bit
+ * 16*(i & 1) + 4*(i >> 1) on of the little-endian 32-bit word
+ *     (rt*nb + b)*256 + (g*16 + r)*4 + c
+ * (so the lane (r, g) of a matrix-core operand has a block's 32 weights in one
+ * 16-byte load), Np*K/2 bytes in all.  The scales follow, fp16: with kt = b/4,
+ * bq = b%4, nbq = min(4, nb - 4kt) and per = 128/group, the j-th of block b at
+ * element ((rt*nb + 4kt)*16 + r*nbq + bq)*per + j.  4 + 16/group bits per
+ * weight. */
+
+/* Bytes of the 4-bit blob of W[N][K]: Np*K/2 + 2*Np*K/group, or -1 for N < 0,
+ * K < 0, K % 128 != 0 or a group that is not 32, 64 or 128. */
+int64_t q4_packed_bytes(int64_t N, int64_t K, int64_t group);
+
+/* Pack t int8 [N][K] (values outside [-8, 7] are clamped to it) and scale, fp16
+ * bit patterns [N][K/group], into a blob of q4_packed_bytes(N, K, group) bytes
+ * (every byte written, padding rows as zeros).  t and packed 16-byte aligned. */
+int q4_pack(const int8_t* t, const uint16_t* scale, int64_t N, int64_t K, int64_t group, void* packed, void* stream);
+
+/* y[m][n] = sum_g scale[n][g] * sum_{k in g} t[n][k] * x[m][k].
+ *   packed  q4_pack blob of W[N][K] with this group
+ *   x       bf16 bits [M][K], 1 <= M <= TERN_MAX_M_GEMV, 16-byte aligned
+ *   y       fp32 [M][N], 4-byte aligned
+ * The products of a group are summed on the fp16 matrix cores in fp32: t is
+ * exact there, and a row's x, times a power of two, are exact to 2^-39 of the
+ * largest among their 512 neighbours of the same k / 512.  A row of x with an
+ * infinity or a NaN gives infinities or NaN, and the others what they give
+ * without it. */
+int q4_gemv(const void* packed, int64_t N, int64_t K, int64_t group, const uint16_t* x, int64_t M, float* y,
+            void* stream);
+
+/* int8 activations (tern_quantize_i8 output):
+ *   acc[m][n][g] = sum_{k in g} t[n][k] * q[m][k]   (exact int32)
+ *   y[m][n] = s_x[m] * sum_g scale[n][g] * acc[m][n][g]   (fp32)
+ *   q int8 [M][K] (16-byte aligned), s_x fp32 [M]. */
+int q4_gemv_i8(const void* packed, int64_t N, int64_t K, int64_t group, const int8_t* q, const float* s_x, int64_t M,
+               float* y, void* stream);
+
 /* ---- attention over a paged int8 cache (between the q|k|v linear and o) ----
  *
  * The models behind these linears normalise every query and key head, rotate
@@ -568,6 +614,84 @@ int64_t i8_kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64
 int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
                  int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows, uint16_t* out,
                  void* workspace, void* stream);
+
+/* ---- a tree of drafted tokens ----
+ *
+ * A draft is verified in one batched forward and the part that agrees with the
+ * target's own tokens is kept ([P2], the section on verified speculative
+ * decoding).  Several continuations at once make a tree: the newest rows of a
+ * sequence are its nodes, in an order in which every row follows the row that
+ * it continues.  A step is then
+ *   draft_tree_mask    who sees whom, and the positions for the rotation
+ *   (a layer) i8_kv_append with these positions, i8_kv_attend_tree
+ *   the head's argmax for every row, then draft_tree_accept
+ *   (a layer) i8_kv_keep: the accepted branch moves up in the cache.
+ * `batch` is the one that the rows are appended with: row j of sequence i is
+ * row cu[i] + j and stands at slot p0 + j of its cache, p0 = lens[i] - rows.
+ *   parent int32 [T]: the row (counted from cu[i]) that a row continues, or -1:
+ *   it continues the cached context.  Anything else than an earlier row of the
+ *   sequence counts as -1.
+ * A sequence has at most TERN_TREE_ROWS rows that belong to its tree; rows
+ * behind them, if any, are seen by none and kept by none. */
+#define TERN_TREE_ROWS 512
+#define TERN_TREE_WORDS 8     /* of 64 rows */
+
+/* mask uint64 [T][words], 1 <= words <= TERN_TREE_WORDS: bit a of a row's mask
+ * (word a / 64) is set for the row itself and for every row that it descends
+ * from, where a < 64 * words.
+ * pos int32 [T] (or NULL): p0 plus the rows that it descends from, the position
+ * that the token has if its branch is accepted.  A row j >= 64 * words has an
+ * empty mask and the position of its slot.  Rows of no sequence are left as
+ * they are. */
+int draft_tree_mask(const i8_kv_batch* batch, int64_t T, const int32_t* parent, int64_t words, uint64_t* mask,
+                    int32_t* pos, void* stream);
+
+/* i8_kv_attend for the rows of trees: row j of a sequence sees the cached
+ * tokens in front of the tree (positions below p0) and, of the tree, the rows
+ * a <= j whose bit its mask has (its own among them as any other).  mask as
+ * draft_tree_mask writes it, or any other; a row that sees nothing gives zeros.
+ * Arguments, workspace (i8_kv_attend_workspace_bytes) and accuracy are those of
+ * i8_kv_attend without a window.  A chain's mask gives what i8_kv_attend
+ * gives. */
+int i8_kv_attend_tree(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
+                      int64_t q_stride, float scale, const uint64_t* mask, int64_t words, int64_t max_len,
+                      int64_t max_rows, uint16_t* out, void* workspace, void* stream);
+
+/* The branch that the target's own tokens take, greedily: from row 0 on, as
+ * long as a row c (the first such) continues the current one and carries the
+ * token that the target answers there, token[c] == target[current], c is next.
+ *   token, target int32 [T]: the token that a row carries, and the one that the
+ *   target finds behind it (the head's argmax)
+ *   path int32 [nseq][width], width >= 1: the rows taken, row 0 first, then -1
+ *   count int32 [nseq] (or NULL): how many; next int32 [nseq] (or NULL): the
+ *   target's token behind the last of them, the next step's row 0.
+ * A branch longer than width ends there.  A sequence without rows, or one that
+ * leaves the T rows, has path -1, count 0 and next -1. */
+int draft_tree_accept(const i8_kv_batch* batch, int64_t T, const int32_t* parent, const int32_t* token,
+                      const int32_t* target, int64_t width, int32_t* path, int32_t* count, int32_t* next,
+                      void* stream);
+
+/* Leave of each sequence's newest rows only those of its path in the cache: the
+ * token at slot p0 + path[k] moves to slot p0 + k, for k in order up to the
+ * first entry that is not above the one before it, or no row of the tree.
+ *   lens_out int32 [nseq] (or NULL, not lens itself): p0 plus the rows kept, the
+ *   length to go on with; lens[i] for a sequence without rows or with rows
+ *   outside the T (cut at 0).
+ * A token that stays in its block keeps its codes.  One that moves into another
+ * block takes that block's scale, which grows as an append's does: with a the
+ * largest |code| * scale among the tokens that come from other blocks,
+ *   scale = old * 2^g, the least g >= 0 with a <= fl(127 * old) * 2^g,
+ *   code = clamp(rint(fl(code * its scale) / scale), -127, 127),
+ *   every other code of the block (those of tokens that stay in it among them)
+ *   = rint(code / 2^g);
+ *   where old is 0: scale = a / 127, the other codes 0.
+ * A block that takes a token whose scale is not finite gets that scale, and one
+ * that takes a value past fp32 an infinity; it then reads as NaN, as one whose
+ * own scale is not finite does.  Slots behind the kept tokens stand for nothing.  Tokens whose block is not in the table are not moved, and nothing
+ * is moved to where there is no block.
+ * The blocks from p0 on must be the sequence's own (as for the append). */
+int i8_kv_keep(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const int32_t* path, int64_t width,
+               int32_t* lens_out, void* stream);
 
 /* ---- launch-configuration introspection (no operation of the method) ----
  *

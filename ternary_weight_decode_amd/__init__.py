@@ -24,6 +24,10 @@ side of a step ``qk_norm_rope``, ``i8_kv_append``, ``i8_kv_read`` and
 ``i8_kv_attend`` (with the handles ``QkTransform``, ``I8KvCache`` and
 ``I8KvBatch``), and the launch-configuration views
 ``tern_gemv_config``, ``tern_prefill_config`` and ``i8_kv_attend_config``.
+The submodules ``q4`` (4-bit weights: ``q4_packed_bytes``, ``q4_pack``,
+``q4_gemv[_i8]``) and ``draft_tree`` (``draft_tree_mask``,
+``i8_kv_attend_tree``, ``draft_tree_accept``, ``i8_kv_keep``) hold further
+calls of the ABI, which are found here under the same names.
 """
 from __future__ import annotations
 
@@ -42,7 +46,9 @@ SYMBOLS = ("tern_strerror", "tern_last_error", "tern_abi_version", "tern_packed_
            "i8_head_gemv_packed", "i8_head_gemv_packed_i8", "i8_head_argmax_packed", "i8_head_argmax_packed_i8",
            "fv5b_head_gemv_packed", "fv5b_head_gemv_packed_i8", "fv5b_head_argmax_packed",
            "fv5b_head_argmax_packed_i8", "qk_norm_rope", "i8_kv_append", "i8_kv_read",
-           "i8_kv_attend_workspace_bytes", "i8_kv_attend", "i8_kv_attend_config")
+           "i8_kv_attend_workspace_bytes", "i8_kv_attend", "i8_kv_attend_config",
+           "q4_packed_bytes", "q4_pack", "q4_gemv", "q4_gemv_i8",
+           "draft_tree_mask", "i8_kv_attend_tree", "draft_tree_accept", "i8_kv_keep")
 _INT_STATUS = ("tern_pack", "tern_stats", "tern_quantize_i8", "tern_gemv", "tern_gemv_i8", "i8_head_gemv",
                "i8_head_gemv_i8", "tern_gemm_prefill", "tern_chain_plan", "tern_gemv_chain", "i8_head_argmax",
                "i8_head_argmax_i8", "tern5_pack", "tern5_gemv", "tern5_gemv_i8", "fv5b_head_gemv", "fv5b_head_gemv_i8",
@@ -50,7 +56,9 @@ _INT_STATUS = ("tern_pack", "tern_stats", "tern_quantize_i8", "tern_gemv", "tern
                "tern_launch_probe", "i8_head_argmax_noalloc", "i8_head_pack", "i8_head_gemv_packed",
                "i8_head_gemv_packed_i8", "i8_head_argmax_packed", "i8_head_argmax_packed_i8",
                "fv5b_head_gemv_packed", "fv5b_head_gemv_packed_i8", "fv5b_head_argmax_packed",
-               "fv5b_head_argmax_packed_i8", "qk_norm_rope", "i8_kv_append", "i8_kv_read", "i8_kv_attend")
+               "fv5b_head_argmax_packed_i8", "qk_norm_rope", "i8_kv_append", "i8_kv_read", "i8_kv_attend",
+               "q4_pack", "q4_gemv", "q4_gemv_i8", "draft_tree_mask", "i8_kv_attend_tree", "draft_tree_accept",
+               "i8_kv_keep")
 KV_BLOCK = 64
 
 _lib = None
@@ -154,6 +162,16 @@ def lib():
         L.i8_kv_attend_workspace_bytes.restype = _i64
         L.i8_kv_attend_workspace_bytes.argtypes = [_i64] * 7
         L.i8_kv_attend.argtypes = [cache, batch, _i64, _p, _i64, _i64, ctypes.c_float, _i64, _i64, _i64, _p, _p, _p]
+        L.q4_packed_bytes.restype = _i64
+        L.q4_packed_bytes.argtypes = [_i64] * 3
+        L.q4_pack.argtypes = [_p, _p, _i64, _i64, _i64, _p, _p]
+        L.q4_gemv.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _p, _p]
+        L.q4_gemv_i8.argtypes = [_p, _i64, _i64, _i64, _p, _p, _i64, _p, _p]
+        L.draft_tree_mask.argtypes = [batch, _i64, _p, _i64, _p, _p, _p]
+        L.i8_kv_attend_tree.argtypes = [cache, batch, _i64, _p, _i64, _i64, ctypes.c_float, _p, _i64, _i64, _i64, _p,
+                                        _p, _p]
+        L.draft_tree_accept.argtypes = [batch, _i64, _p, _p, _p, _i64, _p, _p, _p, _p]
+        L.i8_kv_keep.argtypes = [cache, batch, _i64, _p, _i64, _p, _p]
         for name in _INT_STATUS:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -1050,3 +1068,21 @@ def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, max
     _call("i8_kv_attend", device, stream, cache.ref, batch.ref, tokens, q.data_ptr(), hq, stride,
           d ** -0.5 if scale is None else scale, window, max_len, max_rows, out.data_ptr(), _addr(workspace))
     return out
+
+
+# ---- calls that submodules hold ----
+
+_HELD = {"q4_packed_bytes": "q4", "q4_pack": "q4", "q4_gemv": "q4", "q4_gemv_i8": "q4",
+         "TREE_ROWS": "draft_tree", "draft_tree_mask": "draft_tree", "i8_kv_attend_tree": "draft_tree",
+         "draft_tree_accept": "draft_tree", "i8_kv_keep": "draft_tree"}
+
+
+def __getattr__(name):
+    if name in _HELD:
+        import importlib
+        return getattr(importlib.import_module("." + _HELD[name], __name__), name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_HELD})

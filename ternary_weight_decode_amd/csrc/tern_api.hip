@@ -467,6 +467,68 @@ int tern5_gemv(const void* packed, int64_t N, int64_t K, const uint16_t* x, int6
 
 }  // extern "C"
 
+// ---- 4-bit weights with group scales
+
+namespace {
+
+constexpr int64_t kQ4MaxRows = 1ll << 28;   // workgroups of one launch: 2^32 threads at 256 or more each
+
+bool q4_bad(int64_t N, int64_t K, int64_t group)
+{
+    return bad_nk(N, K) || (group != 32 && group != 64 && group != 128);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t q4_packed_bytes(int64_t N, int64_t K, int64_t group)
+{
+    if (q4_bad(N, K, group)) return -1;
+    return tern::q4_code_bytes(N, K) + tern::npad16(N) * (K / group) * 2;
+}
+
+int q4_pack(const int8_t* t, const uint16_t* scale, int64_t N, int64_t K, int64_t group, void* packed, void* stream)
+{
+    if (q4_bad(N, K, group)) return TERN_E_SHAPE;
+    if (N == 0 || K == 0) return TERN_OK;
+    if (!t || !scale || !packed) return TERN_E_NULL;
+    if (!aligned16(t) || !aligned16(packed) || ((uintptr_t)scale & 1u)) return TERN_E_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    return finish(tern::launch_q4_pack(t, scale, N, K, (int)group, (uint8_t*)packed, (hipStream_t)stream));
+}
+
+int q4_gemv(const void* packed, int64_t N, int64_t K, int64_t group, const uint16_t* x, int64_t M, float* y,
+            void* stream)
+{
+    if (q4_bad(N, K, group) || M < 0 || M > TERN_MAX_M_GEMV || N > kQ4MaxRows) return TERN_E_SHAPE;
+    if (N == 0 || M == 0) return TERN_OK;
+    if (!y || (K > 0 && (!packed || !x))) return TERN_E_NULL;
+    if ((packed && !aligned16(packed)) || (x && !aligned16(x)) || !aligned4(y)) return TERN_E_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    if (K == 0) return finish(tern::launch_fill_zero(y, M * N * 4, (hipStream_t)stream));
+    return finish(tern::launch_q4_gemv_bf16((const uint8_t*)packed, N, K, (int)group, x, M, y, (hipStream_t)stream));
+}
+
+int q4_gemv_i8(const void* packed, int64_t N, int64_t K, int64_t group, const int8_t* q, const float* s_x, int64_t M,
+               float* y, void* stream)
+{
+    if (q4_bad(N, K, group) || M < 0 || M > TERN_MAX_M_GEMV || N > kQ4MaxRows) return TERN_E_SHAPE;
+    if (N == 0 || M == 0) return TERN_OK;
+    if (!y || !s_x || (K > 0 && (!packed || !q))) return TERN_E_NULL;
+    if ((packed && !aligned16(packed)) || (q && !aligned16(q)) || !aligned4(y) || !aligned4(s_x))
+        return TERN_E_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    if (K == 0) return finish(tern::launch_fill_zero(y, M * N * 4, (hipStream_t)stream));
+    return finish(
+        tern::launch_q4_gemv_i8((const uint8_t*)packed, N, K, (int)group, q, s_x, M, y, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
 // ---- block-scaled (FV5B-style) head and embedding rows
 
 namespace {
@@ -615,6 +677,7 @@ namespace {
 constexpr int64_t kKvMaxRows = 1 << 24;     // rows of a per-token tensor, sequences of a batch
 constexpr int64_t kKvMaxHeads = 1024;
 constexpr int64_t kKvMaxGrid = (1 << 24) - 1; // workgroups of one launch: 2^32 threads at 256 each
+constexpr int64_t kTreeMaxWidth = 1 << 16;    // entries of an accepted branch
 constexpr int64_t kKvMaxPairs = 1 << 25;      // (row, query head) pairs of one attention call
 
 bool kv_bad_d(int64_t D) { return D != 64 && D != 128; }
@@ -662,6 +725,13 @@ int kv_check_pointers(const i8_kv_cache* c, const i8_kv_batch* b)
         !aligned4(b->lens) || (b->table && !aligned4(b->table)))
         return TERN_E_ALIGN;
     return TERN_OK;
+}
+
+// the batch of a call that reads no cache
+int tree_check(const i8_kv_batch* b, int64_t T)
+{
+    if (!b) return TERN_E_NULL;
+    return b->nseq < 0 || b->nseq > kKvMaxGrid / 2 || T < 0 || T > kKvMaxRows ? TERN_E_SHAPE : TERN_OK;
 }
 
 tern::KvCache kv_cache(const i8_kv_cache* c) { return {c->codes, c->scales, c->blocks, (int)c->heads}; }
@@ -764,7 +834,77 @@ int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, 
     if (!aligned16(q) || !aligned16(out) || (need > 0 && !aligned16(workspace))) return TERN_E_ALIGN;
     if ((rc = check_device())) return rc;
     return finish(tern::launch_kv_attend(kv_cache(cache), kv_batch(batch, T), cache->D, q, Hq, q_stride, scale,
-                                         window, max_len, max_rows, out, workspace, (hipStream_t)stream));
+                                         window, nullptr, 0, max_len, max_rows, out, workspace, (hipStream_t)stream));
+}
+
+int i8_kv_attend_tree(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
+                      int64_t q_stride, float scale, const uint64_t* mask, int64_t words, int64_t max_len,
+                      int64_t max_rows, uint16_t* out, void* workspace, void* stream)
+{
+    bool empty = false;
+    int rc = kv_check_shape(cache, batch, T, &empty);
+    if (rc) return rc;
+    const int64_t need = i8_kv_attend_workspace_bytes(T, Hq, cache->heads, cache->D, batch->nseq, max_len,
+                                                      max_rows);
+    if (need < 0 || words < 1 || words > TERN_TREE_WORDS || !std::isfinite(scale) ||
+        kv_bad_stride(Hq, cache->D, q_stride, TERN_BF16))
+        return TERN_E_SHAPE;
+    if (empty) return TERN_OK;
+    if ((rc = kv_check_pointers(cache, batch))) return rc;
+    if (!q || !out || !mask || (need > 0 && !workspace)) return TERN_E_NULL;
+    if (!aligned16(q) || !aligned16(out) || ((uintptr_t)mask & 7u) || (need > 0 && !aligned16(workspace)))
+        return TERN_E_ALIGN;
+    if ((rc = check_device())) return rc;
+    return finish(tern::launch_kv_attend(kv_cache(cache), kv_batch(batch, T), cache->D, q, Hq, q_stride, scale, 0,
+                                         mask, (int)words, max_len, max_rows, out, workspace, (hipStream_t)stream));
+}
+
+int i8_kv_keep(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const int32_t* path, int64_t width,
+               int32_t* lens_out, void* stream)
+{
+    bool empty = false;
+    int rc = kv_check_shape(cache, batch, T, &empty);
+    if (rc) return rc;
+    if (width < 1 || width > kTreeMaxWidth || 2 * batch->nseq * cache->heads > kKvMaxGrid) return TERN_E_SHAPE;
+    if (batch->nseq == 0) return TERN_OK;
+    if ((rc = kv_check_pointers(cache, batch))) return rc;
+    if (!path) return TERN_E_NULL;
+    if (!aligned4(path) || (lens_out && !aligned4(lens_out))) return TERN_E_ALIGN;
+    if ((rc = check_device())) return rc;
+    return finish(tern::launch_kv_keep(kv_cache(cache), kv_batch(batch, T), cache->D, path, (int)width, lens_out,
+                                       (hipStream_t)stream));
+}
+
+int draft_tree_mask(const i8_kv_batch* batch, int64_t T, const int32_t* parent, int64_t words, uint64_t* mask,
+                    int32_t* pos, void* stream)
+{
+    int rc = tree_check(batch, T);
+    if (rc) return rc;
+    if (words < 1 || words > TERN_TREE_WORDS) return TERN_E_SHAPE;
+    if (T == 0 || batch->nseq == 0) return TERN_OK;
+    if (!batch->cu || !batch->lens || !parent || !mask) return TERN_E_NULL;
+    if (!aligned4(batch->cu) || !aligned4(batch->lens) || !aligned4(parent) || ((uintptr_t)mask & 7u) ||
+        (pos && !aligned4(pos)))
+        return TERN_E_ALIGN;
+    if ((rc = check_device())) return rc;
+    return finish(
+        tern::launch_tree_mask(kv_batch(batch, T), parent, (int)words, mask, pos, (hipStream_t)stream));
+}
+
+int draft_tree_accept(const i8_kv_batch* batch, int64_t T, const int32_t* parent, const int32_t* token,
+                      const int32_t* target, int64_t width, int32_t* path, int32_t* count, int32_t* next, void* stream)
+{
+    int rc = tree_check(batch, T);
+    if (rc) return rc;
+    if (width < 1 || width > kTreeMaxWidth) return TERN_E_SHAPE;
+    if (batch->nseq == 0) return TERN_OK;
+    if (!batch->cu || !path || (T > 0 && (!parent || !token || !target))) return TERN_E_NULL;
+    if (!aligned4(batch->cu) || !aligned4(parent) || !aligned4(token) || !aligned4(target) || !aligned4(path) ||
+        (count && !aligned4(count)) || (next && !aligned4(next)))
+        return TERN_E_ALIGN;
+    if ((rc = check_device())) return rc;
+    return finish(tern::launch_tree_accept(kv_batch(batch, T), parent, token, target, (int)width, path, count, next,
+                                           (hipStream_t)stream));
 }
 
 }  // extern "C"

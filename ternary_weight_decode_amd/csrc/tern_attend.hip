@@ -111,6 +111,8 @@ struct AttArgs {
     uint32_t* start;           // [nseq] where each sequence starts in the line, then the total
     int64_t q_stride;
     int window;
+    const uint64_t* mask;      // TREE: [T][words], the newest rows that a row sees
+    int words;
     float scale;
     int G;
     int groups;                // workgroups that share the line; 0: one workgroup for each unit
@@ -173,6 +175,20 @@ __device__ __forceinline__ uint32_t att_stretch(uint32_t total, int groups)
     return (total + turn - 1) / turn * kTurn;
 }
 
+// A row's tree: the words of its mask in LDS, behind them the position of the
+// tree's first row.  The 64 bits of the tokens from `at` on that a row sees
+// whose last token is `last`: all in front of the tree, of the tree those of
+// the mask.
+__device__ __forceinline__ uint64_t tree_bits(const uint64_t* row, int words, int p0, int at, int last)
+{
+    const int o = at - p0, w = o >> 6, sh = o & 63;
+    const uint64_t lo = w >= 0 && w < words ? row[w] : 0, hi = w + 1 >= 0 && w + 1 < words ? row[w + 1] : 0;
+    uint64_t bits = sh ? lo >> sh | hi << (64 - sh) : lo;
+    if (o < 0) bits |= o > -64 ? (1ull << -o) - 1 : ~0ull;
+    const int most = last - at;
+    return most >= 63 ? bits : most < 0 ? 0 : bits & ((2ull << most) - 1);
+}
+
 // bits 0, N, 2 N, ...
 template <int N>
 constexpr uint64_t every()
@@ -183,8 +199,9 @@ constexpr uint64_t every()
 }
 
 // blocks [begin, end) of one unit; whole: the result is written, else it is
-// part `slot` of the unit.  STREAM: codes are read past the caches.
-template <int D, int X, bool STREAM>
+// part `slot` of the unit.  STREAM: codes are read past the caches.  TREE: of
+// the newest rows a row sees those of its mask.
+template <int D, int X, bool STREAM, bool TREE>
 __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b, const AttArgs& a,
                                               const AttTile& tile, int h, int begin, int end, bool whole,
                                               uint32_t slot)
@@ -202,6 +219,8 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
     u32x4 qhi[S], qlo[S];
     float rowf;
     int first, last;
+    // a wave's own columns' masks: no other wave waits for them
+    __shared__ uint64_t smask[TREE ? kAttWaves : 1][16][TREE ? kTreeWords + 1 : 1];
     {
         const int col = 16 * group + n;
         const bool live = col < tile.cols;
@@ -211,6 +230,11 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
         const int pos = tile.s.p0 + j;
         first = live ? att_first(pos, a.window) : 0;
         last = live ? att_last(pos, limit) : INT32_MAX;
+        if constexpr (TREE) {
+            const uint64_t* words = a.mask + (int64_t)(tile.s.t0 + j) * a.words;
+            for (int w = g; w < a.words; w += 4) smask[wave][n][w] = words[w];
+            __builtin_amdgcn_wave_barrier();         // read by the column's other lanes
+        }
         u32x4 raw[S][2];
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -316,8 +340,21 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int s = 0; s < S; ++s) kr[t][s] = load(next, kib * (t * S + s));
-            const bool sees = first <= at + 63 && last >= at;
-            if (__any(first > at || last < at + 63)) {
+            bool sees;
+            if constexpr (TREE) {
+                sees = true;
+                if (at + 63 >= tile.s.p0) {
+                    const uint64_t bits = tree_bits(smask[wave][n], a.words, tile.s.p0, at, last);
+                    sees = bits != 0;
+                    const uint64_t mine = bits >> 4 * g;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        x[e] = mine >> (16 * (e >> 2) + (e & 3)) & 1 ? x[e] : -INFINITY;
+                }
+            } else {
+                sees = first <= at + 63 && last >= at;
+            }
+            if (!TREE && __any(first > at || last < at + 63)) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int p = at + 16 * (e >> 2) + 4 * g + (e & 3);
@@ -490,13 +527,14 @@ __device__ __forceinline__ void half_turn()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int D>
+template <int D, bool TREE>
 __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch& b, const AttArgs& a,
                                                 const AttTile& tile, int h, int begin, int end, bool whole,
                                                 uint32_t slot)
 {
     constexpr int S = D / 64, ST = D / 16, DT = D / 32, COLS = 32 * kTileWaves;
     __shared__ u32x4 kbuf[2][kKvBlock * D / 8], vbuf[2][kKvBlock * D / 8];
+    __shared__ uint64_t smask[TREE ? kTileWaves : 1][32][TREE ? kTreeWords + 1 : 1];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int half = lane >> 5;
     const bool second = wave >= kTileWaves / 2;      // waves i and i + 4 share a SIMD
@@ -511,6 +549,11 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
     const int pos = tile.s.p0 + j;
     const int first = live ? att_first(pos, a.window) : 0;
     const int last = live ? att_last(pos, att_limit(b)) : INT32_MAX;
+    if constexpr (TREE) {
+        const uint64_t* words = a.mask + (int64_t)(tile.s.t0 + j) * a.words;
+        for (int w = half; w < a.words; w += 2) smask[wave][lane & 31][w] = words[w];
+        __builtin_amdgcn_wave_barrier();             // read by the column's other lane
+    }
     int all_first = first, all_last = last;           // keys that every column sees
     for (int off = 1; off < 32; off <<= 1) {
         const int x = __shfl_xor(all_first, off), y = __shfl_xor(all_last, off);
@@ -659,7 +702,16 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[t][e] = fmaf(x[t][e], f, base);
-            if (all_first > at || all_last < at + 63) {
+            if constexpr (TREE) {
+                if (at + 63 >= tile.s.p0) {
+                    const uint64_t mine = tree_bits(smask[wave][lane & 31], a.words, tile.s.p0, at, last) >> 4 * half;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            x[t][e] = mine >> (32 * t + 8 * (e >> 2) + (e & 3)) & 1 ? x[t][e] : -INFINITY;
+                }
+            } else if (all_first > at || all_last < at + 63) {
                 const int lo = first - at - 4 * half, hi = last - at - 4 * half;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
@@ -773,7 +825,7 @@ __device__ __forceinline__ void attend_tile_f16(const KvCache& c, const KvBatch&
 template <int COLS>
 constexpr int att_threads() { return COLS <= 64 ? 64 * kAttWaves : 64 * kTileWaves; }
 
-template <int D, int COLS, bool STREAM>
+template <int D, int COLS, bool STREAM, bool TREE>
 __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_attend_kernel(KvCache c, KvBatch b,
                                                                                             AttArgs a)
 {
@@ -864,8 +916,9 @@ __global__ __launch_bounds__(att_threads<COLS>(), COLS <= 64 ? 3 : 2) void kv_at
             att_uniform(tile);
             end = end < tile.nblk ? end : tile.nblk;
             if (begin < end || begin == 0) {
-                if constexpr (COLS <= 64) attend_blocks<D, COLS / 16, STREAM>(c, b, a, tile, h, begin, end, whole, slot);
-                else attend_tile_f16<D>(c, b, a, tile, h, begin, end, whole, slot);
+                if constexpr (COLS <= 64)
+                    attend_blocks<D, COLS / 16, STREAM, TREE>(c, b, a, tile, h, begin, end, whole, slot);
+                else attend_tile_f16<D, TREE>(c, b, a, tile, h, begin, end, whole, slot);
             }
         }
         if (x >= x1) break;
@@ -1115,15 +1168,15 @@ int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t 
     return p.bytes();
 }
 
-template <int D, int COLS>
+template <int D, int COLS, bool TREE>
 static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, int64_t items, bool streams,
                          hipStream_t stream)
 {
     const int64_t grid = a.groups ? a.groups : items * c.heads;
     if (COLS == 16 && streams)
-        kv_attend_kernel<D, COLS, COLS == 16><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
+        kv_attend_kernel<D, COLS, COLS == 16, TREE><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
     else
-        kv_attend_kernel<D, COLS, false><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
+        kv_attend_kernel<D, COLS, false, TREE><<<(unsigned)grid, att_threads<COLS>(), 0, stream>>>(c, b, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.groups == 0) return e;
     int64_t rows = (int64_t)b.T * c.heads * a.G;
@@ -1138,15 +1191,15 @@ static hipError_t attend(const KvCache& c, const KvBatch& b, const AttArgs& a, i
     return hipGetLastError();
 }
 
-template <int D>
+template <int D, bool TREE>
 static hipError_t attend_part(const KvCache& c, const KvBatch& b, const AttArgs& a, const AttPart& p,
                               hipStream_t stream)
 {
     switch (p.cols) {
-    case 16: return attend<D, 16>(c, b, a, p.items, p.streams, stream);
-    case 32: return attend<D, 32>(c, b, a, p.items, p.streams, stream);
-    case 64: return attend<D, 64>(c, b, a, p.items, p.streams, stream);
-    default: return attend<D, 256>(c, b, a, p.items, p.streams, stream);
+    case 16: return attend<D, 16, TREE>(c, b, a, p.items, p.streams, stream);
+    case 32: return attend<D, 32, TREE>(c, b, a, p.items, p.streams, stream);
+    case 64: return attend<D, 64, TREE>(c, b, a, p.items, p.streams, stream);
+    default: return attend<D, 256, TREE>(c, b, a, p.items, p.streams, stream);
     }
 }
 
@@ -1186,8 +1239,8 @@ int kv_attend_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t ns
 }
 
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
-                            int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows,
-                            uint16_t* out, void* workspace, hipStream_t stream)
+                            int64_t q_stride, float scale, int64_t window, const uint64_t* mask, int words,
+                            int64_t max_len, int64_t max_rows, uint16_t* out, void* workspace, hipStream_t stream)
 {
     const AttPlan plan = att_choose(b.T, Hq, c.heads, D, b.nseq, b.table_width, window, max_len, max_rows);
     uint8_t* ws = (uint8_t*)workspace;
@@ -1202,13 +1255,18 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const
         ws += p.bytes();
         a.q_stride = q_stride;
         a.window = window < INT32_MAX ? (int)window : 0;      // one that nothing is as far as
+        a.mask = mask;
+        a.words = words;
         a.scale = scale;
         a.G = (int)(Hq / c.heads);
         a.min_cols = p.min_cols;
         a.max_cols = p.max_cols;
         a.by_sequence = p.max_cols < INT32_MAX && (int64_t)b.nseq * p.max_cols < (int64_t)b.T * a.G;
         a.groups = p.groups;
-        const hipError_t e = D == 128 ? attend_part<128>(c, b, a, p, stream) : attend_part<64>(c, b, a, p, stream);
+        const hipError_t e = mask ? (D == 128 ? attend_part<128, true>(c, b, a, p, stream)
+                                              : attend_part<64, true>(c, b, a, p, stream))
+                                  : (D == 128 ? attend_part<128, false>(c, b, a, p, stream)
+                                              : attend_part<64, false>(c, b, a, p, stream));
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

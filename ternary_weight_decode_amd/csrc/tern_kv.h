@@ -91,6 +91,23 @@ __device__ __forceinline__ bool kv_find(const KvBatch& b, int64_t item, int mul,
     return local >= 0;
 }
 
+// Sequence i; all lanes of a wave call it together.  False: no rows, rows
+// outside the tensors, or cu descends up to there (s.n is 0 then, and s.p0 the
+// sequence's length).
+__device__ __forceinline__ bool kv_seq(const KvBatch& b, int i, KvSeq& s)
+{
+    const int lane = threadIdx.x & 63;
+    bool falls = false;
+    for (int c = lane; c <= i; c += 64) falls |= b.cu[c + 1] < b.cu[c];
+    s.i = i;
+    s.t0 = b.cu[i];
+    s.n = b.cu[i + 1] - s.t0;
+    const bool good = !__any(falls) && s.t0 >= 0 && (int64_t)s.t0 + s.n <= b.T && s.n > 0;
+    if (!good) s.n = 0;
+    s.p0 = kv_length(b, i) - s.n;
+    return good;
+}
+
 // Physical block of a sequence's block, -1 where there is none.
 __device__ __forceinline__ int kv_block(const KvBatch& b, const KvCache& c, int seq, int block)
 {

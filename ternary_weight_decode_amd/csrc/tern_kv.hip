@@ -502,6 +502,159 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, KvBatch b, TO* 
     }
 }
 
+// ---- keep ------------------------------------------------------------------
+// The accepted branch of a tree moves up: slot p0 + k takes the token of slot
+// p0 + path[k].  One workgroup per (sequence, head, side): a branch is a few
+// tokens in one or two blocks, so the launch is bound by the chain from cu over
+// the path and the table to the scales and the codes.  Blocks go one after
+// another.  A path ascends, so a block's tokens come from itself or from blocks
+// behind it, whose bytes are as they were: each block's tokens are taken to LDS
+// before anything of it is written.
+
+// The first entry of a path that is no row of the tree or not above the one
+// before it; all threads of a workgroup of 256 call it.
+__device__ __forceinline__ int path_length(const int32_t* path, int width, int rows, int* found)
+{
+    const int most = width < rows ? width : rows;      // it ascends: not more entries than rows
+    if (threadIdx.x == 0) *found = most;
+    __syncthreads();
+    for (int k = threadIdx.x; k < most; k += 256) {
+        const int r = path[k], before = k > 0 ? path[k - 1] : -1;
+        if (r <= before || r < 0 || r >= rows) {
+            atomicMin(found, k);
+            break;
+        }
+    }
+    __syncthreads();
+    return *found;
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void kv_keep_kernel(KvCache c, KvBatch b, const int32_t* paths, int width,
+                                                      int32_t* lens_out)
+{
+    __shared__ __align__(16) int8_t code[kKvBlock][D];
+    __shared__ int64_t from[kKvBlock];                 // unit (block and head) of a token's source, -1: none
+    __shared__ float its[kKvBlock];                    // the source's scale where it is another block's
+    __shared__ int slot[kKvBlock];
+    __shared__ int found;
+    __shared__ uint32_t tops[4];
+    const int side = blockIdx.x & 1, h = (blockIdx.x >> 1) % c.heads, i = (blockIdx.x >> 1) / c.heads;
+    const int32_t* path = paths + (int64_t)i * width;
+    KvSeq s;
+    const bool any = kv_seq(b, i, s);
+    const int kept = any ? path_length(path, width, s.n < kTreeRows ? s.n : kTreeRows, &found) : 0;
+    if (lens_out && side == 0 && h == 0 && threadIdx.x == 0) {
+        const int len = any ? s.p0 + kept : s.p0;
+        lens_out[i] = len > 0 ? len : 0;
+    }
+    // tokens in front of position 0 are not there
+    for (int k0 = s.p0 < 0 ? -s.p0 : 0; k0 < kept;) {
+        const int block = (s.p0 + k0) >> 6, base = (s.p0 + k0) & 63;
+        const int n = kept - k0 < kKvBlock - base ? kept - k0 : kKvBlock - base;
+        const int phys = kv_block(b, c, s.i, block);
+        bool moves = false;
+        if (threadIdx.x < n) {
+            const int r = path[k0 + threadIdx.x], p = s.p0 + r;
+            const int source = kv_block(b, c, s.i, p >> 6);
+            const int64_t unit = (int64_t)source * c.heads + h;
+            slot[threadIdx.x] = p & 63;
+            from[threadIdx.x] = source < 0 ? -1 : unit;
+            its[threadIdx.x] = source >= 0 && source != phys ? c.scales[unit * 2 + side] : 0.0f;
+            moves = r != k0 + (int)threadIdx.x;
+        }
+        moves = __syncthreads_or(moves);
+        if (phys >= 0 && moves) {
+            const int64_t unit = (int64_t)phys * c.heads + h;
+            int8_t* const mine = c.codes + (unit * 2 + side) * (kKvBlock * D);
+            // the tokens to LDS, and the largest value that comes from elsewhere
+            uint32_t top = 0;
+            const auto sized = [&](int t, int most) {
+                if (from[t] != unit && from[t] >= 0) {
+                    // of a scale that is not finite, itself (not 0 times it)
+                    const float scale = fabsf(its[t]), value = scale < INFINITY ? (float)most * scale : scale;
+                    const uint32_t x = __builtin_bit_cast(uint32_t, value);
+                    top = x > top ? x : top;
+                }
+            };
+            if (side == 0) {
+                for (int e = threadIdx.x; e < n * (D / 16); e += 256) {
+                    const int t = e / (D / 16), d = e % (D / 16) * 16;
+                    if (from[t] < 0) continue;
+                    const u32x4 x = *(const u32x4*)(c.codes + from[t] * 2 * (kKvBlock * D) + kv_k_byte<D>(slot[t], d));
+                    *(u32x4*)&code[t][d] = x;
+                    int most = 0;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int v = (int8_t)(x[j >> 2] >> 8 * (j & 3));
+                        most = v > most ? v : -v > most ? -v : most;
+                    }
+                    sized(t, most);
+                }
+            } else {
+                for (int e = threadIdx.x; e < n * D; e += 256) {
+                    const int t = e / D, d = e % D;
+                    if (from[t] < 0) continue;
+                    const int8_t x = c.codes[(from[t] * 2 + 1) * (kKvBlock * D) + kv_v_byte(slot[t], d)];
+                    code[t][d] = x;
+                    sized(t, x < 0 ? -x : x);
+                }
+            }
+            for (int off = 1; off < 64; off <<= 1) {
+                const uint32_t x = __shfl_xor(top, off);
+                top = x > top ? x : top;
+            }
+            if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+            __syncthreads();                           // code, tops
+#pragma unroll
+            for (int w = 0; w < 4; ++w) top = tops[w] > top ? tops[w] : top;
+            float scale = c.scales[unit * 2 + side];
+            int shift = 0;
+            if (top > 0) {
+                const float old = scale;
+                scale = join_scale(old, top, false, shift);
+                if (old == 0.0f) shift = 31;
+            }
+            __syncthreads();                           // every thread has the old scale
+            if (threadIdx.x == 0 && top > 0) c.scales[unit * 2 + side] = scale;
+            // whole chunks: K 16 dims of a token, V 16 tokens of a dim
+            for (int i16 = threadIdx.x; i16 < kKvBlock * D / 16; i16 += 256) {
+                const int r = i16 & 15, g = i16 >> 4 & 3, rest = i16 >> 6;
+                const auto put = [&](uint32_t& w, int byte, int t, int d) {
+                    if (t < 0 || t >= n || from[t] < 0) return;
+                    uint32_t x = (uint32_t)(int)code[t][d] & 0xFFu;
+                    if (from[t] != unit) x = quantise((float)code[t][d] * its[t], scale);
+                    else if (shift) x = shift_codes(x, shift) & 0xFFu;
+                    w = (w & ~(0xFFu << 8 * byte)) | x << 8 * byte;
+                };
+                bool hit = shift != 0;
+                if (side == 0) {
+                    const int t = rest / (D / 64) * 16 + r - base;
+                    hit |= t >= 0 && t < n;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) hit |= 16 * e + 4 * g + 3 >= base && 16 * e + 4 * g < base + n;
+                }
+                if (!hit) continue;
+                u32x4 x = *(const u32x4*)(mine + 16 * i16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t w = shift ? shift_codes(x[e], shift) : x[e];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (side == 0) put(w, j, rest / (D / 64) * 16 + r - base, rest % (D / 64) * 64 + 16 * g + 4 * e + j);
+                        else put(w, j, 16 * e + 4 * g + j - base, rest * 16 + r);
+                    }
+                    x[e] = w;
+                }
+                *(u32x4*)(mine + 16 * i16) = x;
+            }
+        }
+        __syncthreads();                               // LDS is used again
+        k0 += n;
+    }
+}
+
 // ---- launchers -------------------------------------------------------------
 template <int D, typename TI, typename TO>
 static hipError_t norm_rope(const QkTransform& f, int64_t T, const void* q, int64_t Hq, int64_t q_stride,
@@ -573,6 +726,15 @@ hipError_t launch_kv_read(const KvCache& c, const KvBatch& b, int64_t D, void* k
         else TERN_RD(64, float);
     }
 #undef TERN_RD
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_keep(const KvCache& c, const KvBatch& b, int64_t D, const int32_t* path, int width,
+                          int32_t* lens_out, hipStream_t stream)
+{
+    const unsigned grid = (unsigned)((int64_t)b.nseq * c.heads * 2);
+    if (D == 128) kv_keep_kernel<128><<<grid, 256, 0, stream>>>(c, b, path, width, lens_out);
+    else kv_keep_kernel<64><<<grid, 256, 0, stream>>>(c, b, path, width, lens_out);
     return hipGetLastError();
 }
 

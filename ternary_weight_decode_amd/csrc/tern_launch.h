@@ -131,6 +131,15 @@ hipError_t launch_gemv5_bf16(const uint8_t* packed, int64_t N, int64_t K, const 
 hipError_t launch_gemv5_i8(const uint8_t* packed, int64_t N, int64_t K, const int8_t* q, const float* s_x, int64_t M,
                            float* y, int32_t* acc, hipStream_t stream);
 
+// ---- 4-bit weights with group scales ----
+__host__ __device__ inline int64_t q4_code_bytes(int64_t N, int64_t K) { return npad16(N) * K / 2; }
+hipError_t launch_q4_pack(const int8_t* t, const uint16_t* scale, int64_t N, int64_t K, int group, uint8_t* packed,
+                          hipStream_t stream);
+hipError_t launch_q4_gemv_bf16(const uint8_t* packed, int64_t N, int64_t K, int group, const uint16_t* x, int64_t M,
+                               float* y, hipStream_t stream);
+hipError_t launch_q4_gemv_i8(const uint8_t* packed, int64_t N, int64_t K, int group, const int8_t* q,
+                             const float* s_x, int64_t M, float* y, hipStream_t stream);
+
 // ---- query/key norm with rotation, paged int8 cache and its attention ----
 hipError_t launch_qk_norm_rope(const QkTransform& f, int64_t T, int64_t D, const void* q, int64_t Hq,
                                int64_t q_stride, const void* k, int64_t Hk, int64_t k_stride, bool in_bf16,
@@ -144,9 +153,20 @@ int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t 
                                   int64_t max_rows);
 int kv_attend_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
                      int64_t window, int64_t max_len, int64_t max_rows, int64_t* out);
+// mask NULL: every row sees all in front of it (and the window); else words of it a row, and no window
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
-                            int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows,
-                            uint16_t* out, void* workspace, hipStream_t stream);
+                            int64_t q_stride, float scale, int64_t window, const uint64_t* mask, int words,
+                            int64_t max_len, int64_t max_rows, uint16_t* out, void* workspace, hipStream_t stream);
+
+// ---- trees of drafted tokens ----
+constexpr int kTreeRows = 512;                    // rows of a tree
+constexpr int kTreeWords = kTreeRows / 64;
+hipError_t launch_tree_mask(const KvBatch& b, const int32_t* parent, int words, uint64_t* mask, int32_t* pos,
+                            hipStream_t stream);
+hipError_t launch_tree_accept(const KvBatch& b, const int32_t* parent, const int32_t* token, const int32_t* target,
+                              int width, int32_t* path, int32_t* count, int32_t* next, hipStream_t stream);
+hipError_t launch_kv_keep(const KvCache& c, const KvBatch& b, int64_t D, const int32_t* path, int width,
+                          int32_t* lens_out, hipStream_t stream);
 
 // ---- matrix-core throughput probe (measurement aid) ----
 double mfma_peak_ops(int kind, int64_t iters, int64_t grid);

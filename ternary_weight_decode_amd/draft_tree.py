@@ -1,0 +1,112 @@
+"""A tree of drafted tokens over the paged int8 cache: the newest rows of a sequence are the tree's nodes, row j
+continuing row parent[j] (an earlier one, or -1: the cached context).  One step:
+
+    mask, pos = tw.draft_tree_mask(batch, parent, words)             # once for all layers
+    q = tw.i8_kv_append(cache, batch, f, k, v, q=q, pos=pos)         # a layer
+    o = tw.i8_kv_attend_tree(cache, batch, q, mask)
+    ...                                                              # head: target = argmax of every row
+    path, count, following = tw.draft_tree_accept(batch, parent, token, target)
+    lens = tw.i8_kv_keep(cache, batch, tokens, path)                 # a layer
+"""
+from __future__ import annotations
+
+import ternary_weight_decode_amd as _tw
+
+_torch = _tw._setup()
+TREE_ROWS = 512
+TREE_WORDS = TREE_ROWS // 64
+
+
+def _int32(t, name, shape, device):
+    _tw._vec(t, name, _torch.int32, shape, device)
+
+
+def draft_tree_mask(batch, parent, words: int = 1, mask=None, pos=None, stream=None):
+    """Who descends from whom: parent int32 [T] -> (mask int64 [T, words], 64 rows of the tree to a word;
+    pos int32 [T], the positions for the rotation).  words: enough for the largest tree, at most 8."""
+    device = batch.device
+    _int32(parent, "parent", (None,), device)
+    tokens = parent.shape[0]
+    if not 1 <= words <= TREE_WORDS:
+        raise RuntimeError(f"words is {words}, expected 1 to {TREE_WORDS}")
+    if mask is None:
+        mask = _tw._new((tokens, words), _torch.int64, device, stream)
+    else:
+        _tw._vec(mask, "mask", _torch.int64, (tokens, words), device)
+    if pos is None:
+        pos = _tw._new((tokens,), _torch.int32, device, stream)
+    else:
+        _int32(pos, "pos", (tokens,), device)
+    _tw._call("draft_tree_mask", device, stream, batch.ref, tokens, parent.data_ptr(), words, mask.data_ptr(),
+              pos.data_ptr())
+    return mask, pos
+
+
+def i8_kv_attend_tree(cache, batch, q, mask, scale=None, max_len=None, max_rows: int = 0, out=None, workspace=None,
+                      stream=None):
+    """Attention of q bf16 [T, Hq, D] over the batch's cached tokens -> bf16 [T, Hq, D]: a row sees what stands in
+    front of its tree, and of the tree the rows up to its own whose bits its mask has (int64 [T, words]).
+    Everything else, the workspace too, as i8_kv_attend."""
+    device, d = _tw._kv_device(cache, batch), cache.d
+    tokens, hq, stride = _tw._rows(q, "q", _torch.bfloat16, device, None, d, None)
+    _tw._vec(mask, "mask", _torch.int64, (tokens, None), device)
+    if max_len is None:
+        max_len = batch.width * _tw.KV_BLOCK or 1
+    if out is None:
+        out = _tw._new((tokens, hq, d), _torch.bfloat16, device, stream)
+    else:
+        _tw._vec(out, "out", _torch.bfloat16, (tokens, hq, d), device)
+    need = _tw.lib().i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len, max_rows)
+    if workspace is None:
+        if need > 0:
+            workspace = _tw._new(need, _torch.uint8, device, stream, returned=False)
+    elif workspace.get_device() != device or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < need:
+        raise RuntimeError(f"workspace must be a contiguous tensor of at least {need} bytes on device {device}")
+    _tw._call("i8_kv_attend_tree", device, stream, cache.ref, batch.ref, tokens, q.data_ptr(), hq, stride,
+              d ** -0.5 if scale is None else scale, mask.data_ptr(), mask.shape[1], max_len, max_rows,
+              out.data_ptr(), _tw._addr(workspace))
+    return out
+
+
+def draft_tree_accept(batch, parent, token, target, width: int = 64, path=None, count=None, following=None,
+                      stream=None):
+    """The branch that the target's own tokens take: token int32 [T], what a row carries; target int32 [T], what the
+    target answers there -> (path int32 [nseq, width], rows of each tree and then -1; count int32 [nseq];
+    following int32 [nseq], the target's token behind the last)."""
+    device, nseq = batch.device, batch.nseq
+    _int32(parent, "parent", (None,), device)
+    tokens = parent.shape[0]
+    _int32(token, "token", (tokens,), device)
+    _int32(target, "target", (tokens,), device)
+    if path is None:
+        path = _tw._new((nseq, width), _torch.int32, device, stream)
+    else:
+        _int32(path, "path", (nseq, width), device)
+    if count is None:
+        count = _tw._new((nseq,), _torch.int32, device, stream)
+    else:
+        _int32(count, "count", (nseq,), device)
+    if following is None:
+        following = _tw._new((nseq,), _torch.int32, device, stream)
+    else:
+        _int32(following, "following", (nseq,), device)
+    _tw._call("draft_tree_accept", device, stream, batch.ref, tokens, parent.data_ptr(), token.data_ptr(),
+              target.data_ptr(), width, path.data_ptr(), count.data_ptr(), following.data_ptr())
+    return path, count, following
+
+
+def i8_kv_keep(cache, batch, tokens: int, path, lens_out=None, stream=None):
+    """Of the batch's `tokens` newest rows only those of path int32 [nseq, width] stay in the cache, moved up to
+    where their tree began -> int32 [nseq], the lengths to go on with."""
+    device = _tw._kv_device(cache, batch)
+    _int32(path, "path", (batch.nseq, None), device)
+    if lens_out is None:
+        lens_out = _tw._new((batch.nseq,), _torch.int32, device, stream)
+    else:
+        _int32(lens_out, "lens_out", (batch.nseq,), device)
+        if lens_out.data_ptr() == batch.lens.data_ptr() and batch.nseq:
+            raise RuntimeError("lens_out must not be the batch's lens")
+    _tw._call("i8_kv_keep", device, stream, cache.ref, batch.ref, tokens, path.data_ptr(), path.shape[1],
+              lens_out.data_ptr())
+    return lens_out

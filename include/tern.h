@@ -463,7 +463,7 @@ int64_t q4_packed_bytes(int64_t N, int64_t K, int64_t group);
 int q4_pack(const int8_t* t, const uint16_t* scale, int64_t N, int64_t K, int64_t group, void* packed, void* stream);
 
 /* y[m][n] = sum_g scale[n][g] * sum_{k in g} t[n][k] * x[m][k].
- *   packed  q4_pack blob of W[N][K] with this group
+ *   packed  q4_pack blob of W[N][K] with this group, N <= 2^26, K <= 2^24
  *   x       bf16 bits [M][K], 1 <= M <= TERN_MAX_M_GEMV, 16-byte aligned
  *   y       fp32 [M][N], 4-byte aligned
  * The products of a group are summed on the fp16 matrix cores in fp32: t is
@@ -650,9 +650,10 @@ int draft_tree_mask(const i8_kv_batch* batch, int64_t T, const int32_t* parent, 
  * tokens in front of the tree (positions below p0) and, of the tree, the rows
  * a <= j whose bit its mask has (its own among them as any other).  mask as
  * draft_tree_mask writes it, or any other; a row that sees nothing gives zeros.
- * Arguments, workspace (i8_kv_attend_workspace_bytes) and accuracy are those of
- * i8_kv_attend without a window.  A chain's mask gives what i8_kv_attend
- * gives. */
+ * Arguments, workspace and accuracy are those of i8_kv_attend without a window,
+ * with a max_rows of 0 or above 64 * words taken as 64 * words (for
+ * i8_kv_attend_workspace_bytes too).  A chain's mask gives what i8_kv_attend
+ * gives with that max_rows. */
 int i8_kv_attend_tree(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
                       int64_t q_stride, float scale, const uint64_t* mask, int64_t words, int64_t max_len,
                       int64_t max_rows, uint16_t* out, void* workspace, void* stream);

@@ -864,6 +864,25 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _empty(dtype, device, stream, *shape):
+    """_new, at the least cost where the call is on the current stream (torch takes 1.3 us for sizes as arguments
+    of their own, 1.7 for a tuple of them)."""
+    if stream is None:
+        return _torch.empty(*shape, dtype=dtype, device=device)
+    return _new(shape, dtype, device, stream)
+
+
+def _launch(f, device, stream, *args):
+    """_call of the library function f, at the least cost where the device is the current one and the call on its
+    current stream."""
+    if stream is None and _torch._C._cuda_getDevice() == device:
+        rc = f(*args, _raw_stream(device))
+        if rc:
+            _check(f.__name__, rc)
+    else:
+        _call(f.__name__, device, stream, *args)
+
+
 class QkTransform:
     """Norm gains (fp32 [D]), inverse frequencies (fp64 [D/2], radians per position) and rotation
     style of one layer's query and key heads; None leaves a part out."""
@@ -1078,10 +1097,13 @@ _HELD = {"q4_packed_bytes": "q4", "q4_pack": "q4", "q4_gemv": "q4", "q4_gemv_i8"
 
 
 def __getattr__(name):
-    if name in _HELD:
+    held = _HELD.get(name)
+    if held is None:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    if type(held) is str:              # the first time
         import importlib
-        return getattr(importlib.import_module("." + _HELD[name], __name__), name)
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        held = _HELD[name] = getattr(importlib.import_module("." + held, __name__), name)
+    return held
 
 
 def __dir__():

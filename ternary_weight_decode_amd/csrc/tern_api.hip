@@ -471,7 +471,8 @@ int tern5_gemv(const void* packed, int64_t N, int64_t K, const uint16_t* x, int6
 
 namespace {
 
-constexpr int64_t kQ4MaxRows = 1ll << 28;   // workgroups of one launch: 2^32 threads at 256 or more each
+constexpr int64_t kQ4MaxRows = 1ll << 26;   // workgroups of one launch: 2^32 threads at 1024 each
+constexpr int64_t kQ4MaxK = 1ll << 24;      // k are 32-bit in a kernel
 
 bool q4_bad(int64_t N, int64_t K, int64_t group)
 {
@@ -502,7 +503,8 @@ int q4_pack(const int8_t* t, const uint16_t* scale, int64_t N, int64_t K, int64_
 int q4_gemv(const void* packed, int64_t N, int64_t K, int64_t group, const uint16_t* x, int64_t M, float* y,
             void* stream)
 {
-    if (q4_bad(N, K, group) || M < 0 || M > TERN_MAX_M_GEMV || N > kQ4MaxRows) return TERN_E_SHAPE;
+    if (q4_bad(N, K, group) || M < 0 || M > TERN_MAX_M_GEMV || N > kQ4MaxRows || K > kQ4MaxK)
+        return TERN_E_SHAPE;
     if (N == 0 || M == 0) return TERN_OK;
     if (!y || (K > 0 && (!packed || !x))) return TERN_E_NULL;
     if ((packed && !aligned16(packed)) || (x && !aligned16(x)) || !aligned4(y)) return TERN_E_ALIGN;
@@ -515,7 +517,8 @@ int q4_gemv(const void* packed, int64_t N, int64_t K, int64_t group, const uint1
 int q4_gemv_i8(const void* packed, int64_t N, int64_t K, int64_t group, const int8_t* q, const float* s_x, int64_t M,
                float* y, void* stream)
 {
-    if (q4_bad(N, K, group) || M < 0 || M > TERN_MAX_M_GEMV || N > kQ4MaxRows) return TERN_E_SHAPE;
+    if (q4_bad(N, K, group) || M < 0 || M > TERN_MAX_M_GEMV || N > kQ4MaxRows || K > kQ4MaxK)
+        return TERN_E_SHAPE;
     if (N == 0 || M == 0) return TERN_OK;
     if (!y || !s_x || (K > 0 && (!packed || !q))) return TERN_E_NULL;
     if ((packed && !aligned16(packed)) || (q && !aligned16(q)) || !aligned4(y) || !aligned4(s_x))
@@ -844,9 +847,12 @@ int i8_kv_attend_tree(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_
     bool empty = false;
     int rc = kv_check_shape(cache, batch, T, &empty);
     if (rc) return rc;
+    if (words < 1 || words > TERN_TREE_WORDS) return TERN_E_SHAPE;
+    // the masks' width says how many rows a tree has at most
+    if (max_rows == 0 || max_rows > 64 * words) max_rows = 64 * words;
     const int64_t need = i8_kv_attend_workspace_bytes(T, Hq, cache->heads, cache->D, batch->nseq, max_len,
                                                       max_rows);
-    if (need < 0 || words < 1 || words > TERN_TREE_WORDS || !std::isfinite(scale) ||
+    if (need < 0 || !std::isfinite(scale) ||
         kv_bad_stride(Hq, cache->D, q_stride, TERN_BF16))
         return TERN_E_SHAPE;
     if (empty) return TERN_OK;

@@ -12,13 +12,16 @@ from __future__ import annotations
 
 import ternary_weight_decode_amd as _tw
 
+# These calls take as long as their launches: what they need is looked up once.
 _torch = _tw._setup()
+_lib = _tw.lib()
+_i32, _i64, _bf16 = _torch.int32, _torch.int64, _torch.bfloat16
 TREE_ROWS = 512
 TREE_WORDS = TREE_ROWS // 64
 
 
 def _int32(t, name, shape, device):
-    _tw._vec(t, name, _torch.int32, shape, device)
+    _tw._vec(t, name, _i32, shape, device)
 
 
 def draft_tree_mask(batch, parent, words: int = 1, mask=None, pos=None, stream=None):
@@ -30,14 +33,14 @@ def draft_tree_mask(batch, parent, words: int = 1, mask=None, pos=None, stream=N
     if not 1 <= words <= TREE_WORDS:
         raise RuntimeError(f"words is {words}, expected 1 to {TREE_WORDS}")
     if mask is None:
-        mask = _tw._new((tokens, words), _torch.int64, device, stream)
+        mask = _tw._empty(_i64, device, stream, tokens, words)
     else:
-        _tw._vec(mask, "mask", _torch.int64, (tokens, words), device)
+        _tw._vec(mask, "mask", _i64, (tokens, words), device)
     if pos is None:
-        pos = _tw._new((tokens,), _torch.int32, device, stream)
+        pos = _tw._empty(_i32, device, stream, tokens)
     else:
         _int32(pos, "pos", (tokens,), device)
-    _tw._call("draft_tree_mask", device, stream, batch.ref, tokens, parent.data_ptr(), words, mask.data_ptr(),
+    _tw._launch(_lib.draft_tree_mask, device, stream, batch.ref, tokens, parent.data_ptr(), words, mask.data_ptr(),
               pos.data_ptr())
     return mask, pos
 
@@ -46,25 +49,29 @@ def i8_kv_attend_tree(cache, batch, q, mask, scale=None, max_len=None, max_rows:
                       stream=None):
     """Attention of q bf16 [T, Hq, D] over the batch's cached tokens -> bf16 [T, Hq, D]: a row sees what stands in
     front of its tree, and of the tree the rows up to its own whose bits its mask has (int64 [T, words]).
-    Everything else, the workspace too, as i8_kv_attend."""
+    Everything else as i8_kv_attend; a workspace is i8_kv_attend_workspace's for max_rows, at most 64 * words (and
+    that where max_rows is 0)."""
     device, d = _tw._kv_device(cache, batch), cache.d
-    tokens, hq, stride = _tw._rows(q, "q", _torch.bfloat16, device, None, d, None)
-    _tw._vec(mask, "mask", _torch.int64, (tokens, None), device)
+    tokens, hq, stride = _tw._rows(q, "q", _bf16, device, None, d, None)
+    _tw._vec(mask, "mask", _i64, (tokens, None), device)
     if max_len is None:
         max_len = batch.width * _tw.KV_BLOCK or 1
     if out is None:
-        out = _tw._new((tokens, hq, d), _torch.bfloat16, device, stream)
+        out = _tw._empty(_bf16, device, stream, tokens, hq, d)
     else:
-        _tw._vec(out, "out", _torch.bfloat16, (tokens, hq, d), device)
-    need = _tw.lib().i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len, max_rows)
+        _tw._vec(out, "out", _bf16, (tokens, hq, d), device)
+    words = mask.shape[1]
+    if max_rows == 0 or max_rows > 64 * words:           # the masks' width says how many rows a tree has at most
+        max_rows = 64 * words
+    need = _lib.i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len, max_rows)
     if workspace is None:
         if need > 0:
             workspace = _tw._new(need, _torch.uint8, device, stream, returned=False)
     elif workspace.get_device() != device or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise RuntimeError(f"workspace must be a contiguous tensor of at least {need} bytes on device {device}")
-    _tw._call("i8_kv_attend_tree", device, stream, cache.ref, batch.ref, tokens, q.data_ptr(), hq, stride,
-              d ** -0.5 if scale is None else scale, mask.data_ptr(), mask.shape[1], max_len, max_rows,
+    _tw._launch(_lib.i8_kv_attend_tree, device, stream, cache.ref, batch.ref, tokens, q.data_ptr(), hq, stride,
+              d ** -0.5 if scale is None else scale, mask.data_ptr(), words, max_len, max_rows,
               out.data_ptr(), _tw._addr(workspace))
     return out
 
@@ -80,18 +87,18 @@ def draft_tree_accept(batch, parent, token, target, width: int = 64, path=None, 
     _int32(token, "token", (tokens,), device)
     _int32(target, "target", (tokens,), device)
     if path is None:
-        path = _tw._new((nseq, width), _torch.int32, device, stream)
+        path = _tw._empty(_i32, device, stream, nseq, width)
     else:
         _int32(path, "path", (nseq, width), device)
     if count is None:
-        count = _tw._new((nseq,), _torch.int32, device, stream)
+        count = _tw._empty(_i32, device, stream, nseq)
     else:
         _int32(count, "count", (nseq,), device)
     if following is None:
-        following = _tw._new((nseq,), _torch.int32, device, stream)
+        following = _tw._empty(_i32, device, stream, nseq)
     else:
         _int32(following, "following", (nseq,), device)
-    _tw._call("draft_tree_accept", device, stream, batch.ref, tokens, parent.data_ptr(), token.data_ptr(),
+    _tw._launch(_lib.draft_tree_accept, device, stream, batch.ref, tokens, parent.data_ptr(), token.data_ptr(),
               target.data_ptr(), width, path.data_ptr(), count.data_ptr(), following.data_ptr())
     return path, count, following
 
@@ -102,11 +109,11 @@ def i8_kv_keep(cache, batch, tokens: int, path, lens_out=None, stream=None):
     device = _tw._kv_device(cache, batch)
     _int32(path, "path", (batch.nseq, None), device)
     if lens_out is None:
-        lens_out = _tw._new((batch.nseq,), _torch.int32, device, stream)
+        lens_out = _tw._empty(_i32, device, stream, batch.nseq)
     else:
         _int32(lens_out, "lens_out", (batch.nseq,), device)
         if lens_out.data_ptr() == batch.lens.data_ptr() and batch.nseq:
             raise RuntimeError("lens_out must not be the batch's lens")
-    _tw._call("i8_kv_keep", device, stream, cache.ref, batch.ref, tokens, path.data_ptr(), path.shape[1],
+    _tw._launch(_lib.i8_kv_keep, device, stream, cache.ref, batch.ref, tokens, path.data_ptr(), path.shape[1],
               lens_out.data_ptr())
     return lens_out

@@ -81,7 +81,7 @@ def check(s, q, parent=None, masks=None, words=1, scale=None, max_len=None, max_
     else:
         m = dev(masks.view(np.int64))
     launches = tw.i8_kv_attend_config(s.tokens, q.shape[1], s.heads, s.d, len(s.lens), s.table.shape[1], 0, max_len,
-                                      max_rows)
+                                      min(max_rows or 64 * masks.shape[1], 64 * masks.shape[1]))
     if cols is not None:
         assert cols in [x["cols"] for x in launches], launches
     if groups is not None:
@@ -151,7 +151,8 @@ def test_a_chain_is_causal_attention():
         q = dev(queries(s, hq), torch.bfloat16)
         chain = np.concatenate([np.arange(-1, n - 1) for n in new]).astype(np.int32)
         m, pos = tw.draft_tree_mask(b, dev(chain), -(-max(new) // 64))
-        assert torch.equal(tw.i8_kv_attend_tree(c, b, q, m, max_len=max_len), tw.i8_kv_attend(c, b, q, max_len=max_len))
+        assert torch.equal(tw.i8_kv_attend_tree(c, b, q, m, max_len=max_len),
+                           tw.i8_kv_attend(c, b, q, max_len=max_len, max_rows=64 * m.shape[1]))
 
 
 def test_what_is_hidden_has_no_say():

@@ -46,7 +46,8 @@ def attend(c=None, b=None, T=1, q=P, hq=4, qs=512, scale=0.1, mask=P, words=1, m
 BAD = [(dict(n=-1), E_SHAPE), (dict(k=64), E_SHAPE), (dict(k=-128), E_SHAPE), (dict(group=48), E_SHAPE),
        (dict(group=0), E_SHAPE), (dict(group=256), E_SHAPE), (dict(packed=None), E_NULL), (dict(packed=ODD), E_ALIGN),
        (dict(n=0, packed=None), E_OK)]
-PRODUCT = BAD + [(dict(m=-1), E_SHAPE), (dict(m=17), E_SHAPE), (dict(n=1 << 29), E_SHAPE), (dict(y=None), E_NULL),
+PRODUCT = BAD + [(dict(m=-1), E_SHAPE), (dict(m=17), E_SHAPE), (dict(n=1 << 29), E_SHAPE),
+                 (dict(k=1 << 25), E_SHAPE), (dict(y=None), E_NULL),
                  (dict(y=P + 2), E_ALIGN), (dict(m=0, y=None), E_OK)]
 
 

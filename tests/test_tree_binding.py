@@ -1,6 +1,7 @@
 """Host side of the 4-bit and tree calls' binding, with the library and the
 allocator stood in for (no GPU): names, memory, checks of tensors."""
 import inspect
+import types
 
 import pytest
 import torch
@@ -42,13 +43,38 @@ def calls(monkeypatch):
         seen["taken"].append(stream)
         return torch.zeros(shape, dtype=dtype).as_subclass(Tensor)
 
-    def call(name, device, stream, *args):
-        assert device == 0
-        seen["called"].append((name, stream))
+    def empty(dtype, device, stream, *shape):
+        return new(shape, dtype, device, stream) if stream is None else real(dtype, device, stream, *shape)
 
+    def launch(f, device, stream, *args):
+        assert device == 0
+        seen["called"].append((f.__name__, stream))
+
+    real = tw._empty
     monkeypatch.setattr(tw, "_new", new)
-    monkeypatch.setattr(tw, "_call", call)
+    monkeypatch.setattr(tw, "_empty", empty)
+    monkeypatch.setattr(tw, "_launch", launch)
     return seen
+
+
+def test_launches_on_the_device_and_stream_asked_for(monkeypatch):
+    """On the current device and stream at once, on others through _call."""
+    seen = []
+
+    def f(*args):
+        seen.append(args)
+        return 0
+
+    monkeypatch.setattr(tw, "_torch", types.SimpleNamespace(_C=types.SimpleNamespace(_cuda_getDevice=lambda: 1)))
+    monkeypatch.setattr(tw, "_raw_stream", lambda device: 70 + device)
+    monkeypatch.setattr(tw, "_call", lambda *a: seen.append(a))
+    tw._launch(f, 1, None, 5)
+    tw._launch(f, 0, None, 5)
+    tw._launch(f, 1, "side", 5)
+    assert seen == [(5, 71), ("f", 0, None, 5), ("f", 1, "side", 5)]
+    monkeypatch.setattr(tw, "_check", lambda name, rc: seen.append((name, rc)))
+    tw._launch(lambda *a: 3, 1, None)
+    assert seen[-1] == ("<lambda>", 3)
 
 
 def batch(nseq=2, width=3):

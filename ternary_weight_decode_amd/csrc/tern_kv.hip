@@ -504,77 +504,74 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, KvBatch b, TO* 
 
 // ---- keep ------------------------------------------------------------------
 // The accepted branch of a tree moves up: slot p0 + k takes the token of slot
-// p0 + path[k].  One workgroup per (sequence, head, side): a branch is a few
-// tokens in one or two blocks, so the launch is bound by the chain from cu over
-// the path and the table to the scales and the codes.  Blocks go one after
-// another.  A path ascends, so a block's tokens come from itself or from blocks
-// behind it, whose bytes are as they were: each block's tokens are taken to LDS
-// before anything of it is written.
-
-// The first entry of a path that is no row of the tree or not above the one
-// before it; all threads of a workgroup of 256 call it.
-__device__ __forceinline__ int path_length(const int32_t* path, int width, int rows, int* found)
-{
-    const int most = width < rows ? width : rows;      // it ascends: not more entries than rows
-    if (threadIdx.x == 0) *found = most;
-    __syncthreads();
-    for (int k = threadIdx.x; k < most; k += 256) {
-        const int r = path[k], before = k > 0 ? path[k - 1] : -1;
-        if (r <= before || r < 0 || r >= rows) {
-            atomicMin(found, k);
-            break;
-        }
-    }
-    __syncthreads();
-    return *found;
-}
-
+// p0 + path[k].  One workgroup per (sequence, head, side), 64 tokens of the path
+// at a time, which go to two blocks at most.  A path ascends, so they come from
+// these blocks or from others behind, whose bytes are as they were: all tokens
+// are in LDS before anything is written.
+// A branch is a few tokens: bound by the launch and the chain from cu over the
+// table to scales and codes.
 template <int D>
 __global__ __launch_bounds__(256) void kv_keep_kernel(KvCache c, KvBatch b, const int32_t* paths, int width,
                                                       int32_t* lens_out)
 {
     __shared__ __align__(16) int8_t code[kKvBlock][D];
     __shared__ int64_t from[kKvBlock];                 // unit (block and head) of a token's source, -1: none
-    __shared__ float its[kKvBlock];                    // the source's scale where it is another block's
+    __shared__ float its[kKvBlock];                    // the source's scale
     __shared__ int slot[kKvBlock];
-    __shared__ int found;
-    __shared__ uint32_t tops[4];
+    __shared__ int tokens;
+    __shared__ int64_t place[2];                       // the units that tokens go to, -1: none, or nothing moves
+    __shared__ uint32_t tops[2][4];
     const int side = blockIdx.x & 1, h = (blockIdx.x >> 1) % c.heads, i = (blockIdx.x >> 1) / c.heads;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int32_t* path = paths + (int64_t)i * width;
+    int r = wave == 0 && lane < width ? path[lane] : -1;
     KvSeq s;
     const bool any = kv_seq(b, i, s);
-    const int kept = any ? path_length(path, width, s.n < kTreeRows ? s.n : kTreeRows, &found) : 0;
-    if (lens_out && side == 0 && h == 0 && threadIdx.x == 0) {
-        const int len = any ? s.p0 + kept : s.p0;
-        lens_out[i] = len > 0 ? len : 0;
-    }
-    // tokens in front of position 0 are not there
-    for (int k0 = s.p0 < 0 ? -s.p0 : 0; k0 < kept;) {
+    const int rows = any ? (s.n < kTreeRows ? s.n : kTreeRows) : 0, most = width < rows ? width : rows;
+    int kept = 0;
+    for (int k0 = 0; k0 < most; k0 += kKvBlock) {
         const int block = (s.p0 + k0) >> 6, base = (s.p0 + k0) & 63;
-        const int n = kept - k0 < kKvBlock - base ? kept - k0 : kKvBlock - base;
-        const int phys = kv_block(b, c, s.i, block);
-        bool moves = false;
-        if (threadIdx.x < n) {
-            const int r = path[k0 + threadIdx.x], p = s.p0 + r;
-            const int source = kv_block(b, c, s.i, p >> 6);
+        if (wave == 0) {
+            const int k = k0 + lane;
+            if (k0 > 0) r = k < most ? path[k] : -1;
+            int before = __shfl(r, lane - 1);
+            if (lane == 0) before = k0 > 0 ? path[k0 - 1] : -1;
+            const uint64_t end = __ballot(!(k < most && r > before && r >= 0 && r < rows));
+            const int n = end ? __builtin_ctzll(end) : 64;
+            const bool mine = lane < n;
+            // tokens in front of position 0 are not there (their block is below 0)
+            const int p = s.p0 + r, source = mine ? kv_block(b, c, s.i, p >> 6) : -1;
+            const int to = mine ? kv_block(b, c, s.i, (s.p0 + k) >> 6) : -1, second = base + lane >= kKvBlock;
             const int64_t unit = (int64_t)source * c.heads + h;
-            slot[threadIdx.x] = p & 63;
-            from[threadIdx.x] = source < 0 ? -1 : unit;
-            its[threadIdx.x] = source >= 0 && source != phys ? c.scales[unit * 2 + side] : 0.0f;
-            moves = r != k0 + (int)threadIdx.x;
+            from[lane] = source < 0 ? -1 : unit;
+            its[lane] = source >= 0 ? c.scales[unit * 2 + side] : 0.0f;
+            slot[lane] = p & 63;
+            const bool moves = mine && r != k && source >= 0 && to >= 0;
+            const uint64_t m0 = __ballot(moves && !second), m1 = __ballot(moves && second);
+            if (lane == 0) {
+                tokens = n;
+                place[0] = place[1] = -1;
+            }
+            __builtin_amdgcn_wave_barrier();
+            if (mine && to >= 0 && (second ? m1 : m0)) place[second] = (int64_t)to * c.heads + h;
         }
-        moves = __syncthreads_or(moves);
-        if (phys >= 0 && moves) {
-            const int64_t unit = (int64_t)phys * c.heads + h;
-            int8_t* const mine = c.codes + (unit * 2 + side) * (kKvBlock * D);
-            // the tokens to LDS, and the largest value that comes from elsewhere
-            uint32_t top = 0;
-            const auto sized = [&](int t, int most) {
-                if (from[t] != unit && from[t] >= 0) {
+        __syncthreads();
+        const int n = tokens;
+        kept += n;
+        const int64_t unit[2] = {place[0], place[1]};
+        if (unit[0] >= 0 || unit[1] >= 0) {
+            const float before[2] = {unit[0] >= 0 ? c.scales[unit[0] * 2 + side] : 0.0f,
+                                     unit[1] >= 0 ? c.scales[unit[1] * 2 + side] : 0.0f};
+            // the tokens to LDS, and the largest value that comes from another block
+            uint32_t top[2] = {0, 0};
+            const auto sized = [&](int t, int largest) {
+                const int w = base + t >= kKvBlock;
+                if (from[t] != unit[w]) {
                     // of a scale that is not finite, itself (not 0 times it)
-                    const float scale = fabsf(its[t]), value = scale < INFINITY ? (float)most * scale : scale;
+                    const float scale = fabsf(its[t]), value = scale < INFINITY ? (float)largest * scale : scale;
                     const uint32_t x = __builtin_bit_cast(uint32_t, value);
-                    top = x > top ? x : top;
+                    top[0] = w == 0 && x > top[0] ? x : top[0];
+                    top[1] = w == 1 && x > top[1] ? x : top[1];
                 }
             };
             if (side == 0) {
@@ -583,75 +580,110 @@ __global__ __launch_bounds__(256) void kv_keep_kernel(KvCache c, KvBatch b, cons
                     if (from[t] < 0) continue;
                     const u32x4 x = *(const u32x4*)(c.codes + from[t] * 2 * (kKvBlock * D) + kv_k_byte<D>(slot[t], d));
                     *(u32x4*)&code[t][d] = x;
-                    int most = 0;
+                    int largest = 0;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int v = (int8_t)(x[j >> 2] >> 8 * (j & 3));
-                        most = v > most ? v : -v > most ? -v : most;
+                        largest = v > largest ? v : -v > largest ? -v : largest;
                     }
-                    sized(t, most);
+                    sized(t, largest);
                 }
             } else {
-                for (int e = threadIdx.x; e < n * D; e += 256) {
-                    const int t = e / D, d = e % D;
-                    if (from[t] < 0) continue;
-                    const int8_t x = c.codes[(from[t] * 2 + 1) * (kKvBlock * D) + kv_v_byte(slot[t], d)];
-                    code[t][d] = x;
-                    sized(t, x < 0 ? -x : x);
+                // eight bytes a thread under way: a branch of 16 tokens waits once
+                for (int e0 = threadIdx.x; e0 < n * D; e0 += 256 * 8) {
+                    int8_t x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int e = e0 + 256 * j < n * D ? e0 + 256 * j : e0, t = e / D;
+                        const int64_t of = from[t] < 0 ? 0 : from[t];
+                        x[j] = c.codes[(of * 2 + 1) * (kKvBlock * D) + kv_v_byte(slot[t], e % D)];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int e = e0 + 256 * j, t = e / D;
+                        if (e >= n * D || from[t] < 0) continue;
+                        code[t][e % D] = x[j];
+                        sized(t, x[j] < 0 ? -x[j] : x[j]);
+                    }
                 }
             }
-            for (int off = 1; off < 64; off <<= 1) {
-                const uint32_t x = __shfl_xor(top, off);
-                top = x > top ? x : top;
-            }
-            if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-            __syncthreads();                           // code, tops
 #pragma unroll
-            for (int w = 0; w < 4; ++w) top = tops[w] > top ? tops[w] : top;
-            float scale = c.scales[unit * 2 + side];
-            int shift = 0;
-            if (top > 0) {
-                const float old = scale;
-                scale = join_scale(old, top, false, shift);
-                if (old == 0.0f) shift = 31;
+            for (int w = 0; w < 2; ++w) {
+                for (int off = 1; off < 64; off <<= 1) {
+                    const uint32_t x = __shfl_xor(top[w], off);
+                    top[w] = x > top[w] ? x : top[w];
+                }
+                if (lane == 0) tops[w][wave] = top[w];
             }
-            __syncthreads();                           // every thread has the old scale
-            if (threadIdx.x == 0 && top > 0) c.scales[unit * 2 + side] = scale;
-            // whole chunks: K 16 dims of a token, V 16 tokens of a dim
-            for (int i16 = threadIdx.x; i16 < kKvBlock * D / 16; i16 += 256) {
-                const int r = i16 & 15, g = i16 >> 4 & 3, rest = i16 >> 6;
-                const auto put = [&](uint32_t& w, int byte, int t, int d) {
-                    if (t < 0 || t >= n || from[t] < 0) return;
-                    uint32_t x = (uint32_t)(int)code[t][d] & 0xFFu;
-                    if (from[t] != unit) x = quantise((float)code[t][d] * its[t], scale);
-                    else if (shift) x = shift_codes(x, shift) & 0xFFu;
-                    w = (w & ~(0xFFu << 8 * byte)) | x << 8 * byte;
-                };
-                bool hit = shift != 0;
+            __syncthreads();                           // code and tops are there, the old scales read
+            float scale[2];
+            int shift[2];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) top[w] = tops[w][v] > top[w] ? tops[w][v] : top[w];
+                scale[w] = before[w];
+                shift[w] = 0;
+                if (unit[w] < 0 || top[w] == 0) continue;
+                scale[w] = join_scale(before[w], top[w], false, shift[w]);
+                if (before[w] == 0.0f) shift[w] = 31;
+                if (threadIdx.x == 0) c.scales[unit[w] * 2 + side] = scale[w];
+            }
+            if (shift[0] || shift[1]) {                // every code follows a doubled scale, 16 bytes a thread
+#pragma unroll 1
+                for (int w = 0; w < 2; ++w) {
+                    const int by = w ? shift[1] : shift[0];
+                    int8_t* const codes = c.codes + ((w ? unit[1] : unit[0]) * 2 + side) * (kKvBlock * D);
+                    if (by)
+#pragma unroll 1
+                        for (int e = threadIdx.x; e < kKvBlock * D / 16; e += 256) {
+                            u32x4 x = *(const u32x4*)(codes + 16 * e);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[j] = shift_codes(x[j], by);
+                            *(u32x4*)(codes + 16 * e) = x;
+                        }
+                }
+                __syncthreads();                       // before the tokens are written over them
+            }
+            // tokens at their places: K 16 dims a thread, V one
+            const int per = side == 0 ? D / 16 : D;
+#pragma unroll 1
+            for (int e = threadIdx.x; e < n * per; e += 256) {
+                const int t = e / per, d = e % per, w = base + t >= kKvBlock, at = (base + t) & 63;
+                const int64_t of = from[t], to = w ? unit[1] : unit[0];
+                if (of < 0 || to < 0) continue;
+                const bool far = of != to;
+                const float by = its[t], sc = w ? scale[1] : scale[0];
+                const int sh = w ? shift[1] : shift[0];
+                int8_t* const codes = c.codes + (to * 2 + side) * (kKvBlock * D);
                 if (side == 0) {
-                    const int t = rest / (D / 64) * 16 + r - base;
-                    hit |= t >= 0 && t < n;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) hit |= 16 * e + 4 * g + 3 >= base && 16 * e + 4 * g < base + n;
-                }
-                if (!hit) continue;
-                u32x4 x = *(const u32x4*)(mine + 16 * i16);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t w = shift ? shift_codes(x[e], shift) : x[e];
+                    u32x4 x = *(const u32x4*)&code[t][16 * d];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (side == 0) put(w, j, rest / (D / 64) * 16 + r - base, rest % (D / 64) * 64 + 16 * g + 4 * e + j);
-                        else put(w, j, 16 * e + 4 * g + j - base, rest * 16 + r);
+                        if (far) {
+                            uint32_t y = 0;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) y |= quantise((float)(int8_t)(x[j] >> 8 * q) * by, sc) << 8 * q;
+                            x[j] = y;
+                        } else if (sh) {
+                            x[j] = shift_codes(x[j], sh);
+                        }
                     }
-                    x[e] = w;
+                    *(u32x4*)(codes + kv_k_byte<D>(at, 16 * d)) = x;
+                } else {
+                    uint32_t x = (uint8_t)code[t][d];
+                    if (far) x = quantise((float)(int8_t)x * by, sc);
+                    else if (sh) x = shift_codes(x, sh);
+                    codes[kv_v_byte(at, d)] = (int8_t)x;
                 }
-                *(u32x4*)(mine + 16 * i16) = x;
             }
         }
+        if (n < kKvBlock) break;
         __syncthreads();                               // LDS is used again
-        k0 += n;
+    }
+    if (lens_out && side == 0 && h == 0 && threadIdx.x == 0) {
+        const int len = s.p0 + kept;                   // without rows: the length as it is
+        lens_out[i] = len > 0 ? len : 0;
     }
 }
 

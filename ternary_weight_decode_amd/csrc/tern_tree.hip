@@ -13,11 +13,15 @@ namespace tern {
 // parent of row r as the calls take it: an earlier row, or -1
 __device__ __forceinline__ int tree_parent(int p, int r) { return p >= 0 && p < r ? p : -1; }
 
-// mask[r] = mask[parent[r]] | 1 << r, by doubling: a row's mask holds the rows
-// up to `jump` rows of its branch back, and takes in that row's mask.  A mask
+// mask[r] = mask[parent[r]] | 1 << r.  Every row walks up its branch, a load
+// from LDS a step, which ends a tree of ordinary depth; the bits go to LDS on the
+// side.  From there on by doubling, for chains: a row's mask holds the branch from
+// the row down to before `jump`, and takes in that row's mask and jump.  A mask
 // that is read while its owner adds to it holds rows of the branch either way;
-// the jumps change between barriers.  log2(depth) + 1 rounds.
-// One thread per row of 64 * words.
+// the jumps change between barriers.  (48 trees of up to 512 rows 20 deep: by
+// doubling alone 8.7 us.)  One thread per row of 64 * words.
+constexpr int kTreeWalk = 24;
+
 __global__ __launch_bounds__(kTreeRows) void tree_mask_kernel(KvBatch b, const int32_t* parent, int words,
                                                               uint64_t* mask, int32_t* pos)
 {
@@ -26,33 +30,40 @@ __global__ __launch_bounds__(kTreeRows) void tree_mask_kernel(KvBatch b, const i
     KvSeq s;
     if (!kv_seq(b, blockIdx.x, s)) return;
     const int r = threadIdx.x, n = s.n < 64 * words ? s.n : 64 * words;
-    uint64_t m[kTreeWords];
     int j = r < n ? tree_parent(parent[s.t0 + r], r) : -1;
 #pragma unroll
-    for (int w = 0; w < kTreeWords; ++w) {
-        m[w] = r < n && w == r >> 6 ? 1ull << (r & 63) : 0;
-        if (w < words) rows[r][w] = m[w];
-    }
+    for (int w = 0; w < kTreeWords; ++w)
+        if (w < words) rows[r][w] = r < n && w == r >> 6 ? 1ull << (r & 63) : 0;
     jump[r] = j;
+    __syncthreads();
+    for (int k = 0; k < kTreeWalk && __any(j >= 0); ++k)
+        if (j >= 0) {
+            atomicOr((unsigned long long*)&rows[r][j >> 6], 1ull << (j & 63));
+            j = jump[j];
+        }
     while (__syncthreads_or(j >= 0)) {
+        jump[r] = j;
+        __syncthreads();
         int next = -1;
+        uint64_t m[kTreeWords];
         if (j >= 0) {
             next = jump[j];
 #pragma unroll
             for (int w = 0; w < kTreeWords; ++w)
-                if (w < words) m[w] |= rows[j][w];
-        }
-        __syncthreads();
+                if (w < words) m[w] = rows[j][w];
 #pragma unroll
-        for (int w = 0; w < kTreeWords; ++w)
-            if (w < words) rows[r][w] = m[w];
-        jump[r] = j = next;
+            for (int w = 0; w < kTreeWords; ++w)
+                if (w < words) rows[r][w] |= m[w];
+        }
+        j = next;
     }
     int depth = -1;
 #pragma unroll
     for (int w = 0; w < kTreeWords; ++w) {
-        if (w < words && r < n) mask[(int64_t)(s.t0 + r) * words + w] = m[w];
-        depth += __popcll(m[w]);
+        if (w >= words || r >= n) continue;
+        const uint64_t m = rows[r][w];
+        mask[(int64_t)(s.t0 + r) * words + w] = m;
+        depth += __popcll(m);
     }
     if (pos && r < n) pos[s.t0 + r] = s.p0 + depth;
     // rows that no mask has a bit for

@@ -24,12 +24,20 @@ def _int32(t, name, shape, device):
     _tw._vec(t, name, _i32, shape, device)
 
 
+def _parents(parent, device):
+    """Rows of the batch, one parent each."""
+    if not isinstance(parent, _torch.Tensor) or parent.dim() != 1:
+        _int32(parent, "parent", (None,), device)
+    n = parent.shape[0]
+    _int32(parent, "parent", (n,), device)
+    return n
+
+
 def draft_tree_mask(batch, parent, words: int = 1, mask=None, pos=None, stream=None):
     """Who descends from whom: parent int32 [T] -> (mask int64 [T, words], 64 rows of the tree to a word;
     pos int32 [T], the positions for the rotation).  words: enough for the largest tree, at most 8."""
     device = batch.device
-    _int32(parent, "parent", (None,), device)
-    tokens = parent.shape[0]
+    tokens = _parents(parent, device)
     if not 1 <= words <= TREE_WORDS:
         raise RuntimeError(f"words is {words}, expected 1 to {TREE_WORDS}")
     if mask is None:
@@ -53,14 +61,16 @@ def i8_kv_attend_tree(cache, batch, q, mask, scale=None, max_len=None, max_rows:
     that where max_rows is 0)."""
     device, d = _tw._kv_device(cache, batch), cache.d
     tokens, hq, stride = _tw._rows(q, "q", _bf16, device, None, d, None)
-    _tw._vec(mask, "mask", _i64, (tokens, None), device)
+    if not isinstance(mask, _torch.Tensor) or mask.dim() != 2:
+        _tw._vec(mask, "mask", _i64, (tokens, None), device)
+    words = mask.shape[1]
+    _tw._vec(mask, "mask", _i64, (tokens, words), device)
     if max_len is None:
         max_len = batch.width * _tw.KV_BLOCK or 1
     if out is None:
         out = _tw._empty(_bf16, device, stream, tokens, hq, d)
     else:
         _tw._vec(out, "out", _bf16, (tokens, hq, d), device)
-    words = mask.shape[1]
     if max_rows == 0 or max_rows > 64 * words:           # the masks' width says how many rows a tree has at most
         max_rows = 64 * words
     need = _lib.i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len, max_rows)
@@ -82,8 +92,7 @@ def draft_tree_accept(batch, parent, token, target, width: int = 64, path=None, 
     target answers there -> (path int32 [nseq, width], rows of each tree and then -1; count int32 [nseq];
     following int32 [nseq], the target's token behind the last)."""
     device, nseq = batch.device, batch.nseq
-    _int32(parent, "parent", (None,), device)
-    tokens = parent.shape[0]
+    tokens = _parents(parent, device)
     _int32(token, "token", (tokens,), device)
     _int32(target, "target", (tokens,), device)
     if path is None:
@@ -107,13 +116,16 @@ def i8_kv_keep(cache, batch, tokens: int, path, lens_out=None, stream=None):
     """Of the batch's `tokens` newest rows only those of path int32 [nseq, width] stay in the cache, moved up to
     where their tree began -> int32 [nseq], the lengths to go on with."""
     device = _tw._kv_device(cache, batch)
-    _int32(path, "path", (batch.nseq, None), device)
+    if not isinstance(path, _torch.Tensor) or path.dim() != 2:
+        _int32(path, "path", (batch.nseq, None), device)
+    width = path.shape[1]
+    _int32(path, "path", (batch.nseq, width), device)
     if lens_out is None:
         lens_out = _tw._empty(_i32, device, stream, batch.nseq)
     else:
         _int32(lens_out, "lens_out", (batch.nseq,), device)
         if lens_out.data_ptr() == batch.lens.data_ptr() and batch.nseq:
             raise RuntimeError("lens_out must not be the batch's lens")
-    _tw._launch(_lib.i8_kv_keep, device, stream, cache.ref, batch.ref, tokens, path.data_ptr(), path.shape[1],
+    _tw._launch(_lib.i8_kv_keep, device, stream, cache.ref, batch.ref, tokens, path.data_ptr(), width,
               lens_out.data_ptr())
     return lens_out

@@ -646,17 +646,21 @@ int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, 
 int draft_tree_mask(const i8_kv_batch* batch, int64_t T, const int32_t* parent, int64_t words, uint64_t* mask,
                     int32_t* pos, void* stream);
 
-/* i8_kv_attend for the rows of trees: row j of a sequence sees the cached
- * tokens in front of the tree (positions below p0) and, of the tree, the rows
- * a <= j whose bit its mask has (its own among them as any other).  mask as
- * draft_tree_mask writes it, or any other; a row that sees nothing gives zeros.
- * Arguments, workspace and accuracy are those of i8_kv_attend without a window,
- * with a max_rows of 0 or above 64 * words taken as 64 * words (for
- * i8_kv_attend_workspace_bytes too).  A chain's mask gives what i8_kv_attend
- * gives with that max_rows. */
+/* Attention for the rows of trees, as i8_kv_attend without a window, but row j of
+ * a sequence sees the cached tokens in front of the tree (positions below p0)
+ * and, of the tree, the rows a <= j whose bit its mask has (its own among them as
+ * any other).  mask as draft_tree_mask writes it, or any other; a row that sees
+ * nothing gives zeros.
+ *   mask uint64 [T][words], 1 <= words <= TERN_TREE_WORDS
+ *   max_len: the longest length that lens will hold, a hint as there
+ *   workspace: i8_kv_attend_tree_workspace_bytes() bytes, 16-byte aligned, NULL
+ *   when that is 0; overwritten, so calls that share it must not overlap in time.
+ * The other arguments, and the accuracy, are those of i8_kv_attend. */
+int64_t i8_kv_attend_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq,
+                                          int64_t max_len);
 int i8_kv_attend_tree(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
                       int64_t q_stride, float scale, const uint64_t* mask, int64_t words, int64_t max_len,
-                      int64_t max_rows, uint16_t* out, void* workspace, void* stream);
+                      uint16_t* out, void* workspace, void* stream);
 
 /* The branch that the target's own tokens take, greedily: from row 0 on, as
  * long as a row c (the first such) continues the current one and carries the
@@ -737,6 +741,13 @@ int tern_prefill_config(int64_t N, int64_t K, int64_t M, int64_t* out);
  * out, -TERN_E_SHAPE for what i8_kv_attend refuses.  Touches no device memory. */
 int i8_kv_attend_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
                         int64_t window, int64_t max_len, int64_t max_rows, int64_t* out);
+
+/* The kernel that i8_kv_attend_tree takes, in the same way: returns 1 (0 where there
+ * is nothing to do) and fills out[3] = {columns of a workgroup's tile: 16 the int8
+ * path, 128 the fp16 path; workgroups that long units are cut for, their parts
+ * joined by a second kernel, or 0: a workgroup for each tile and head; workgroups}. */
+int i8_kv_attend_tree_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
+                             int64_t max_len, int64_t* out);
 
 /* ---- matrix-core throughput probe (a measurement aid; no operation of the method) ----
  *

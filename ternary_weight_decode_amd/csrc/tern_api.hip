@@ -837,32 +837,48 @@ int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, 
     if (!aligned16(q) || !aligned16(out) || (need > 0 && !aligned16(workspace))) return TERN_E_ALIGN;
     if ((rc = check_device())) return rc;
     return finish(tern::launch_kv_attend(kv_cache(cache), kv_batch(batch, T), cache->D, q, Hq, q_stride, scale,
-                                         window, nullptr, 0, max_len, max_rows, out, workspace, (hipStream_t)stream));
+                                         window, max_len, max_rows, out, workspace, (hipStream_t)stream));
+}
+
+int64_t i8_kv_attend_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq,
+                                          int64_t max_len)
+{
+    if (kv_bad_d(D) || T < 0 || T > kKvMaxRows || heads < 1 || heads > kKvMaxHeads || Hq < 1 || Hq > kKvMaxHeads ||
+        Hq % heads != 0 || T * Hq > kKvMaxPairs || nseq < 0 || nseq > kKvMaxRows || max_len < 1 ||
+        max_len > INT32_MAX)
+        return -1;
+    if (T == 0 || nseq == 0) return 0;
+    return tern::kv_attend_tree_workspace_bytes(T, Hq, heads, D, nseq, max_len);
+}
+
+int i8_kv_attend_tree_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
+                             int64_t max_len, int64_t* out)
+{
+    if (!out) return -TERN_E_NULL;
+    const int64_t need = i8_kv_attend_tree_workspace_bytes(T, Hq, heads, D, nseq, max_len);
+    if (need < 0 || table_width < 0 || table_width > INT32_MAX / TERN_KV_BLOCK) return -TERN_E_SHAPE;
+    if (T == 0 || nseq == 0) return 0;
+    tern::kv_attend_tree_config(T, Hq, heads, D, nseq, table_width, max_len, out);
+    return 1;
 }
 
 int i8_kv_attend_tree(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
                       int64_t q_stride, float scale, const uint64_t* mask, int64_t words, int64_t max_len,
-                      int64_t max_rows, uint16_t* out, void* workspace, void* stream)
+                      uint16_t* out, void* workspace, void* stream)
 {
     bool empty = false;
     int rc = kv_check_shape(cache, batch, T, &empty);
     if (rc) return rc;
-    if (words < 1 || words > TERN_TREE_WORDS) return TERN_E_SHAPE;
-    // the masks' width says how many rows a tree has at most
-    if (max_rows == 0 || max_rows > 64 * words) max_rows = 64 * words;
-    const int64_t need = i8_kv_attend_workspace_bytes(T, Hq, cache->heads, cache->D, batch->nseq, max_len,
-                                                      max_rows);
-    if (need < 0 || !std::isfinite(scale) ||
-        kv_bad_stride(Hq, cache->D, q_stride, TERN_BF16))
-        return TERN_E_SHAPE;
+    const int64_t need = i8_kv_attend_tree_workspace_bytes(T, Hq, cache->heads, cache->D, batch->nseq, max_len);
+    if (need < 0 || words < 1 || words > TERN_TREE_WORDS || !std::isfinite(scale) || kv_bad_stride(Hq, cache->D, q_stride, TERN_BF16)) return TERN_E_SHAPE;
     if (empty) return TERN_OK;
     if ((rc = kv_check_pointers(cache, batch))) return rc;
     if (!q || !out || !mask || (need > 0 && !workspace)) return TERN_E_NULL;
     if (!aligned16(q) || !aligned16(out) || ((uintptr_t)mask & 7u) || (need > 0 && !aligned16(workspace)))
         return TERN_E_ALIGN;
     if ((rc = check_device())) return rc;
-    return finish(tern::launch_kv_attend(kv_cache(cache), kv_batch(batch, T), cache->D, q, Hq, q_stride, scale, 0,
-                                         mask, (int)words, max_len, max_rows, out, workspace, (hipStream_t)stream));
+    return finish(tern::launch_kv_attend_tree(kv_cache(cache), kv_batch(batch, T), cache->D, q, Hq, q_stride, scale,
+                                              mask, (int)words, max_len, out, workspace, (hipStream_t)stream));
 }
 
 int i8_kv_keep(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const int32_t* path, int64_t width,

@@ -153,10 +153,9 @@ int64_t kv_attend_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t 
                                   int64_t max_rows);
 int kv_attend_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
                      int64_t window, int64_t max_len, int64_t max_rows, int64_t* out);
-// mask NULL: every row sees all in front of it (and the window); else words of it a row, and no window
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
-                            int64_t q_stride, float scale, int64_t window, const uint64_t* mask, int words,
-                            int64_t max_len, int64_t max_rows, uint16_t* out, void* workspace, hipStream_t stream);
+                            int64_t q_stride, float scale, int64_t window, int64_t max_len, int64_t max_rows,
+                            uint16_t* out, void* workspace, hipStream_t stream);
 
 // ---- trees of drafted tokens ----
 constexpr int kTreeRows = 512;                    // rows of a tree
@@ -165,6 +164,12 @@ hipError_t launch_tree_mask(const KvBatch& b, const int32_t* parent, int words, 
                             hipStream_t stream);
 hipError_t launch_tree_accept(const KvBatch& b, const int32_t* parent, const int32_t* token, const int32_t* target,
                               int width, int32_t* path, int32_t* count, int32_t* next, hipStream_t stream);
+int64_t kv_attend_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len);
+void kv_attend_tree_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
+                           int64_t max_len, int64_t* out);
+hipError_t launch_kv_attend_tree(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,
+                                 int64_t q_stride, float scale, const uint64_t* mask, int words, int64_t max_len,
+                                 uint16_t* out, void* workspace, hipStream_t stream);
 hipError_t launch_kv_keep(const KvCache& c, const KvBatch& b, int64_t D, const int32_t* path, int width,
                           int32_t* lens_out, hipStream_t stream);
 

@@ -15,6 +15,7 @@ import ternary_weight_decode_amd as _tw
 # These calls take as long as their launches: what they need is looked up once.
 _torch = _tw._setup()
 _lib = _tw.lib()
+_i64c = _tw._i64
 _i32, _i64, _bf16 = _torch.int32, _torch.int64, _torch.bfloat16
 TREE_ROWS = 512
 TREE_WORDS = TREE_ROWS // 64
@@ -53,12 +54,35 @@ def draft_tree_mask(batch, parent, words: int = 1, mask=None, pos=None, stream=N
     return mask, pos
 
 
-def i8_kv_attend_tree(cache, batch, q, mask, scale=None, max_len=None, max_rows: int = 0, out=None, workspace=None,
-                      stream=None):
+def i8_kv_attend_tree_workspace_bytes(tokens: int, hq: int, heads: int, d: int, nseq: int, max_len: int) -> int:
+    return int(_lib.i8_kv_attend_tree_workspace_bytes(tokens, hq, heads, d, nseq, max_len))
+
+
+def i8_kv_attend_tree_workspace(cache, batch, tokens: int, hq: int, max_len=None):
+    """A workspace for i8_kv_attend_tree of `tokens` rows of hq heads (None where none is needed)."""
+    nbytes = i8_kv_attend_tree_workspace_bytes(tokens, hq, cache.heads, cache.d, batch.nseq,
+                                               max(1, batch.width * _tw.KV_BLOCK) if max_len is None else max_len)
+    if nbytes < 0:
+        _tw._check("i8_kv_attend_tree_workspace_bytes", 2)
+    return _torch.empty(nbytes, dtype=_torch.uint8, device=cache.device) if nbytes else None
+
+
+def i8_kv_attend_tree_config(tokens: int, hq: int, heads: int, d: int, nseq: int, width: int, max_len=None):
+    """The kernel that i8_kv_attend_tree takes for `tokens` rows of hq heads (host-side, no device needed; width:
+    of the table, max_len by default what that holds): a dict, empty where there is nothing to do."""
+    out = (_i64c * 3)()
+    rc = _lib.i8_kv_attend_tree_config(tokens, hq, heads, d, nseq, width,
+                                       max(1, width * _tw.KV_BLOCK) if max_len is None else max_len, out)
+    if rc < 0:
+        _tw._check("i8_kv_attend_tree_config", -rc)
+    return dict(zip(("cols", "groups", "grid"), map(int, out))) if rc else {}
+
+
+def i8_kv_attend_tree(cache, batch, q, mask, scale=None, max_len=None, out=None, workspace=None, stream=None):
     """Attention of q bf16 [T, Hq, D] over the batch's cached tokens -> bf16 [T, Hq, D]: a row sees what stands in
     front of its tree, and of the tree the rows up to its own whose bits its mask has (int64 [T, words]).
-    Everything else as i8_kv_attend; a workspace is i8_kv_attend_workspace's for max_rows, at most 64 * words (and
-    that where max_rows is 0)."""
+    scale: D ** -0.5 by default.  max_len: the longest length that batch.lens will hold, a hint (default: what
+    the table can hold)."""
     device, d = _tw._kv_device(cache, batch), cache.d
     tokens, hq, stride = _tw._rows(q, "q", _bf16, device, None, d, None)
     if not isinstance(mask, _torch.Tensor) or mask.dim() != 2:
@@ -71,18 +95,15 @@ def i8_kv_attend_tree(cache, batch, q, mask, scale=None, max_len=None, max_rows:
         out = _tw._empty(_bf16, device, stream, tokens, hq, d)
     else:
         _tw._vec(out, "out", _bf16, (tokens, hq, d), device)
-    if max_rows == 0 or max_rows > 64 * words:           # the masks' width says how many rows a tree has at most
-        max_rows = 64 * words
-    need = _lib.i8_kv_attend_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len, max_rows)
+    need = _lib.i8_kv_attend_tree_workspace_bytes(tokens, hq, cache.heads, d, batch.nseq, max_len)
     if workspace is None:
         if need > 0:
             workspace = _tw._new(need, _torch.uint8, device, stream, returned=False)
-    elif workspace.get_device() != device or not workspace.is_contiguous() or \
-            workspace.numel() * workspace.element_size() < need:
+    elif workspace.get_device() != device or not workspace.is_contiguous() or workspace.nbytes < need:
         raise RuntimeError(f"workspace must be a contiguous tensor of at least {need} bytes on device {device}")
     _tw._launch(_lib.i8_kv_attend_tree, device, stream, cache.ref, batch.ref, tokens, q.data_ptr(), hq, stride,
-              d ** -0.5 if scale is None else scale, mask.data_ptr(), words, max_len, max_rows,
-              out.data_ptr(), _tw._addr(workspace))
+                d ** -0.5 if scale is None else scale, mask.data_ptr(), words, max_len, out.data_ptr(),
+                _tw._addr(workspace))
     return out
 
 

@@ -72,7 +72,7 @@ def test_masks_of_odd_input():
 
 
 # ---- attention ----
-def check(s, q, parent=None, masks=None, words=1, scale=None, max_len=None, max_rows=0, cols=None, groups=None):
+def check(s, q, parent=None, masks=None, words=1, scale=None, max_len=None):
     import torch
     c, b = s.device()
     if masks is None:
@@ -80,14 +80,8 @@ def check(s, q, parent=None, masks=None, words=1, scale=None, max_len=None, max_
         masks = host(m).view(np.uint64)
     else:
         m = dev(masks.view(np.int64))
-    launches = tw.i8_kv_attend_config(s.tokens, q.shape[1], s.heads, s.d, len(s.lens), s.table.shape[1], 0, max_len,
-                                      min(max_rows or 64 * masks.shape[1], 64 * masks.shape[1]))
-    if cols is not None:
-        assert cols in [x["cols"] for x in launches], launches
-    if groups is not None:
-        assert (launches[0]["groups"] > 0) == groups, launches
     out = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device="cuda")
-    tw.i8_kv_attend_tree(c, b, dev(q, torch.bfloat16), m, scale=scale, max_len=max_len, max_rows=max_rows, out=out)
+    tw.i8_kv_attend_tree(c, b, dev(q, torch.bfloat16), m, scale=scale, max_len=max_len, out=out)
     got = host(out)
     want, bound = tree.attend(kv.Cache(s.codes, s.scales), s.cu, s.lens, s.table, q,
                               s.d ** -0.5 if scale is None else scale, masks)
@@ -107,20 +101,98 @@ def test_attend(d, heads, hq, new, prev, words):
     check(s, queries(s, hq), parent, words=words)
 
 
-@pytest.mark.parametrize("kind, d, heads, hq, new, prev, words, hints, cols, groups", [
-    ("16 split", 128, 2, 8, [4], [9000], 1, {}, 16, True),
-    ("16 whole", 64, 2, 4, [5, 3], [300, 100], 1, {}, 16, False),
-    ("64 split", 64, 2, 8, [16] * 12, [600] * 12, 1, dict(max_len=16000, max_rows=16), 64, True),
-    ("32 split", 64, 4, 16, [8] * 24, [600] * 24, 1, dict(max_len=30000, max_rows=8), 32, True),
-    ("64 whole", 64, 8, 32, [16] * 160, [40] * 160, 1, dict(max_rows=16), 64, False),
-    ("32 whole", 64, 8, 32, [8] * 160, [40] * 160, 1, dict(max_rows=8), 32, False),
-    ("256 split", 64, 1, 4, [200], [500], 4, dict(max_len=10 ** 6), 256, True),
-    ("256 whole", 64, 16, 128, [300], [100], 5, dict(max_len=5000), 256, False),
-    ("256 and 16", 64, 2, 8, [1, 200, 3, 2], [700, 500, 60, 130], 4, dict(max_len=10 ** 6), 256, None),
+LONG = 10 ** 6
+
+
+@pytest.mark.parametrize("d, heads, hq, new, prev, max_len, cols, cut", [
+    (64, 2, 4, [5, 3], [300, 100], None, 16, False),
+    (128, 8, 32, [20, 1, 64, 33], [130, 700, 0, 64], None, 16, False),
+    (128, 2, 8, [4], [9000], None, 16, True),
+    (64, 8, 32, [4, 0, 9, 1, 30], [2000, 10, 7000, 64, 0], LONG, 16, True),
+    (64, 1, 4, [200], [500], LONG, 128, True),
+    (128, 2, 16, [40, 90], [1100, 3], LONG, 128, True),
+    (64, 2, 16, [17, 1, 500, 8], [700, 500, 60, 130], LONG, 128, True),
+    (64, 2, 32, [8] * 90 + [0, 3], [(37 * i) % 300 for i in range(92)], LONG, 128, True),
+    (64, 8, 32, [24] * 140, [40] * 140, 20000, 128, False),
 ])
-def test_every_path(kind, d, heads, hq, new, prev, words, hints, cols, groups):
+def test_every_path(d, heads, hq, new, prev, max_len, cols, cut):
     s = Case(tw, [7, sum(new)], d, heads, new, prev)
-    check(s, queries(s, hq), forest(s.rng, new, 12), words=words, cols=cols, groups=groups, **hints)
+    c = tw.i8_kv_attend_tree_config(s.tokens, hq, heads, d, len(new), s.table.shape[1], max_len)
+    assert c["cols"] == cols and (c["groups"] > 0) == cut, c
+    check(s, queries(s, hq), forest(s.rng, new, 12), words=-(-max(new) // 64), max_len=max_len)
+
+
+@pytest.mark.parametrize("new, prev, max_len", [([40], [1500], 1), ([40], [1500], LONG), ([4], [9000], 64)])
+def test_the_hint_is_only_a_hint(new, prev, max_len):
+    """Lengths above and far below max_len."""
+    s = Case(tw, 13, 64, 1, new, prev)
+    check(s, queries(s, 4), forest(s.rng, new), max_len=max_len)
+
+
+@pytest.mark.parametrize("max_len, cols, cut", [(None, 16, False), (20000, 16, True), (LONG, 128, True)])
+def test_attend_up_to_a_descent_of_cu(max_len, cols, cut):
+    """Sequences in front of the descent as if they were alone, rows of the others left as they were."""
+    s = Case(tw, 19, 64, 2, [60, 3], [700, 30], spare_rows=30)
+    n = int(s.cu[-1])
+    s.cu = np.array([0, 60, n, n - 1, n, 2, n + 20, n + 30], np.int32)
+    s.lens = np.array([*s.lens, 64, 64, 500, 500, 500], np.int32)
+    s.table = np.concatenate([s.table, np.resize(s.table, (5, s.table.shape[1]))])
+    hq = 32 if cols > 16 else 8
+    c = tw.i8_kv_attend_tree_config(s.tokens, hq, 2, 64, len(s.lens), s.table.shape[1], max_len)
+    assert c["cols"] == cols and (c["groups"] > 0) == cut, c
+    parent = np.concatenate([forest(s.rng, [60, 3]), np.zeros(s.tokens - n, np.int32)]).astype(np.int32)
+    check(s, queries(s, hq), parent, max_len=max_len)
+
+
+@pytest.mark.parametrize("hq, max_len", [(8, 20000), (32, LONG)])
+def test_one_workspace_for_many_calls(hq, max_len):
+    """Calls of other lengths and rows, one after another and in two captured graphs, over one workspace."""
+    import torch
+    parts, graphs = [], []
+    for i, (new, prev) in enumerate((([64], [3000]), ([9, 40], [50, 2000]))):
+        s = Case(tw, 81 + i, 64, 1, new, prev)
+        c, b = s.device()
+        m, _ = tw.draft_tree_mask(b, dev(forest(s.rng, new)))
+        parts.append((c, b, dev(queries(s, hq), torch.bfloat16), m))
+    want = [tw.i8_kv_attend_tree(*p, max_len=max_len) for p in parts]
+    need = [tw.i8_kv_attend_tree_workspace(p[0], p[1], p[2].shape[0], hq, max_len) for p in parts]
+    shared = max(need, key=lambda t: t.numel())
+    assert shared.numel() > 0
+    for p in parts:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = tw.i8_kv_attend_tree(*p, max_len=max_len, workspace=shared)
+        graphs.append((g, out))
+    for k in (0, 1, 1, 0, 0, 1):
+        shared.fill_(255)
+        got = tw.i8_kv_attend_tree(*parts[1 - k], max_len=max_len, workspace=shared)
+        graphs[k][0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphs[k][1], want[k]) and torch.equal(got, want[1 - k])
+
+
+def test_a_captured_call_follows_the_lengths():
+    """A graph of a cut call replayed with other lengths, rows and masks in the same tensors."""
+    import torch
+    s = Case(tw, 91, 64, 1, [64], [6000])
+    q = queries(s, 16)
+    c, b = s.device()
+    qd = dev(q, torch.bfloat16)
+    m = torch.zeros(64, 1, dtype=torch.int64, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = tw.i8_kv_attend_tree(c, b, qd, m, max_len=LONG)
+    for rows, length in ((64, 6064), (64, 64), (9, 500), (1, 6064), (33, 4000)):
+        s.cu, s.lens = np.array([0, rows], np.int32), np.array([length], np.int32)
+        b.cu.copy_(dev(s.cu)), b.lens.copy_(dev(s.lens))
+        tw.draft_tree_mask(b, dev(np.concatenate([grow(s.rng, rows), np.zeros(64 - rows, np.int32)]).astype(np.int32)),
+                           mask=m)
+        out.fill_(9.0)
+        g.replay()
+        got = host(out)
+        want, bound = tree.attend(kv.Cache(s.codes, s.scales), s.cu, s.lens, s.table, q, 64 ** -0.5,
+                                  host(m).view(np.uint64))
+        assert np.all((np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + bound)[:rows]) and np.all(got[rows:] == 9)
 
 
 @pytest.mark.parametrize("rows, prev, max_len", [(6, 0, None), (6, 500, None), (6, 9000, None), (200, 0, 10 ** 6),
@@ -151,8 +223,8 @@ def test_a_chain_is_causal_attention():
         q = dev(queries(s, hq), torch.bfloat16)
         chain = np.concatenate([np.arange(-1, n - 1) for n in new]).astype(np.int32)
         m, pos = tw.draft_tree_mask(b, dev(chain), -(-max(new) // 64))
-        assert torch.equal(tw.i8_kv_attend_tree(c, b, q, m, max_len=max_len),
-                           tw.i8_kv_attend(c, b, q, max_len=max_len, max_rows=64 * m.shape[1]))
+        assert torch.allclose(tw.i8_kv_attend_tree(c, b, q, m, max_len=max_len).float(),
+                              tw.i8_kv_attend(c, b, q, max_len=max_len).float(), atol=0.05)
 
 
 def test_what_is_hidden_has_no_say():

@@ -1,6 +1,7 @@
 """The 4-bit and tree calls refuse bad arguments on the host, before any HIP
 call (no GPU): every call here passes addresses that are never dereferenced."""
 import ctypes
+import itertools
 
 import pytest
 
@@ -38,9 +39,9 @@ def keep(c=None, b=None, T=1, path=P, width=4, lens=P, nulls=()):
     return tw.lib().i8_kv_keep(ref("c", c or cache()), ref("b", b or batch()), T, path, width, lens, None)
 
 
-def attend(c=None, b=None, T=1, q=P, hq=4, qs=512, scale=0.1, mask=P, words=1, max_len=256, max_rows=0, out=P, ws=P):
+def attend(c=None, b=None, T=1, q=P, hq=4, qs=512, scale=0.1, mask=P, words=1, max_len=256, out=P, ws=P):
     return tw.lib().i8_kv_attend_tree(ctypes.byref(c or cache()), ctypes.byref(b or batch()), T, q, hq, qs, scale,
-                                      mask, words, max_len, max_rows, out, ws, None)
+                                      mask, words, max_len, out, ws, None)
 
 
 BAD = [(dict(n=-1), E_SHAPE), (dict(k=64), E_SHAPE), (dict(k=-128), E_SHAPE), (dict(group=48), E_SHAPE),
@@ -102,9 +103,34 @@ def test_keep_refuses(kw, rc):
 
 @pytest.mark.parametrize("kw, rc", [
     (dict(words=0), E_SHAPE), (dict(words=9), E_SHAPE), (dict(hq=3), E_SHAPE), (dict(scale=float("nan")), E_SHAPE),
-    (dict(qs=504), E_SHAPE), (dict(max_len=0), E_SHAPE), (dict(max_rows=-1), E_SHAPE), (dict(c=cache(d=32)), E_SHAPE),
+    (dict(qs=504), E_SHAPE), (dict(max_len=0), E_SHAPE), (dict(c=cache(d=32)), E_SHAPE),
     (dict(mask=None), E_NULL), (dict(q=None), E_NULL), (dict(out=None), E_NULL), (dict(mask=ODD), E_ALIGN),
     (dict(q=ODD), E_ALIGN), (dict(out=ODD), E_ALIGN), (dict(T=0, mask=None), E_OK),
 ])
 def test_attend_refuses(kw, rc):
     assert attend(**kw) == rc
+
+
+@pytest.mark.parametrize("hq, heads, d", [(32, 8, 128), (16, 8, 128), (1, 1, 64), (20, 1, 128)])
+def test_attend_plan(hq, heads, d):
+    """Every unit has a workgroup, cut or not, and the workspace is what the cut takes."""
+    for rows, nseq, width in itertools.product((1, 7, 64, 500, 5000), (1, 2, 70, 2000), (0, 1, 30, 700, 20000)):
+        p = tw.i8_kv_attend_tree_config(rows, hq, heads, d, nseq, width)
+        units = (rows * (hq // heads) // p["cols"] + nseq) * heads
+        assert p["cols"] in (16, 128) and p["groups"] in ((0, 768) if p["cols"] == 16 else (0, 512)), (rows, nseq, width, p)
+        assert p["grid"] == units + p["groups"] and not (p["cols"] == 128 and p["groups"] and units > 1024)
+        need = tw.i8_kv_attend_tree_workspace_bytes(rows, hq, heads, d, nseq, max(1, 64 * width))
+        used = p["grid"] * p["cols"] * (4 * d + 8) + (nseq + 5) // 4 * 16 if p["groups"] else 0
+        # lengths that would pass 32 bits in the line stay whole, whatever the workspace
+        assert used == need or units * width > 2 ** 30, (rows, nseq, width, p, used, need)
+    wide = (2 ** 31 - 1) // 64
+    assert tw.i8_kv_attend_tree_config(64, hq, heads, d, 1, 1000)["groups"] > 0
+    assert tw.i8_kv_attend_tree_config(64, 32, 8, d, 64, wide, 64000)["groups"] == 0
+    assert tw.i8_kv_attend_tree_config(0, hq, heads, d, 1, 5) == {} == tw.i8_kv_attend_tree_config(5, hq, heads, d, 0, 5)
+
+
+@pytest.mark.parametrize("bad", [dict(tokens=-1), dict(hq=3), dict(heads=0), dict(d=96), dict(nseq=-1), dict(width=-1),
+                                 dict(width=2 ** 26), dict(max_len=0), dict(max_len=2 ** 31)])
+def test_attend_plan_refuses(bad):
+    with pytest.raises(RuntimeError):
+        tw.i8_kv_attend_tree_config(**{**dict(tokens=8, hq=4, heads=2, d=64, nseq=2, width=9), **bad})

@@ -480,18 +480,18 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
 
 // Joins the parts of the cut units.  A job is 32 columns and 8 dims of a unit (fp16
 // path: 1 KiB of each part in the order in which the lanes held it), or a column
-// (int8 path).  JW = 4: few units, and the waves of a workgroup take one job's parts
-// in turn; JW = 1: a workgroup has kTreeJobs jobs of one unit, a wave each in turn.
-constexpr int kTreeJobs = 16;
-
-template <int D, int COLS, int JW>
+// (int8 path).  Few units: the waves of a workgroup take one job's parts in turn, JW
+// = 4.  Many: a wave has JOBS jobs of one unit, all their loads in flight at once
+// (32 trees 12.2 us one after another).
+template <int D, int COLS, int JW, int JOBS>
 __global__ __launch_bounds__(64 * kAttWaves) void kv_attend_tree_join_kernel(KvCache c, KvBatch b, AttArgs a)
 {
     constexpr bool F16 = COLS >= 64;
-    constexpr int kJobs = F16 ? COLS / 32 * (D / 8) : COLS, kDims = F16 ? 4 : D / 64;
-    constexpr int kEach = JW == 1 ? kTreeJobs : 1, kLoads = JW == 1 ? 4 : 8;
+    constexpr int kAll = F16 ? COLS / 32 * (D / 8) : COLS, kDims = F16 ? 4 : D / 64;
+    constexpr int kEach = JOBS * kAttWaves / JW, kLoads = JW == 1 ? 4 : 8;
     const int lane = threadIdx.x & 63, own = uni(threadIdx.x >> 6), wave = JW == 1 ? 0 : own;
-    const uint32_t unit = blockIdx.x / (kJobs / kEach), first = (blockIdx.x - unit * (kJobs / kEach)) * kEach;
+    const uint32_t unit = blockIdx.x / (kAll / kEach);
+    const int first = (blockIdx.x - unit * (kAll / kEach)) * kEach + (JW == 1 ? own * JOBS : 0);
     const uint32_t tiles = unit / c.heads, h = unit - tiles * c.heads;
     const uint32_t all = a.start[b.nseq], most = a.start[b.nseq + 1];
     const uint32_t starts = a.start[lane < b.nseq ? lane : 0];
@@ -504,76 +504,93 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attend_tree_join_kernel(KvC
     uint32_t each;
     if (start >= all || tree_chunks<COLS>(r.blocks, most, each) == 1) return;     // written already
     const int used = tile.nblk > 0 ? (int)((tile.nblk + each - 1) / each) : 1;    // parts that have blocks
-#pragma unroll 2
-    for (uint32_t job = first + (JW == 1 ? own : 0); job < first + kEach; job += kAttWaves) {
-        const int col = F16 ? 32 * (int)(job / (D / 8)) + (lane & 31) : (int)job;
-        if ((F16 ? 32 * (int)(job / (D / 8)) : col) >= tile.cols) return;
-        float top = -INFINITY, sum = 0.0f, o[kDims] = {};
-        for (int seg = 0; seg < used; seg += kLoads * JW) {
-            float x[kLoads][kDims];
-            float2 st[kLoads];
+    // a wave's jobs are of the same columns (fp16), or of the columns from `first` on
+    const int col0 = F16 ? first / (D / 8) * 32 : first;
+    if (col0 >= tile.cols) return;
+    const auto column = [&](int f) { return F16 ? col0 + (lane & 31) : first + f; };
+    float top[JOBS], sum[JOBS], o[JOBS][kDims];
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) {           // behind the last part its values are read again, unused
-                const int s = seg + wave + JW * k;
-                const int64_t at =
-                    start + ((uint32_t)(s < used ? s : used - 1) * r.tiles + (uint32_t)number) * c.heads + h;
-                st[k] = a.stat[at * COLS + col];
-                if (s >= used) st[k] = make_float2(-INFINITY, 0.0f);
+    for (int f = 0; f < JOBS; ++f) {
+        top[f] = -INFINITY;
+        sum[f] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kDims; ++u) o[f][u] = 0.0f;
+    }
+    for (int seg = 0; seg < used; seg += kLoads * JW) {
+        float x[kLoads][JOBS][kDims];
+        float2 st[kLoads][JOBS];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {          // behind the last part its values are read again, unused
+            const int s = seg + wave + JW * k;
+            const int64_t at = start + ((uint32_t)(s < used ? s : used - 1) * r.tiles + (uint32_t)number) * c.heads + h;
+#pragma unroll
+            for (int f = 0; f < JOBS; ++f) {
+                st[k][f] = F16 && f > 0 ? st[k][0] : a.stat[at * COLS + column(f)];
+                if (s >= used) st[k][f] = make_float2(-INFINITY, 0.0f);
                 if constexpr (F16) {
-                    const f32x4 v = *(const f32x4*)(a.part + at * (COLS * D) + job * 256 + lane * 4);
+                    const f32x4 v = *(const f32x4*)(a.part + at * (COLS * D) + (first + f) * 256 + lane * 4);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) x[k][u] = v[u];
+                    for (int u = 0; u < 4; ++u) x[k][f][u] = v[u];
                 } else {
 #pragma unroll
-                    for (int u = 0; u < kDims; ++u) x[k][u] = a.part[(at * COLS + col) * D + u * 64 + lane];
+                    for (int u = 0; u < kDims; ++u) x[k][f][u] = a.part[(at * COLS + column(f)) * D + u * 64 + lane];
                 }
             }
-            float now = top;
+        }
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) now = fmaxf(now, st[k].x);
-            const float keep = top == now ? 1.0f : exp2_fast(top - now);
-            top = now;
-            sum *= keep;
+        for (int f = 0; f < JOBS; ++f) {
+            float now = top[f];
 #pragma unroll
-            for (int u = 0; u < kDims; ++u) o[u] *= keep;
+            for (int k = 0; k < kLoads; ++k) now = fmaxf(now, st[k][f].x);
+            const float keep = top[f] == now ? 1.0f : exp2_fast(top[f] - now);
+            top[f] = now;
+            sum[f] *= keep;
+#pragma unroll
+            for (int u = 0; u < kDims; ++u) o[f][u] *= keep;
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
-                const float f = st[k].x == top ? 1.0f : exp2_fast(st[k].x - top);
-                sum = fmaf(st[k].y, f, sum);
+                const float w = st[k][f].x == now ? 1.0f : exp2_fast(st[k][f].x - now);
+                sum[f] = fmaf(st[k][f].y, w, sum[f]);
 #pragma unroll
-                for (int u = 0; u < kDims; ++u) o[u] = seg + wave + JW * k < used ? fmaf(x[k][u], f, o[u]) : o[u];
+                for (int u = 0; u < kDims; ++u)
+                    o[f][u] = seg + wave + JW * k < used ? fmaf(x[k][f][u], w, o[f][u]) : o[f][u];
             }
         }
-        if constexpr (JW > 1) {
-            __shared__ float so[JW][kDims][64];
-            __shared__ float2 sst[JW][64];
-            sst[wave][lane] = make_float2(top, sum);
+    }
+    if constexpr (JW > 1) {
+        static_assert(JOBS == 1);
+        __shared__ float so[JW][kDims][64];
+        __shared__ float2 sst[JW][64];
+        sst[wave][lane] = make_float2(top[0], sum[0]);
 #pragma unroll
-            for (int u = 0; u < kDims; ++u) so[wave][u][lane] = o[u];
-            __syncthreads();
-            if (wave > 0) return;
-            sum = 0.0f;
+        for (int u = 0; u < kDims; ++u) so[wave][u][lane] = o[0][u];
+        __syncthreads();
+        if (wave > 0) return;
+        sum[0] = 0.0f;
 #pragma unroll
-            for (int w = 0; w < JW; ++w) top = fmaxf(top, sst[w][lane].x);
+        for (int w = 0; w < JW; ++w) top[0] = fmaxf(top[0], sst[w][lane].x);
 #pragma unroll
-            for (int u = 0; u < kDims; ++u) o[u] = 0.0f;
+        for (int u = 0; u < kDims; ++u) o[0][u] = 0.0f;
 #pragma unroll
-            for (int w = 0; w < JW; ++w) {
-                const float f = sst[w][lane].x == top ? 1.0f : exp2_fast(sst[w][lane].x - top);
-                sum = fmaf(sst[w][lane].y, f, sum);
+        for (int w = 0; w < JW; ++w) {
+            const float f = sst[w][lane].x == top[0] ? 1.0f : exp2_fast(sst[w][lane].x - top[0]);
+            sum[0] = fmaf(sst[w][lane].y, f, sum[0]);
 #pragma unroll
-                for (int u = 0; u < kDims; ++u) o[u] = fmaf(so[w][u][lane], f, o[u]);
-            }
+            for (int u = 0; u < kDims; ++u) o[0][u] = fmaf(so[w][u][lane], f, o[0][u]);
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        uint16_t* to = tree_row(a, tile, h, col < tile.cols ? col : 0, c.heads, D);
+    }
+#pragma unroll
+    for (int f = 0; f < JOBS; ++f) {
+        const int col = column(f);
+        if (col >= tile.cols) continue;
+        const float inv = sum[f] == 0.0f ? 0.0f : 1.0f / sum[f];
+        uint16_t* to = tree_row(a, tile, h, col, c.heads, D);
         if constexpr (F16) {
-            if (col < tile.cols)
-                *(u16x4*)(to + job % (D / 8) * 8 + 4 * (lane >> 5)) =
-                    tree_result(f32x4{o[0], o[1], o[2], o[3]}, sum, inv);
+            *(u16x4*)(to + (first + f) % (D / 8) * 8 + 4 * (lane >> 5)) =
+                tree_result(f32x4{o[f][0], o[f][1], o[f][2], o[f][3]}, sum[f], inv);
         } else {
 #pragma unroll
-            for (int u = 0; u < kDims; ++u) to[u * 64 + lane] = f32_to_bf16(sum == 0.0f ? 0.0f : o[u] * inv);
+            for (int u = 0; u < kDims; ++u) to[u * 64 + lane] = f32_to_bf16(sum[f] == 0.0f ? 0.0f : o[f][u] * inv);
         }
     }
 }
@@ -589,16 +606,18 @@ struct TreePlan {
 };
 
 // Estimates in us, fitted to 14 shapes of D 128 (1 to 64 trees of 8 to 500 rows
-// over 500 to 40000 tokens, G 2 and 4, graphs of calls whose caches do not stay in
-// the chip's): 16 columns whole take 0.27 us a block of the longest unit (four waves
-// take blocks in turn) or 1 / 1050 us a block of all units; cut, nothing waits for
-// the longest but parts are written, read and joined; 128 columns do 205 blocks a
-// us.  What decides, measured, us (16 whole, 16 cut, 128 cut):
+// over 500 to 40000 tokens, G 2 and 4, graphs of calls over caches used in turn).
+// 16 columns whole: 0.27 us a block of the longest unit (four waves take blocks in
+// turn), or 1050 blocks of all units a us and the starts of each round of the card;
+// cut, nothing waits for the longest, but parts are written, read and joined.  128
+// columns: 205 blocks a us, more where waves have no columns.  What decides, us (16
+// whole, 16 cut, 128 cut):
 //   64 rows over   1000 tokens     10.8   17.5   20.9
 //   64 rows over   4000 tokens     22.3   24.6   27.1
 //   16 rows over  12338 tokens     54.9   20.6   26.9
 //   64 rows over  12338 tokens     56     40     35.7
 //   16 x 64 rows over 3000        103    106     80
+//   32 trees of 9 to 33 rows over 200 to 8000     85     92     76
 // Above 1024 units 128 columns are not cut: they fill the card, and parts would
 // take gigabytes.
 static TreePlan tree_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
@@ -606,9 +625,13 @@ static TreePlan tree_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64
 {
     const int64_t cols = T * (Hq / heads), blocks = (max_len + kKvBlock - 1) / kKvBlock;
     const auto units = [&](int c) { return (cols / c + nseq) * heads; };                      // at most
-    const auto tiles = [&](int c) { return (double)(nseq * heads * ((cols + nseq * c - 1) / (nseq * c))); };   // alike
-    const double all16 = tiles(16) * blocks / 1050, all128 = tiles(128) * blocks / 205;
-    const double whole16 = 6 + (0.27 * blocks > all16 ? 0.27 * blocks : all16), cut16 = 15 + all16, cut128 = 20 + all128;
+    const auto alike = [&](int c) { return (double)(nseq * heads * ((cols + nseq * c - 1) / (nseq * c))); };
+    // lengths lie between all alike and evenly spread from none
+    const double mean = (nseq > 1 ? 0.75 : 1.0) * blocks, u16 = alike(16);
+    const double all16 = u16 * mean / 1050, longest = 0.27 * blocks;
+    const double all128 = (0.45 * alike(128) + 0.55 * heads * cols / 128) * mean / 205;
+    const double starts = 6 * (u16 > 768 ? u16 / 768 : 1), whole16 = starts + (longest > all16 ? longest : all16);
+    const double cut16 = starts + 11 + all16, cut128 = 20 + all128;
     TreePlan p{};
     const bool wide = cut128 < whole16 && cut128 < cut16;
     p.cols = wide ? 128 : 16;
@@ -645,10 +668,9 @@ static hipError_t attend_tree(const KvCache& c, const KvBatch& b, const AttArgs&
     kv_attend_tree_kernel<D, COLS><<<(unsigned)p.grid, 64 * kAttWaves, 0, stream>>>(c, b, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.groups == 0) return e;
-    constexpr int kJobs = COLS >= 64 ? COLS / 32 * (D / 8) : COLS;
-    const int64_t jobs = (p.grid - p.groups) * kJobs;
-    if (jobs <= 4096) kv_attend_tree_join_kernel<D, COLS, 4><<<(unsigned)jobs, 256, 0, stream>>>(c, b, a);
-    else kv_attend_tree_join_kernel<D, COLS, 1><<<(unsigned)(jobs / kTreeJobs), 256, 0, stream>>>(c, b, a);
+    const int64_t jobs = (p.grid - p.groups) * (COLS >= 64 ? COLS / 32 * (D / 8) : COLS);
+    if (jobs <= 4096) kv_attend_tree_join_kernel<D, COLS, 4, 1><<<(unsigned)jobs, 256, 0, stream>>>(c, b, a);
+    else kv_attend_tree_join_kernel<D, COLS, 1, 4><<<(unsigned)(jobs / 16), 256, 0, stream>>>(c, b, a);
     return hipGetLastError();
 }
 

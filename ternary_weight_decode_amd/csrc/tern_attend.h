@@ -112,6 +112,13 @@ __device__ __forceinline__ uint64_t tree_bits(const uint64_t* row, int words, in
     return most >= 63 ? bits : most < 0 ? 0 : bits & ((2ull << most) - 1);
 }
 
+// x where bit k is set, else -inf: two instructions
+__device__ __forceinline__ float tree_sees(uint32_t bits, int k, float x)
+{
+    const uint32_t sees = (uint32_t)((int32_t)(bits << (31 - k)) >> 31);
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & sees) | (0xFF800000u & ~sees));
+}
+
 // bits 0, N, 2 N, ...
 template <int N>
 constexpr uint64_t every()
@@ -272,7 +279,7 @@ __device__ __forceinline__ void attend_blocks(const KvCache& c, const KvBatch& b
                     const uint64_t mine = bits >> 4 * g;
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        x[e] = mine >> (16 * (e >> 2) + (e & 3)) & 1 ? x[e] : -INFINITY;
+                        x[e] = tree_sees(e < 8 ? (uint32_t)mine : (uint32_t)(mine >> 32), 16 * (e >> 2 & 1) + (e & 3), x[e]);
                 }
             } else {
                 sees = first <= at + 63 && last >= at;

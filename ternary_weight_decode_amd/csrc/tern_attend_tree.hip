@@ -18,6 +18,14 @@
 // tiles of a chunk run at the same time, where heads are a multiple of 8 on one
 // XCD, and share its reads in L2.  The parts of a cut unit are joined by a second
 // kernel.
+//
+// Measured, us, kernel and join (MI355X, 32:8 heads of 128, caches used in turn):
+//   64 rows over 12338 tokens                 30.3 + 8.3   (26 MB: 12.9 read, 29 of parts)
+//   32 trees of 9 to 33 rows over 200 to 8000   69 + 9.3   (154 MB: 2.2 TB/s)
+//   500 rows over 4001, 130 over 900            68 + 7.8   (37.9e6 matrix-core cycles: 27% of them)
+//   8 rows over 512, 16:8 heads                9.0
+// What bounds the second and third: chunks of unlike length (the longest ends at 65
+// us, the median at 44) and the blocks with masks.
 #include "tern_attend.h"
 
 namespace tern {
@@ -55,6 +63,11 @@ __device__ __forceinline__ u16x4 tree_result(f32x4 o, float sum, float r)
 // matrix cores and the vector units busy; the order is written out, piece by piece
 // behind every matrix instruction.  What needs a branch stands in front of them:
 // masks, in the blocks that hold rows of the tree, and a maximum that moves.
+// A block takes a lone workgroup of a CU 2400 cycles, two together 3150 for a block
+// of each (scores 1090, values 1350, barrier 290 of them); 4900 a pair before the
+// order was written out.  The matrix cores need 1024 for each, the vector units
+// about 1400: those are the bound while many blocks are left, the way to the first
+// one (8 us: cu, table, codes, each behind the other) while few are.
 template <int D>
 __device__ __forceinline__ void attend_tree_f16(const KvCache& c, const KvBatch& b, const AttArgs& a,
                                                 const AttTile& tile, int h, int begin, int end, bool whole,
@@ -202,24 +215,30 @@ __device__ __forceinline__ void attend_tree_f16(const KvCache& c, const KvBatch&
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    x[t][e] = bits >> (32 * t + 8 * (e >> 2) + (e & 3)) & 1 ? fmaf(x[t][e], f, base) : -INFINITY;
-            top = x[0][0];
+                    x[t][e] = tree_sees((uint32_t)(bits >> 32 * t), 8 * (e >> 2) + (e & 3), fmaf(x[t][e], f, base));
+            f = 1.0f;                    // exponents already, all but a maximum that moves
+            base = 0.0f;
+            if (moves) {                 // also where only hidden scores are large: then by is 0
+                top = x[0][0];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) top = fmaxf(top, x[t][e]);
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float over = top - kF16Up;
-            const bool first = m == -INFINITY, grow = first ? over > -INFINITY : over > 0.0f;
-            const float by = grow ? over : 0.0f, keep = first ? 0.0f : exp2_fast(-by);
-            m = grow ? (first ? 0.0f : m) + by : m;
-            l *= keep;
+                    for (int e = 0; e < 16; ++e) top = fmaxf(top, x[t][e]);
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float over = top - kF16Up;
+                const bool first = m == -INFINITY, grow = first ? over > -INFINITY : over > 0.0f;
+                const float by = grow ? over : 0.0f;
+                m = grow ? (first ? 0.0f : m) + by : m;
+                if (__any(grow && !first)) {         // what has been summed so far is of the old maximum
+                    const float keep = first ? 1.0f : exp2_fast(-by);
+                    l *= keep;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                    for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) acc[u][e] *= keep;
-            f = 1.0f;                    // exponents already, all but their maximum
-            base = -by;
+                        for (int e = 0; e < 16; ++e) acc[u][e] *= keep;
+                }
+                base = -by;
+            }
         }
         u32x4 w[4];                      // the weights: B operands of 16 tokens each
         float sum0 = 0.0f, sum1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
@@ -631,7 +650,7 @@ static TreePlan tree_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64
     const double all16 = u16 * mean / 1050, longest = 0.27 * blocks;
     const double all128 = (0.45 * alike(128) + 0.55 * heads * cols / 128) * mean / 205;
     const double starts = 6 * (u16 > 768 ? u16 / 768 : 1), whole16 = starts + (longest > all16 ? longest : all16);
-    const double cut16 = starts + 11 + all16, cut128 = 20 + all128;
+    const double cut16 = starts + 11 + all16, cut128 = 22 + all128;
     TreePlan p{};
     const bool wide = cut128 < whole16 && cut128 < cut16;
     p.cols = wide ? 128 : 16;

@@ -113,7 +113,7 @@ LONG = 10 ** 6
     (128, 2, 16, [40, 90], [1100, 3], LONG, 128, True),
     (64, 2, 16, [17, 1, 500, 8], [700, 500, 60, 130], LONG, 128, True),
     (64, 2, 32, [8] * 90 + [0, 3], [(37 * i) % 300 for i in range(92)], LONG, 128, True),
-    (64, 8, 32, [24] * 140, [40] * 140, 20000, 128, False),
+    (64, 8, 32, [24] * 140, [40] * 139 + [9000], 20000, 128, False),
 ])
 def test_every_path(d, heads, hq, new, prev, max_len, cols, cut):
     s = Case(tw, [7, sum(new)], d, heads, new, prev)
@@ -216,36 +216,96 @@ def test_no_words_for_the_last_rows():
 
 
 def test_a_chain_is_causal_attention():
+    """Both calls are within the oracle's bound and half a step of bf16 of it, so within twice that of each other."""
     import torch
-    for new, prev, hq, max_len in (([7], [3000], 8, None), ([64, 3], [100, 40], 4, None), ([300], [700], 8, 10 ** 6)):
+    for new, prev, hq, max_len in (([7], [3000], 8, None), ([64, 3], [100, 40], 4, None), ([150], [300], 8, LONG)):
         s = Case(tw, 23, 128, 2, new, prev)
         c, b = s.device()
-        q = dev(queries(s, hq), torch.bfloat16)
+        q = queries(s, hq)
         chain = np.concatenate([np.arange(-1, n - 1) for n in new]).astype(np.int32)
         m, pos = tw.draft_tree_mask(b, dev(chain), -(-max(new) // 64))
-        assert torch.allclose(tw.i8_kv_attend_tree(c, b, q, m, max_len=max_len).float(),
-                              tw.i8_kv_attend(c, b, q, max_len=max_len).float(), atol=0.05)
+        assert np.array_equal(host(pos), np.concatenate([np.arange(n) + p for n, p in zip(new, prev)]))
+        one = host(tw.i8_kv_attend_tree(c, b, dev(q, torch.bfloat16), m, max_len=max_len))
+        two = host(tw.i8_kv_attend(c, b, dev(q, torch.bfloat16), max_len=max_len))
+        want, bound = tree.attend(kv.Cache(s.codes, s.scales), s.cu, s.lens, s.table, q, 128 ** -0.5,
+                                  host(m).view(np.uint64))
+        assert np.all(np.abs(one - two) <= 2 * (2.0 ** -8 * np.abs(want) + bound))
 
 
-def test_what_is_hidden_has_no_say():
+PATHS = [(2, None, 16, False), (2, 20000, 16, True), (16, LONG, 128, True)]
+
+
+def on_path(s, hq, max_len, cols, cut):
+    c = tw.i8_kv_attend_tree_config(s.tokens, hq, s.heads, s.d, len(s.lens), s.table.shape[1], max_len)
+    assert c["cols"] == cols and (c["groups"] > 0) == cut, c
+
+
+@pytest.mark.parametrize("hq, max_len, cols, cut", PATHS)
+def test_what_is_hidden_has_no_say(hq, max_len, cols, cut):
     """Scales that are not finite, and keys of any size, in places that a row does not see."""
     import torch
     s = Case(tw, 29, 64, 1, [70], [60])                 # rows 4..67 in the second block, 68 and 69 in the third
-    q = queries(s, 2)
+    on_path(s, hq, max_len, cols, cut)
+    q = queries(s, hq)
     parent = np.array([-1, 0, 0, 1] + [3] * 66, np.int32)
     parent[68], parent[69] = 2, 68
     c, b = s.device()
     m, _ = tw.draft_tree_mask(b, dev(parent), 2)
-    clean = host(tw.i8_kv_attend_tree(c, b, dev(q, torch.bfloat16), m))
+    clean = host(tw.i8_kv_attend_tree(c, b, dev(q, torch.bfloat16), m, max_len=max_len))
     for bad in (np.inf, np.nan, 1e30):
         scales = s.scales.copy()
         scales[s.table[0, 1]] = bad                     # the second block: rows 4 to 67
         c2 = tw.I8KvCache(codes=dev(s.codes), scales=dev(scales))
-        got = host(tw.i8_kv_attend_tree(c2, b, dev(q, torch.bfloat16), m))
+        got = host(tw.i8_kv_attend_tree(c2, b, dev(q, torch.bfloat16), m, max_len=max_len))
         free = [0, 1, 2, 3, 68, 69]                     # see none of them
         assert np.array_equal(got[free], clean[free]), bad
         if not np.isfinite(bad):
             assert np.isnan(got[4:68]).all()
+
+
+@pytest.mark.parametrize("hq, max_len, cols, cut", PATHS)
+def test_queries_that_are_not_finite(hq, max_len, cols, cut):
+    """They spoil their own row and head; one that sees nothing gives zeros all the same."""
+    import torch
+    s = Case(tw, 31, 64, 1, [50], [0])
+    on_path(s, hq, max_len, cols, cut)
+    q = queries(s, hq)
+    c, b = s.device()
+    m, _ = tw.draft_tree_mask(b, dev(grow(s.rng, 50)))
+    m[7] = 0
+    clean = host(tw.i8_kv_attend_tree(c, b, dev(q, torch.bfloat16), m, max_len=max_len))
+    bad = q.copy()
+    for row, head, value in ((3, 1, np.nan), (7, 0, np.nan), (20, 0, np.inf), (49, hq - 1, -np.inf)):
+        bad[row, head, 5] = value
+    got = host(tw.i8_kv_attend_tree(c, b, dev(bad, torch.bfloat16), m, max_len=max_len))
+    spoilt = np.zeros((50, hq), bool)
+    spoilt[3, 1] = spoilt[20, 0] = spoilt[49, hq - 1] = True
+    assert np.isnan(got[spoilt]).all() and np.array_equal(got[~spoilt], clean[~spoilt]) and np.all(got[7] == 0)
+
+
+@pytest.mark.parametrize("hq, max_len, cols, cut", [(8, None, 16, False), (64, LONG, 128, True)])
+def test_blocks_past_32_bits(hq, max_len, cols, cut):
+    """A cache of more than 4 GiB whose sequences lie at its end: attended and cut to a branch as in a small one."""
+    import torch
+    d, heads, new, prev = 128, 8, [40], [300]
+    s = Case(tw, 33, d, heads, new, prev)
+    on_path(s, hq, max_len, cols, cut)
+    c, b = s.device()
+    small = c.codes.shape[0]
+    far = 34000 - small
+    codes = torch.zeros(34000, *c.codes.shape[1:], dtype=torch.int8, device="cuda")
+    scales = torch.zeros(34000, *c.scales.shape[1:], device="cuda")
+    assert codes.numel() > 2 ** 32
+    codes[far:], scales[far:] = c.codes, c.scales
+    table = dev(np.where(s.table >= 0, s.table + far, s.table).astype(np.int32))
+    c2, b2 = tw.I8KvCache(codes=codes, scales=scales), tw.I8KvBatch(b.cu, b.lens, table)
+    m, _ = tw.draft_tree_mask(b, dev(forest(s.rng, new)))
+    q = dev(queries(s, hq), torch.bfloat16)
+    assert torch.equal(tw.i8_kv_attend_tree(c, b, q, m, max_len=max_len),
+                       tw.i8_kv_attend_tree(c2, b2, q, m, max_len=max_len))
+    path = dev(np.array([[0, 2, 3, 21, 25, 39]], np.int32))
+    assert torch.equal(tw.i8_kv_keep(c, b, s.tokens, path), tw.i8_kv_keep(c2, b2, s.tokens, path))
+    assert torch.equal(codes[far:], c.codes) and torch.equal(scales[far:], c.scales) and not codes[:far].any()
 
 
 def test_blocks_that_are_not_there():

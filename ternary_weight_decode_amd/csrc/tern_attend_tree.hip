@@ -5,10 +5,10 @@
 //   out = sum_p w_p V[p] / sum_p w_p,  w_p = exp(scale * q . K[p])
 //
 // As in the causal kernels the rows of one key/value head are columns: column c
-// of a sequence is row c / G under query head h*G + c % G.  Up to 16 columns a
-// tree: the int8 path, as single tokens and drafts take it.  More: the fp16 path
-// below, in tiles of 64 or 128 columns.  Only the blocks that hold rows of the
-// tree look at masks.
+// of a sequence is row c / G under query head h*G + c % G.  Few columns or short
+// contexts: the int8 path, in tiles of 16, as single tokens and drafts take it.
+// Long work of many columns: the fp16 path below, in tiles of 128.  Only the blocks
+// that hold rows of the tree look at masks.
 //
 // Work: a unit is a tile of columns and a head.  Long units are cut into chunks
 // of blocks, one for each workgroup; only the device knows the lengths (a
@@ -25,7 +25,9 @@
 //   500 rows over 4001, 130 over 900            68 + 7.8   (37.9e6 matrix-core cycles: 27% of them)
 //   8 rows over 512, 16:8 heads                9.0
 // What bounds the second and third: chunks of unlike length (the longest ends at 65
-// us, the median at 44) and the blocks with masks.
+// us, the median at 44) and the blocks with masks.  Equal stretches of a line of all
+// units, cut anywhere, were built: 63 and 63 us, but more parts, 12.6 and 9.8 us to
+// join, and the first 32: tiles of a head no longer side by side.
 #include "tern_attend.h"
 
 namespace tern {

@@ -114,6 +114,8 @@ LONG = 10 ** 6
     (64, 2, 16, [17, 1, 500, 8], [700, 500, 60, 130], LONG, 128, True),
     (64, 2, 32, [8] * 90 + [0, 3], [(37 * i) % 300 for i in range(92)], LONG, 128, True),
     (64, 8, 32, [24] * 140, [40] * 139 + [9000], 20000, 128, False),
+    (64, 1, 4, [1] * 100 + [70], [64 * (i % 9) for i in range(101)], LONG, 16, True),
+    (64, 800, 800, [90], [20], LONG, 128, True),
 ])
 def test_every_path(d, heads, hq, new, prev, max_len, cols, cut):
     s = Case(tw, [7, sum(new)], d, heads, new, prev)

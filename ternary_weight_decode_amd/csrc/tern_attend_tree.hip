@@ -402,6 +402,10 @@ __device__ __forceinline__ uint32_t tree_chunks(uint32_t blocks, uint32_t most, 
 
 constexpr uint32_t kTreeLeast = 4;           // blocks of a chunk
 constexpr int kTreeTries = 16;
+// Sequences a lane up to which whole units are counted without gaps, so that each CU
+// gets as many; more are found 64 at a time (512 trees of 4 rows over 500 tokens
+// 175 us and 153, 1024 of 2 over 300 382 and 172; 16 of 8 over 3000 26 and 31).
+constexpr int kTreeRun = 4;
 
 // sums over the lanes up to each
 __device__ __forceinline__ uint32_t scan(uint32_t v)
@@ -422,81 +426,94 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
                                                                                             AttArgs a)
 {
     const int lane = threadIdx.x & 63, run = (b.nseq + 63) / 64;
-    AttTile tile;
-    // every lane has a run of sequences, up to the first descent of cu
-    TreeShare r = {0, 1};
-    uint32_t work = 0;
-    bool falls = false;
-    for (int k = lane * run; k < lane * run + run && k < b.nseq && !falls; ++k) {
-        r = tree_share<COLS>(b, k, a.G, tile.s);
-        falls = tile.s.n < 0;
-        work += r.tiles * r.blocks;
-    }
-    const uint64_t fell = __ballot(falls);
-    const int lanes = fell ? __builtin_ctzll(fell) : 63;      // the last that counts
-    // a lane's chunks, `most` blocks each at most
-    const auto chunks = [&](uint32_t most) {
-        uint32_t n = 0, each;
-        if (lane > lanes) return n;
-        if (run == 1) return r.tiles * c.heads * tree_chunks<COLS>(r.blocks, most, each);
-        KvSeq s;
-        for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
-            const TreeShare o = tree_share<COLS>(b, k, a.G, s);
-            if (s.n < 0) break;
-            n += o.tiles * c.heads * tree_chunks<COLS>(o.blocks, most, each);
-        }
-        return n;
-    };
-    // chunks as short as the card holds at one time, to within a sixteenth
-    uint32_t most = 0, mine = 0, upto = 0, sum = 0;
-    if (a.groups > 0) {
-        const uint32_t all = __builtin_amdgcn_readlane(scan(lane > lanes ? 0 : work), 63) * c.heads;
-        most = (all + a.groups - 1) / a.groups;
-        most = most < kTreeLeast ? kTreeLeast : most;
-    }
-    for (int tries = 0;; ++tries) {
-        mine = chunks(most);
-        upto = scan(mine);
-        sum = __builtin_amdgcn_readlane(upto, 63);
-        if (most == 0 || sum <= (uint32_t)a.groups || tries == kTreeTries) break;
-        most += 1 + most / 16;
-    }
-    if (a.groups > 0 && blockIdx.x == 0 && threadIdx.x < 64) {   // for the joining kernel
-        uint32_t from = upto - mine, each;
-        for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
-            KvSeq s;
-            const TreeShare o = tree_share<COLS>(b, k, a.G, s);
-            a.start[k] = lane <= lanes && s.n >= 0 ? from : sum;
-            from += o.tiles * c.heads * tree_chunks<COLS>(o.blocks, most, each);
-            if (s.n < 0) from = sum;
-        }
-        if (lane == 0) {
-            a.start[b.nseq] = sum;
-            a.start[b.nseq + 1] = most;
-        }
-    }
     const uint32_t x = blockIdx.x;
-    if (x >= sum) return;
-    // the lane whose run holds x, then the sequence inside the run
-    const int owner = __popcll(__ballot(upto <= x));
-    uint32_t at = __builtin_amdgcn_readlane(upto - mine, owner), each = 0, n;
-    int i = owner * run;
-    while (true) {
-        r = tree_share<COLS>(b, i, a.G, tile.s);
-        n = tree_chunks<COLS>(r.blocks, most, each);
-        const uint32_t here = r.tiles * c.heads * n;
-        if (x - at < here) break;                             // ends: x is below the run's end
-        at += here;
-        ++i;
+    AttTile tile;
+    uint32_t number, h, parts = 1;
+    int begin = 0, end = INT32_MAX;
+    if (a.groups == 0 && run > kTreeRun) {
+        int64_t local;
+        if (!kv_find(b, x / c.heads, a.G, COLS, 1, tile.s, local)) return;
+        number = (uint32_t)local;
+        h = x % c.heads;
+    } else {
+        // every lane has a run of sequences, up to the first descent of cu
+        TreeShare r = {0, 1};
+        uint32_t work = 0;
+        bool falls = false;
+        for (int k = lane * run; k < lane * run + run && k < b.nseq && !falls; ++k) {
+            r = tree_share<COLS>(b, k, a.G, tile.s);
+            falls = tile.s.n < 0;
+            work += r.tiles * r.blocks;
+        }
+        const uint64_t fell = __ballot(falls);
+        const int lanes = fell ? __builtin_ctzll(fell) : 63;      // the last that counts
+        // a lane's chunks, `most` blocks each at most
+        const auto chunks = [&](uint32_t most) {
+            uint32_t n = 0, each;
+            if (lane > lanes) return n;
+            if (run == 1) return r.tiles * c.heads * tree_chunks<COLS>(r.blocks, most, each);
+            KvSeq s;
+            for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
+                const TreeShare o = tree_share<COLS>(b, k, a.G, s);
+                if (s.n < 0) break;
+                n += o.tiles * c.heads * tree_chunks<COLS>(o.blocks, most, each);
+            }
+            return n;
+        };
+        // chunks as short as the card holds at one time, to within a sixteenth
+        uint32_t most = 0, mine = 0, upto = 0, sum = 0;
+        if (a.groups > 0) {
+            const uint32_t all = __builtin_amdgcn_readlane(scan(lane > lanes ? 0 : work), 63) * c.heads;
+            most = (all + a.groups - 1) / a.groups;
+            most = most < kTreeLeast ? kTreeLeast : most;
+        }
+        for (int tries = 0;; ++tries) {
+            mine = chunks(most);
+            upto = scan(mine);
+            sum = __builtin_amdgcn_readlane(upto, 63);
+            if (most == 0 || sum <= (uint32_t)a.groups || tries == kTreeTries) break;
+            most += 1 + most / 16;
+        }
+        if (a.groups > 0 && blockIdx.x == 0 && threadIdx.x < 64) {   // for the joining kernel
+            uint32_t from = upto - mine, each;
+            for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
+                KvSeq s;
+                const TreeShare o = tree_share<COLS>(b, k, a.G, s);
+                a.start[k] = lane <= lanes && s.n >= 0 ? from : sum;
+                from += o.tiles * c.heads * tree_chunks<COLS>(o.blocks, most, each);
+                if (s.n < 0) from = sum;
+            }
+            if (lane == 0) {
+                a.start[b.nseq] = sum;
+                a.start[b.nseq + 1] = most;
+            }
+        }
+        if (x >= sum) return;
+        // the lane whose run holds x, then the sequence inside the run
+        const int owner = __popcll(__ballot(upto <= x));
+        uint32_t at = __builtin_amdgcn_readlane(upto - mine, owner), each = 0;
+        int i = owner * run;
+        while (true) {
+            r = tree_share<COLS>(b, i, a.G, tile.s);
+            parts = tree_chunks<COLS>(r.blocks, most, each);
+            const uint32_t here = r.tiles * c.heads * parts;
+            if (x - at < here) break;                             // ends: x is below the run's end
+            at += here;
+            ++i;
+        }
+        const uint32_t rest = (x - at) / c.heads, chunk = rest / r.tiles;
+        h = x - at - rest * c.heads;
+        number = rest - chunk * r.tiles;
+        begin = (int)(chunk * each);
+        end = begin + (int)each;
     }
-    const uint32_t rest = (x - at) / c.heads, h = x - at - rest * c.heads, chunk = rest / r.tiles;
-    if (!att_tile<COLS>(b, (int)(rest - chunk * r.tiles), a.G, 0, tile)) return;
+    if (!att_tile<COLS>(b, (int)number, a.G, 0, tile)) return;
     att_uniform(tile);
-    const int begin = uni((int)(chunk * each)), left = tile.nblk - begin;
-    const int end = begin + (left < (int)each ? left : (int)each);
-    if (left <= 0 && chunk > 0) return;                       // the tile sees less than the sequence's last
-    if constexpr (COLS < 64) attend_blocks<D, COLS / 16, false, true>(c, b, a, tile, h, begin, end, n == 1, x);
-    else attend_tree_f16<D>(c, b, a, tile, h, begin, end, n == 1, x);
+    begin = uni(begin);
+    if (begin > 0 && begin >= tile.nblk) return;              // the tile sees less than the sequence's last
+    end = uni(end < tile.nblk ? end : tile.nblk);
+    if constexpr (COLS < 64) attend_blocks<D, COLS / 16, false, true>(c, b, a, tile, h, begin, end, parts == 1, x);
+    else attend_tree_f16<D>(c, b, a, tile, h, begin, end, parts == 1, x);
 }
 
 // Joins the parts of the cut units.  A job is 32 columns and 8 dims of a unit (fp16

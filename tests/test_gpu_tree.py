@@ -116,6 +116,8 @@ LONG = 10 ** 6
     (64, 8, 32, [24] * 140, [40] * 139 + [9000], 20000, 128, False),
     (64, 1, 4, [1] * 100 + [70], [64 * (i % 9) for i in range(101)], LONG, 16, True),
     (64, 800, 800, [90], [20], LONG, 128, True),
+    (64, 2, 8, [2] * 300 + [0, 17], [(29 * i) % 200 for i in range(302)], None, 16, False),
+    (64, 2, 32, [8] * 300 + [0, 17], [(29 * i) % 200 for i in range(302)], 2000, 128, False),
 ])
 def test_every_path(d, heads, hq, new, prev, max_len, cols, cut):
     s = Case(tw, [7, sum(new)], d, heads, new, prev)
@@ -131,14 +133,15 @@ def test_the_hint_is_only_a_hint(new, prev, max_len):
     check(s, queries(s, 4), forest(s.rng, new), max_len=max_len)
 
 
-@pytest.mark.parametrize("max_len, cols, cut", [(None, 16, False), (20000, 16, True), (LONG, 128, True)])
-def test_attend_up_to_a_descent_of_cu(max_len, cols, cut):
+@pytest.mark.parametrize("max_len, cols, cut, more", [(None, 16, False, 0), (20000, 16, True, 0), (LONG, 128, True, 0),
+                                                      (None, 16, False, 300)])
+def test_attend_up_to_a_descent_of_cu(max_len, cols, cut, more):
     """Sequences in front of the descent as if they were alone, rows of the others left as they were."""
     s = Case(tw, 19, 64, 2, [60, 3], [700, 30], spare_rows=30)
     n = int(s.cu[-1])
-    s.cu = np.array([0, 60, n, n - 1, n, 2, n + 20, n + 30], np.int32)
-    s.lens = np.array([*s.lens, 64, 64, 500, 500, 500], np.int32)
-    s.table = np.concatenate([s.table, np.resize(s.table, (5, s.table.shape[1]))])
+    s.cu = np.array([0, 60, n, n - 1, n, 2, n + 20] + [n + 30] * (1 + more), np.int32)
+    s.lens = np.array([*s.lens, 64, 64, 500, 500, 500] + [300] * more, np.int32)
+    s.table = np.concatenate([s.table, np.resize(s.table, (5 + more, s.table.shape[1]))])
     hq = 32 if cols > 16 else 8
     c = tw.i8_kv_attend_tree_config(s.tokens, hq, 2, 64, len(s.lens), s.table.shape[1], max_len)
     assert c["cols"] == cols and (c["groups"] > 0) == cut, c

@@ -656,8 +656,11 @@ struct TreePlan {
 //   64 rows over  12338 tokens     56     40     35.7
 //   16 x 64 rows over 3000        103    106     80
 //   32 trees of 9 to 33 rows over 200 to 8000     85     92     76
-// Above 1024 units 128 columns are not cut: they fill the card, and parts would
-// take gigabytes.
+// 128 columns, one workgroup a CU or two: two leave parts twice as many, and pay off
+// where chunks are long or units many (us, 256 and 512 workgroups: 64 rows over 6000
+// tokens 29.4 and 31.3, over 12338 33.7 and 35.9, over 30000 54.3 and 53.2; 32 trees
+// of 9 to 33 rows 152 and 75).  Above 1024 units they are not cut: they fill the
+// card, and parts would take gigabytes.
 static TreePlan tree_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
                           int64_t max_len)
 {
@@ -673,7 +676,9 @@ static TreePlan tree_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64
     TreePlan p{};
     const bool wide = cut128 < whole16 && cut128 < cut16;
     p.cols = wide ? 128 : 16;
-    p.groups = wide ? (units(128) <= 1024 ? 512 : 0) : cut16 < whole16 ? 768 : 0;
+    const double u128 = alike(128);
+    const int lone = u128 <= 64 && u128 * mean <= 256 * 28 ? 256 : 512;
+    p.groups = wide ? (units(128) <= 1024 ? lone : 0) : cut16 < whole16 ? 768 : 0;
     // the line of blocks is counted in 32 bits
     if (units(p.cols) * (table_width + kTreeTries) > INT32_MAX) p.groups = 0;
     p.grid = units(p.cols) + p.groups;

@@ -117,7 +117,8 @@ def test_attend_plan(hq, heads, d):
     for rows, nseq, width in itertools.product((1, 7, 64, 500, 5000), (1, 2, 70, 2000), (0, 1, 30, 700, 20000)):
         p = tw.i8_kv_attend_tree_config(rows, hq, heads, d, nseq, width)
         units = (rows * (hq // heads) // p["cols"] + nseq) * heads
-        assert p["cols"] in (16, 128) and p["groups"] in ((0, 768) if p["cols"] == 16 else (0, 512)), (rows, nseq, width, p)
+        assert p["cols"] in (16, 128), (rows, nseq, width, p)
+        assert p["groups"] in ((0, 768) if p["cols"] == 16 else (0, 256, 512)), (rows, nseq, width, p)
         assert p["grid"] == units + p["groups"] and not (p["cols"] == 128 and p["groups"] and units > 1024)
         need = tw.i8_kv_attend_tree_workspace_bytes(rows, hq, heads, d, nseq, max(1, 64 * width))
         used = p["grid"] * p["cols"] * (4 * d + 8) + (nseq + 5) // 4 * 16 if p["groups"] else 0

@@ -461,7 +461,7 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
             return n;
         };
         // chunks as short as the card holds at one time, to within a sixteenth
-        uint32_t most = 0, mine = 0, upto = 0, sum = 0;
+        uint32_t most = 0, mine = 0, base = 0, sum = 0, each = 0;
         if (a.groups > 0) {
             const uint32_t all = __builtin_amdgcn_readlane(scan(lane > lanes ? 0 : work), 63) * c.heads;
             most = (all + a.groups - 1) / a.groups;
@@ -469,13 +469,26 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
         }
         for (int tries = 0;; ++tries) {
             mine = chunks(most);
-            upto = scan(mine);
-            sum = __builtin_amdgcn_readlane(upto, 63);
+            base = scan(mine);
+            sum = __builtin_amdgcn_readlane(base, 63);
+            base -= mine;
             if (most == 0 || sum <= (uint32_t)a.groups || tries == kTreeTries) break;
             most += 1 + most / 16;
         }
+        // The longest chunks first, so that the last to run are short (48 trees of 20 to
+        // 32 rows over 200 to 16000 tokens 309 us in order, 291 so, 32 of 9 to 33 over
+        // 200 to 8000 73.0 and 71.3); of whole units the order costs more than it gives (60 of 4 to
+        // 8 rows over 200 to 2000 38.5 and 42.6).
+        if (a.groups > 0 && run == 1) {
+            tree_chunks<COLS>(r.blocks, most, each);
+            base = 0;
+            for (int k = 0; k < b.nseq; ++k) {
+                const uint32_t other = __builtin_amdgcn_readlane(each, k), count = __builtin_amdgcn_readlane(mine, k);
+                base += other > each || (other == each && k < lane) ? count : 0;
+            }
+        }
         if (a.groups > 0 && blockIdx.x == 0 && threadIdx.x < 64) {   // for the joining kernel
-            uint32_t from = upto - mine, each;
+            uint32_t from = base;
             for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
                 KvSeq s;
                 const TreeShare o = tree_share<COLS>(b, k, a.G, s);
@@ -490,8 +503,8 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
         }
         if (x >= sum) return;
         // the lane whose run holds x, then the sequence inside the run
-        const int owner = __popcll(__ballot(upto <= x));
-        uint32_t at = __builtin_amdgcn_readlane(upto - mine, owner), each = 0;
+        const int owner = __builtin_ctzll(__ballot(x - base < mine));
+        uint32_t at = __builtin_amdgcn_readlane(base, owner);
         int i = owner * run;
         while (true) {
             r = tree_share<COLS>(b, i, a.G, tile.s);

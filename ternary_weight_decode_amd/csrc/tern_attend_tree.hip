@@ -360,10 +360,13 @@ __device__ __forceinline__ void attend_tree_f16(const KvCache& c, const KvBatch&
 
 // ---- work --------------------------------------------------------------------
 
-// A sequence's tiles and the blocks that each of its units has at most; none for a
-// sequence without rows, s.n < 0 where cu descends.
+// A sequence's tiles and what each of its units costs at most, in blocks; none for a
+// sequence without rows, s.n < 0 where cu descends.  On the fp16 path one of the last
+// blocks, those that hold rows of the tree and look at masks, counts as two where
+// they are more than two (500 rows over 4001 tokens, 130 over 900: 69.3 us with all
+// blocks alike, 64.5 so; 32 trees of 9 to 33 rows 70.4 and 73.2).
 struct TreeShare {
-    uint32_t tiles, blocks;
+    uint32_t tiles, cost, plain;             // plain: the blocks in front of the tree's
 };
 
 // of a sequence whose rows are its own and inside the tensors
@@ -371,7 +374,21 @@ template <int COLS>
 __device__ __forceinline__ TreeShare tree_share_of(const KvBatch& b, int G, const KvSeq& s)
 {
     const int last = att_last(s.p0 + s.n - 1, att_limit(b));
-    return {(uint32_t)(((int64_t)s.n * G + COLS - 1) / COLS), last < 0 ? 1u : (uint32_t)last / kKvBlock + 1};
+    const uint32_t blocks = last < 0 ? 1 : (uint32_t)last / kKvBlock + 1;
+    const uint32_t front = s.p0 > 0 ? (uint32_t)s.p0 / kKvBlock : 0;
+    const uint32_t plain = COLS == 16 || front + 2 >= blocks ? blocks : front;
+    return {(uint32_t)(((int64_t)s.n * G + COLS - 1) / COLS), 2 * blocks - plain, plain};
+}
+
+// the block at a place of a unit's cost, and the first place of a block
+__device__ __forceinline__ uint32_t tree_block(const TreeShare& r, uint32_t at)
+{
+    return at <= r.plain ? at : r.plain + (at - r.plain + 1) / 2;
+}
+
+__device__ __forceinline__ uint32_t tree_place(const TreeShare& r, uint32_t block)
+{
+    return block <= r.plain ? block : 2 * block - r.plain - 1;
 }
 
 template <int COLS>
@@ -382,22 +399,22 @@ __device__ __forceinline__ TreeShare tree_share(const KvBatch& b, int i, int G, 
     const int t1 = b.cu[i + 1], len = kv_length(b, i);
     s.n = t1 < s.t0 ? -1 : t1 - s.t0;
     s.p0 = len - s.n;
-    if (s.t0 < 0 || t1 > b.T || s.n <= 0) return {0, 1};
+    if (s.t0 < 0 || t1 > b.T || s.n <= 0) return {0, 1, 1};
     return tree_share_of<COLS>(b, G, s);
 }
 
-// chunks of a unit of `blocks` blocks, `most` of them each at most (0: any), and
-// the blocks of each: the waves of the int8 path take theirs in turn
+// chunks of a unit of this cost, `most` of it each at most (0: any), and the cost of
+// each: the waves of the int8 path take blocks in turn
 template <int COLS>
-__device__ __forceinline__ uint32_t tree_chunks(uint32_t blocks, uint32_t most, uint32_t& each)
+__device__ __forceinline__ uint32_t tree_chunks(uint32_t cost, uint32_t most, uint32_t& each)
 {
     constexpr uint32_t kTurn = COLS < 64 ? att_turn<COLS>() : 1;
-    if (most == 0 || blocks <= most) {
-        each = blocks;
+    if (most == 0 || cost <= most) {
+        each = cost;
         return 1;
     }
-    const uint32_t n = (blocks + most - 1) / most;
-    each = ((blocks + n - 1) / n + kTurn - 1) / kTurn * kTurn;
+    const uint32_t n = (cost + most - 1) / most;
+    each = ((cost + n - 1) / n + kTurn - 1) / kTurn * kTurn;
     return n;
 }
 
@@ -438,13 +455,13 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
         h = x % c.heads;
     } else {
         // every lane has a run of sequences, up to the first descent of cu
-        TreeShare r = {0, 1};
+        TreeShare r = {0, 1, 1};
         uint32_t work = 0;
         bool falls = false;
         for (int k = lane * run; k < lane * run + run && k < b.nseq && !falls; ++k) {
             r = tree_share<COLS>(b, k, a.G, tile.s);
             falls = tile.s.n < 0;
-            work += r.tiles * r.blocks;
+            work += r.tiles * r.cost;
         }
         const uint64_t fell = __ballot(falls);
         const int lanes = fell ? __builtin_ctzll(fell) : 63;      // the last that counts
@@ -452,12 +469,12 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
         const auto chunks = [&](uint32_t most) {
             uint32_t n = 0, each;
             if (lane > lanes) return n;
-            if (run == 1) return r.tiles * c.heads * tree_chunks<COLS>(r.blocks, most, each);
+            if (run == 1) return r.tiles * c.heads * tree_chunks<COLS>(r.cost, most, each);
             KvSeq s;
             for (int k = lane * run; k < lane * run + run && k < b.nseq; ++k) {
                 const TreeShare o = tree_share<COLS>(b, k, a.G, s);
                 if (s.n < 0) break;
-                n += o.tiles * c.heads * tree_chunks<COLS>(o.blocks, most, each);
+                n += o.tiles * c.heads * tree_chunks<COLS>(o.cost, most, each);
             }
             return n;
         };
@@ -481,7 +498,7 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
         // 200 to 8000 73.0 and 71.3); of whole units the order costs more than it gives (60 of 4 to
         // 8 rows over 200 to 2000 38.5 and 42.6).
         if (a.groups > 0 && run == 1) {
-            tree_chunks<COLS>(r.blocks, most, each);
+            tree_chunks<COLS>(r.cost, most, each);
             base = 0;
             for (int k = 0; k < b.nseq; ++k) {
                 const uint32_t other = __builtin_amdgcn_readlane(each, k), count = __builtin_amdgcn_readlane(mine, k);
@@ -494,7 +511,7 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
                 KvSeq s;
                 const TreeShare o = tree_share<COLS>(b, k, a.G, s);
                 a.start[k] = lane <= lanes && s.n >= 0 ? from : sum;
-                from += o.tiles * c.heads * tree_chunks<COLS>(o.blocks, most, each);
+                from += o.tiles * c.heads * tree_chunks<COLS>(o.cost, most, each);
                 if (s.n < 0) from = sum;
             }
             if (lane == 0) {
@@ -509,17 +526,17 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
         int i = owner * run;
         while (true) {
             r = tree_share<COLS>(b, i, a.G, tile.s);
-            parts = tree_chunks<COLS>(r.blocks, most, each);
+            parts = tree_chunks<COLS>(r.cost, most, each);
             const uint32_t here = r.tiles * c.heads * parts;
-            if (x - at < here) break;                             // ends: x is below the run's end
+            if (x - at < here || i + 1 >= b.nseq) break;          // the first: x is below the run's end
             at += here;
             ++i;
         }
         const uint32_t rest = (x - at) / c.heads, chunk = rest / r.tiles;
         h = x - at - rest * c.heads;
         number = rest - chunk * r.tiles;
-        begin = (int)(chunk * each);
-        end = begin + (int)each;
+        begin = (int)tree_block(r, chunk * each);
+        end = (int)tree_block(r, (chunk + 1) * each);
     }
     if (!att_tile<COLS>(b, (int)number, a.G, 0, tile)) return;
     att_uniform(tile);
@@ -554,8 +571,9 @@ __global__ __launch_bounds__(64 * kAttWaves) void kv_attend_tree_join_kernel(KvC
     const uint32_t start = tile.s.i < 64 ? __builtin_amdgcn_readlane(starts, tile.s.i) : a.start[tile.s.i];
     const TreeShare r = tree_share_of<COLS>(b, a.G, tile.s);
     uint32_t each;
-    if (start >= all || tree_chunks<COLS>(r.blocks, most, each) == 1) return;     // written already
-    const int used = tile.nblk > 0 ? (int)((tile.nblk + each - 1) / each) : 1;    // parts that have blocks
+    if (start >= all || tree_chunks<COLS>(r.cost, most, each) == 1) return;     // written already
+    // parts that have blocks
+    const int used = tile.nblk > 0 ? (int)((tree_place(r, tile.nblk) + each - 1) / each) : 1;
     // a wave's jobs are of the same columns (fp16), or of the columns from `first` on
     const int col0 = F16 ? first / (D / 8) * 32 : first;
     if (col0 >= tile.cols) return;
@@ -694,7 +712,7 @@ static TreePlan tree_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64
     const int lone = u128 <= 64 && u128 * mean <= 256 * 28 ? 256 : 512;
     p.groups = wide ? (units(128) <= 1024 ? lone : 0) : cut16 < whole16 ? 768 : 0;
     // the line of blocks is counted in 32 bits
-    if (units(p.cols) * (table_width + kTreeTries) > INT32_MAX) p.groups = 0;
+    if (units(p.cols) * 2 * (table_width + kTreeTries) > INT32_MAX) p.groups = 0;
     p.grid = units(p.cols) + p.groups;
     if (p.groups > 0) {
         p.stats = p.grid * p.cols;

@@ -20,14 +20,15 @@
 // kernel.
 //
 // Measured, us, kernel and join (MI355X, 32:8 heads of 128, caches used in turn):
-//   64 rows over 12338 tokens                  29.8 + 6.6   (26 MB, 16 of parts)
-//   32 trees of 9 to 33 rows over 200 to 8000  66.5 + 9.4   (154 MB, 21 of parts)
-//   500 rows over 4001, 130 over 900           66.6 + 7.7   (37.9e6 matrix-core cycles: 27% of them)
+//   64 rows over 12338 tokens                  30.0 + 6.6   (26 MB, 16 of parts)
+//   32 trees of 9 to 33 rows over 200 to 8000  67.0 + 9.4   (154 MB, 21 of parts)
+//   500 rows over 4001, 130 over 900           62.5 + 7.8   (37.9e6 matrix-core cycles: 29% of them)
 //   8 rows over 512, 16:8 heads                 8.9
-// What bounds the second and third: chunks of unlike length (in the third the last
-// ends at 65 us, the median at 46) and the blocks with masks.  Equal stretches of a
-// line of all units, cut anywhere, were built: 63 and 63 us, but more parts, 12.6 and
-// 9.8 us to join, and the first 32: tiles of a head no longer side by side.  Loads a
+// What bounds the second and third: chunks of unlike length (with all blocks alike
+// and sequences in order the last ended at 65 us, the median at 44 to 46).  Equal
+// stretches of a line of all units, cut anywhere, were built: 63 and 63 us, but more
+// parts, 12.6 and 9.8 us to join, and the first 32: tiles of a head no longer side by
+// side.  Loads a
 // block further ahead (the second raw set in registers) changed nothing.
 #include "tern_attend.h"
 

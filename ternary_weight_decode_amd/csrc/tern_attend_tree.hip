@@ -28,8 +28,7 @@
 // and sequences in order the last ended at 65 us, the median at 44 to 46).  Equal
 // stretches of a line of all units, cut anywhere, were built: 63 and 63 us, but more
 // parts, 12.6 and 9.8 us to join, and the first 32: tiles of a head no longer side by
-// side.  Loads a
-// block further ahead (the second raw set in registers) changed nothing.
+// side.  Loads a block further ahead changed nothing.
 #include "tern_attend.h"
 
 namespace tern {

@@ -163,6 +163,16 @@ def test_lens_out_may_not_be_lens(calls):
     b = batch()
     with pytest.raises(RuntimeError, match="lens_out"):
         CALLS["i8_kv_keep"](None, batch=b, lens_out=b.lens)
+    n = b.nseq
+    lengths = fake(3 * n)
+    b.lens = lengths[n:2 * n]
+    for start in (1, n + 1, 2 * n - 1):          # in part the same memory
+        with pytest.raises(RuntimeError, match="lens_out"):
+            CALLS["i8_kv_keep"](None, batch=b, lens_out=lengths[start:start + n])
+    assert n > 1 and not calls["called"]
+    for start in (0, 2 * n):                     # side by side
+        CALLS["i8_kv_keep"](None, batch=b, lens_out=lengths[start:start + n])
+    assert len(calls["called"]) == 2
 
 
 def test_another_device_is_refused(calls):

@@ -188,7 +188,7 @@ __device__ __forceinline__ void attend_tree_f16(const KvCache& c, const KvBatch&
             if (D == 128 || fills) to[buf * kHalf + 64 * e] = u32x4{x0[0], x0[1], x1[0], x1[1]};
         }
     };
-    float m = -INFINITY, l = 0.0f, top = 0.0f;
+    float m = -INFINITY, l = 0.0f, top = 0.0f;         // top: the lane's largest score of the block that a step weighs
     f32x16 acc[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -316,6 +316,14 @@ __device__ __forceinline__ void attend_tree_f16(const KvCache& c, const KvBatch&
             for (int k = 0; k < kScore; ++k) {
                 x0[k % 2] = mfma_f16(ahead[k % kAhead], q[k / 2], k < 2 ? f32x16{} : x0[k % 2]);
                 if (k + kAhead < kScore) ahead[k % kAhead] = key(0, k + kAhead);
+            }
+            // As a step does for the next block; before the first one m is -inf and top not looked at
+            // (64 rows over 12338 tokens 33.4 us in a graph, 33.7 with it there too).
+            if (seg > begin) {
+                top = x0[0][0];
+#pragma unroll
+                for (int p = 0; p < 16; ++p)
+                    top = fmaxf(fmaxf(top, x0[p >> 3][2 * p & 15]), x0[p >> 3][(2 * p & 15) + 1]);
             }
             for (int i = 0;;) {          // the scores change places: no copies
                 step(i, x0, x1);

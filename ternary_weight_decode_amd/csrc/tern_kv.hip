@@ -504,10 +504,12 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache c, KvBatch b, TO* 
 
 // ---- keep ------------------------------------------------------------------
 // The accepted branch of a tree moves up: slot p0 + k takes the token of slot
-// p0 + path[k].  One workgroup per (sequence, head, side), 64 tokens of the path
-// at a time, which go to two blocks at most.  A path ascends, so they come from
-// these blocks or from others behind, whose bytes are as they were: all tokens
-// are in LDS before anything is written.
+// p0 + path[k].  One workgroup per (sequence, head, side).  The last 64 tokens of
+// the path or fewer go to two blocks at most and are taken at once; while more
+// follow, those of one block are, up to its end, so that every block is scaled
+// once, by all tokens that come into it.  A path ascends, so they come from these
+// blocks or from others behind, whose bytes are as they were: all tokens are in
+// LDS before anything is written.
 // A branch is a few tokens: bound by the launch and the chain from cu over the
 // table to scales and codes.
 template <int D>
@@ -518,7 +520,7 @@ __global__ __launch_bounds__(256) void kv_keep_kernel(KvCache c, KvBatch b, cons
     __shared__ int64_t from[kKvBlock];                 // unit (block and head) of a token's source, -1: none
     __shared__ float its[kKvBlock];                    // the source's scale
     __shared__ int slot[kKvBlock];
-    __shared__ int tokens;
+    __shared__ int tokens, more;
     __shared__ int64_t place[2];                       // the units that tokens go to, -1: none, or nothing moves
     __shared__ uint32_t tops[2][4];
     const int side = blockIdx.x & 1, h = (blockIdx.x >> 1) % c.heads, i = (blockIdx.x >> 1) / c.heads;
@@ -529,15 +531,16 @@ __global__ __launch_bounds__(256) void kv_keep_kernel(KvCache c, KvBatch b, cons
     const bool any = kv_seq(b, i, s);
     const int rows = any ? (s.n < kTreeRows ? s.n : kTreeRows) : 0, most = width < rows ? width : rows;
     int kept = 0;
-    for (int k0 = 0; k0 < most; k0 += kKvBlock) {
-        const int block = (s.p0 + k0) >> 6, base = (s.p0 + k0) & 63;
+    for (int k0 = 0; k0 < most;) {
+        const int base = (s.p0 + k0) & 63;
         if (wave == 0) {
             const int k = k0 + lane;
             if (k0 > 0) r = k < most ? path[k] : -1;
             int before = __shfl(r, lane - 1);
             if (lane == 0) before = k0 > 0 ? path[k0 - 1] : -1;
             const uint64_t end = __ballot(!(k < most && r > before && r >= 0 && r < rows));
-            const int n = end ? __builtin_ctzll(end) : 64;
+            const bool on = end == 0 && k0 + kKvBlock < most;
+            const int n = on ? kKvBlock - base : end ? __builtin_ctzll(end) : kKvBlock;
             const bool mine = lane < n;
             // tokens in front of position 0 are not there (their block is below 0)
             const int p = s.p0 + r, source = mine ? kv_block(b, c, s.i, p >> 6) : -1;
@@ -550,6 +553,7 @@ __global__ __launch_bounds__(256) void kv_keep_kernel(KvCache c, KvBatch b, cons
             const uint64_t m0 = __ballot(moves && !second), m1 = __ballot(moves && second);
             if (lane == 0) {
                 tokens = n;
+                more = on;
                 place[0] = place[1] = -1;
             }
             __builtin_amdgcn_wave_barrier();
@@ -557,7 +561,9 @@ __global__ __launch_bounds__(256) void kv_keep_kernel(KvCache c, KvBatch b, cons
         }
         __syncthreads();
         const int n = tokens;
+        const bool on = more;
         kept += n;
+        k0 += n;
         const int64_t unit[2] = {place[0], place[1]};
         if (unit[0] >= 0 || unit[1] >= 0) {
             const float before[2] = {unit[0] >= 0 ? c.scales[unit[0] * 2 + side] : 0.0f,
@@ -678,7 +684,7 @@ __global__ __launch_bounds__(256) void kv_keep_kernel(KvCache c, KvBatch b, cons
                 }
             }
         }
-        if (n < kKvBlock) break;
+        if (!on) break;
         __syncthreads();                               // LDS is used again
     }
     if (lens_out && side == 0 && h == 0 && threadIdx.x == 0) {

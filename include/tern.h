@@ -628,6 +628,7 @@ int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, 
  *   (a layer) i8_kv_keep: the accepted branch moves up in the cache.
  * `batch` is the one that the rows are appended with: row j of sequence i is
  * row cu[i] + j and stands at slot p0 + j of its cache, p0 = lens[i] - rows.
+ * draft_tree_mask and draft_tree_accept need its cu and lens, and no table.
  *   parent int32 [T]: the row (counted from cu[i]) that a row continues, or -1:
  *   it continues the cached context.  Anything else than an earlier row of the
  *   sequence counts as -1.

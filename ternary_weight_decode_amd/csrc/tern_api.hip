@@ -920,8 +920,8 @@ int draft_tree_accept(const i8_kv_batch* batch, int64_t T, const int32_t* parent
     if (rc) return rc;
     if (width < 1 || width > kTreeMaxWidth) return TERN_E_SHAPE;
     if (batch->nseq == 0) return TERN_OK;
-    if (!batch->cu || !path || (T > 0 && (!parent || !token || !target))) return TERN_E_NULL;
-    if (!aligned4(batch->cu) || !aligned4(parent) || !aligned4(token) || !aligned4(target) || !aligned4(path) ||
+    if (!batch->cu || !batch->lens || !path || (T > 0 && (!parent || !token || !target))) return TERN_E_NULL;
+    if (!aligned4(batch->cu) || !aligned4(batch->lens) || !aligned4(parent) || !aligned4(token) || !aligned4(target) || !aligned4(path) ||
         (count && !aligned4(count)) || (next && !aligned4(next)))
         return TERN_E_ALIGN;
     if ((rc = check_device())) return rc;

@@ -135,3 +135,11 @@ def test_attend_plan(hq, heads, d):
 def test_attend_plan_refuses(bad):
     with pytest.raises(RuntimeError):
         tw.i8_kv_attend_tree_config(**{**dict(tokens=8, hq=4, heads=2, d=64, nseq=2, width=9), **bad})
+
+
+@pytest.mark.parametrize("call", [mask, accept])
+def test_a_batch_without_lengths_is_refused(call):
+    """The batch's three arrays, whichever of them a call reads."""
+    assert call(b=batch(lens=None)) == E_NULL
+    assert call(b=batch(lens=P + 2)) == E_ALIGN
+    assert call(b=batch(cu=P + 2)) == E_ALIGN

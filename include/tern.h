@@ -597,8 +597,9 @@ int i8_kv_read(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, vo
  *   rows that a sequence will have, 0 when not known.  Both are hints for the
  *   choice of kernels and the split of long sequences: a batch that goes past
  *   them is slower, and as right.
- *   workspace: i8_kv_attend_workspace_bytes() bytes, 16-byte aligned, NULL when
- *   that is 0; overwritten, so calls that share it must not overlap in time.
+ *   workspace: i8_kv_attend_workspace_bytes() bytes for exactly these sizes and
+ *   hints (smaller ones may need more), 16-byte aligned, NULL when that is 0;
+ *   overwritten, so calls that share it must not overlap in time.
  * The sums do not depend on timing: equal calls give equal bytes.
  * Accuracy, against exact arithmetic over the cached values: the output's
  * rounding to bf16, and below it what the operands of the matrix cores leave
@@ -654,11 +655,16 @@ int draft_tree_mask(const i8_kv_batch* batch, int64_t T, const int32_t* parent, 
  * nothing gives zeros.
  *   mask uint64 [T][words], 1 <= words <= TERN_TREE_WORDS
  *   max_len: the longest length that lens will hold, a hint as there
- *   workspace: i8_kv_attend_tree_workspace_bytes() bytes, 16-byte aligned, NULL
- *   when that is 0; overwritten, so calls that share it must not overlap in time.
+ *   workspace: i8_kv_attend_tree_workspace_bytes() bytes for exactly these sizes
+ *   and this max_len, 16-byte aligned, NULL when that is 0; overwritten, so calls
+ *   that share it must not overlap in time.  A smaller batch, or another max_len,
+ *   may need more: large batches are not cut and need none.
+ *   i8_kv_attend_tree_workspace_limit() bytes serve every call of up to T rows
+ *   and nseq sequences with these heads, whatever its max_len.
  * The other arguments, and the accuracy, are those of i8_kv_attend. */
 int64_t i8_kv_attend_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq,
                                           int64_t max_len);
+int64_t i8_kv_attend_tree_workspace_limit(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq);
 int i8_kv_attend_tree(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const uint16_t* q, int64_t Hq,
                       int64_t q_stride, float scale, const uint64_t* mask, int64_t words, int64_t max_len,
                       uint16_t* out, void* workspace, void* stream);

@@ -26,7 +26,7 @@ side of a step ``qk_norm_rope``, ``i8_kv_append``, ``i8_kv_read`` and
 ``tern_gemv_config``, ``tern_prefill_config`` and ``i8_kv_attend_config``.
 The submodules ``q4`` (4-bit weights: ``q4_packed_bytes``, ``q4_pack``,
 ``q4_gemv[_i8]``) and ``draft_tree`` (``draft_tree_mask``,
-``i8_kv_attend_tree``, ``i8_kv_attend_tree_workspace[_bytes]``,
+``i8_kv_attend_tree``, ``i8_kv_attend_tree_workspace[_bytes,_limit]``,
 ``i8_kv_attend_tree_config``, ``draft_tree_accept``, ``i8_kv_keep``) hold
 further calls of the ABI, which are found here under the same names.
 """
@@ -49,7 +49,8 @@ SYMBOLS = ("tern_strerror", "tern_last_error", "tern_abi_version", "tern_packed_
            "fv5b_head_argmax_packed_i8", "qk_norm_rope", "i8_kv_append", "i8_kv_read",
            "i8_kv_attend_workspace_bytes", "i8_kv_attend", "i8_kv_attend_config",
            "q4_packed_bytes", "q4_pack", "q4_gemv", "q4_gemv_i8",
-           "draft_tree_mask", "i8_kv_attend_tree_workspace_bytes", "i8_kv_attend_tree", "i8_kv_attend_tree_config",
+           "draft_tree_mask", "i8_kv_attend_tree_workspace_bytes", "i8_kv_attend_tree_workspace_limit",
+           "i8_kv_attend_tree", "i8_kv_attend_tree_config",
            "draft_tree_accept", "i8_kv_keep")
 _INT_STATUS = ("tern_pack", "tern_stats", "tern_quantize_i8", "tern_gemv", "tern_gemv_i8", "i8_head_gemv",
                "i8_head_gemv_i8", "tern_gemm_prefill", "tern_chain_plan", "tern_gemv_chain", "i8_head_argmax",
@@ -172,6 +173,8 @@ def lib():
         L.draft_tree_mask.argtypes = [batch, _i64, _p, _i64, _p, _p, _p]
         L.i8_kv_attend_tree_workspace_bytes.restype = _i64
         L.i8_kv_attend_tree_workspace_bytes.argtypes = [_i64] * 6
+        L.i8_kv_attend_tree_workspace_limit.restype = _i64
+        L.i8_kv_attend_tree_workspace_limit.argtypes = [_i64] * 5
         L.i8_kv_attend_tree_config.restype = ctypes.c_int
         L.i8_kv_attend_tree_config.argtypes = [_i64] * 7 + [ctypes.POINTER(_i64)]
         L.i8_kv_attend_tree.argtypes = [cache, batch, _i64, _p, _i64, _i64, ctypes.c_float, _p, _i64, _i64, _p, _p, _p]
@@ -1099,6 +1102,7 @@ def i8_kv_attend(cache, batch, q, scale=None, window: int = 0, max_len=None, max
 _HELD = {"q4_packed_bytes": "q4", "q4_pack": "q4", "q4_gemv": "q4", "q4_gemv_i8": "q4",
          "TREE_ROWS": "draft_tree", "draft_tree_mask": "draft_tree", "i8_kv_attend_tree": "draft_tree",
          "i8_kv_attend_tree_workspace_bytes": "draft_tree", "i8_kv_attend_tree_workspace": "draft_tree",
+         "i8_kv_attend_tree_workspace_limit": "draft_tree",
          "i8_kv_attend_tree_config": "draft_tree", "draft_tree_accept": "draft_tree", "i8_kv_keep": "draft_tree"}
 
 

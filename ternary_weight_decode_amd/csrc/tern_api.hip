@@ -851,6 +851,13 @@ int64_t i8_kv_attend_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, 
     return tern::kv_attend_tree_workspace_bytes(T, Hq, heads, D, nseq, max_len);
 }
 
+int64_t i8_kv_attend_tree_workspace_limit(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq)
+{
+    const int64_t one = i8_kv_attend_tree_workspace_bytes(T, Hq, heads, D, nseq, 1);
+    if (one < 0 || T == 0 || nseq == 0) return one;
+    return tern::kv_attend_tree_workspace_limit(T, Hq, heads, D, nseq);
+}
+
 int i8_kv_attend_tree_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
                              int64_t max_len, int64_t* out)
 {

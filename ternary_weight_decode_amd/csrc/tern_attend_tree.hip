@@ -683,6 +683,16 @@ struct TreePlan {
     int64_t bytes() const { return part_floats * 4 + stats * 8 + (starts + 3) / 4 * 16; }
 };
 
+// what the parts of a cut call take
+static void tree_space(TreePlan& p, int64_t D, int64_t nseq)
+{
+    p.stats = p.grid * p.cols;
+    p.part_floats = p.stats * D;
+    p.starts = nseq + 2;
+}
+
+constexpr int64_t kTreeUnits = 1024;             // of 128 columns that are cut, at most
+
 // Estimates in us, fitted to 14 shapes of D 128 (1 to 64 trees of 8 to 500 rows
 // over 500 to 40000 tokens, G 2 and 4, graphs of calls over caches used in turn).
 // 16 columns whole: 0.27 us a block of the longest unit (four waves take blocks in
@@ -718,21 +728,35 @@ static TreePlan tree_plan(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64
     p.cols = wide ? 128 : 16;
     const double u128 = alike(128);
     const int lone = u128 <= 64 && u128 * mean <= 256 * 28 ? 256 : 512;
-    p.groups = wide ? (units(128) <= 1024 ? lone : 0) : cut16 < whole16 ? 768 : 0;
+    p.groups = wide ? (units(128) <= kTreeUnits ? lone : 0) : cut16 < whole16 ? 768 : 0;
     // the line of blocks is counted in 32 bits
     if (units(p.cols) * 2 * (table_width + kTreeTries) > INT32_MAX) p.groups = 0;
     p.grid = units(p.cols) + p.groups;
-    if (p.groups > 0) {
-        p.stats = p.grid * p.cols;
-        p.part_floats = p.stats * D;
-        p.starts = nseq + 2;
-    }
+    if (p.groups > 0) tree_space(p, D, nseq);
     return p;
 }
 
 int64_t kv_attend_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len)
 {
     return tree_plan(T, Hq, heads, D, nseq, 0, max_len).bytes();
+}
+
+// The most that a call of up to these rows and sequences takes.  16 columns are cut
+// where 0.27 us a block come to more than 11 us and 1050 blocks of all units a us,
+// three quarters of the longest on average: below 0.27 * 1050 / 0.75 = 378 units of
+// sequences alike, or 756 as they are counted for the workspace.
+int64_t kv_attend_tree_workspace_limit(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq)
+{
+    int64_t most = 0;
+    for (int cols : {16, 128}) {
+        const int64_t units = (T * (Hq / heads) / cols + nseq) * heads, cut = cols == 16 ? 756 : kTreeUnits;
+        TreePlan p{};
+        p.cols = cols;
+        p.grid = (units < cut ? units : cut) + (cols == 16 ? 768 : 512);
+        tree_space(p, D, nseq < cut ? nseq : cut);       // a unit for each sequence at least
+        most = p.bytes() > most ? p.bytes() : most;
+    }
+    return most;
 }
 
 void kv_attend_tree_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,

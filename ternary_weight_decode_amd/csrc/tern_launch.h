@@ -165,6 +165,7 @@ hipError_t launch_tree_mask(const KvBatch& b, const int32_t* parent, int words, 
 hipError_t launch_tree_accept(const KvBatch& b, const int32_t* parent, const int32_t* token, const int32_t* target,
                               int width, int32_t* path, int32_t* count, int32_t* next, hipStream_t stream);
 int64_t kv_attend_tree_workspace_bytes(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t max_len);
+int64_t kv_attend_tree_workspace_limit(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq);
 void kv_attend_tree_config(int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t nseq, int64_t table_width,
                            int64_t max_len, int64_t* out);
 hipError_t launch_kv_attend_tree(const KvCache& c, const KvBatch& b, int64_t D, const uint16_t* q, int64_t Hq,

@@ -55,15 +55,21 @@ def draft_tree_mask(batch, parent, words: int = 1, mask=None, pos=None, stream=N
 
 
 def i8_kv_attend_tree_workspace_bytes(tokens: int, hq: int, heads: int, d: int, nseq: int, max_len: int) -> int:
+    """Bytes that i8_kv_attend_tree needs for exactly these sizes and this max_len; smaller ones may need more."""
     return int(_lib.i8_kv_attend_tree_workspace_bytes(tokens, hq, heads, d, nseq, max_len))
 
 
+def i8_kv_attend_tree_workspace_limit(tokens: int, hq: int, heads: int, d: int, nseq: int) -> int:
+    """Bytes that serve every call of up to `tokens` rows and nseq sequences, whatever its max_len."""
+    return int(_lib.i8_kv_attend_tree_workspace_limit(tokens, hq, heads, d, nseq))
+
+
 def i8_kv_attend_tree_workspace(cache, batch, tokens: int, hq: int, max_len=None):
-    """A workspace for i8_kv_attend_tree of `tokens` rows of hq heads (None where none is needed)."""
-    nbytes = i8_kv_attend_tree_workspace_bytes(tokens, hq, cache.heads, cache.d, batch.nseq,
-                                               max(1, batch.width * _tw.KV_BLOCK) if max_len is None else max_len)
-    if nbytes < 0:
-        _tw._check("i8_kv_attend_tree_workspace_bytes", 2)
+    """A workspace for i8_kv_attend_tree of up to `tokens` rows of hq heads and the batch's number of sequences: as
+    large as any of these calls needs, whatever its max_len (None where there is nothing to do)."""
+    nbytes = i8_kv_attend_tree_workspace_limit(tokens, hq, cache.heads, cache.d, batch.nseq)
+    if nbytes < 0 or (max_len is not None and not 0 < max_len < 2 ** 31):
+        _tw._check("i8_kv_attend_tree_workspace", 2)
     return _torch.empty(nbytes, dtype=_torch.uint8, device=cache.device) if nbytes else None
 
 

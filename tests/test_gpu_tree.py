@@ -526,3 +526,19 @@ def test_two_streams_at_once():
         got = [tw.i8_kv_attend_tree(*p, stream=st) for p, st in zip(parts, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_a_workspace_sized_for_the_largest_batch():
+    """It serves smaller ones, which need one where the largest does not."""
+    import torch
+    s = Case(tw, 101, 64, 8, [24, 9, 24], [2000, 30, 700])
+    c, b = s.device()
+    lens = torch.zeros(140, dtype=torch.int32, device="cuda")
+    many = tw.I8KvBatch(torch.zeros(141, dtype=torch.int32, device="cuda"), lens, b.table[:1].expand(140, -1).contiguous())
+    assert tw.i8_kv_attend_tree_workspace_bytes(140 * 24, 32, 8, 64, 140, 16000) == 0
+    ws = tw.i8_kv_attend_tree_workspace(c, many, 140 * 24, 32, 16000)
+    m, _ = tw.draft_tree_mask(b, dev(forest(s.rng, [24, 9, 24])))
+    q = dev(queries(s, 32), torch.bfloat16)
+    for max_len in (None, 500, 16000, LONG):
+        assert torch.equal(tw.i8_kv_attend_tree(c, b, q, m, max_len=max_len, workspace=ws),
+                           tw.i8_kv_attend_tree(c, b, q, m, max_len=max_len))

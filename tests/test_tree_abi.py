@@ -143,3 +143,31 @@ def test_a_batch_without_lengths_is_refused(call):
     assert call(b=batch(lens=None)) == E_NULL
     assert call(b=batch(lens=P + 2)) == E_ALIGN
     assert call(b=batch(cu=P + 2)) == E_ALIGN
+
+
+@pytest.mark.parametrize("hq, heads, d", [(32, 8, 128), (16, 8, 64), (1, 1, 64), (20, 1, 128), (800, 800, 64), (64, 2, 64)])
+def test_one_workspace_serves_smaller_calls(hq, heads, d):
+    """Sizes of a call and of those below it, in which chunks come and go: the limit holds all of them, and grows
+    with the sizes."""
+    need, limit = tw.i8_kv_attend_tree_workspace_bytes, tw.i8_kv_attend_tree_workspace_limit
+    lengths = (1, 64, 500, 2000, 8000, 16000, 60000, 10 ** 6, 2 ** 31 - 1)
+    sizes = sorted({int(1.3 ** i) for i in range(45)} | {24 * i for i in range(0, 200, 7)} | {0, 2000, 5000})
+    most = {}                                   # of any call of these rows, by sequences
+    for rows in sizes:
+        if rows * hq > 2 ** 25:
+            break
+        for nseq in (0, 1, 2, 3, 5, 8, 17, 32, 47, 64, 90, 100, 128, 140, 378, 756, 1024, 3000):
+            largest = max(need(rows, hq, heads, d, nseq, n) for n in lengths)
+            for other, seen in most.items():
+                if other <= nseq:
+                    largest = max(largest, seen)
+            most[nseq] = max(most.get(nseq, 0), largest)
+            assert limit(rows, hq, heads, d, nseq) >= most[nseq], (rows, nseq)
+            if rows and nseq:
+                assert limit(rows, hq, heads, d, nseq) >= limit(max(1, rows - 1), hq, heads, d, max(1, nseq - 1))
+    assert limit(0, hq, heads, d, 5) == 0 == limit(5, hq, heads, d, 0)
+
+
+def test_the_limit_refuses():
+    for kw in (dict(tokens=-1), dict(hq=3), dict(heads=0), dict(d=96), dict(nseq=-1), dict(tokens=2 ** 24)):
+        assert tw.i8_kv_attend_tree_workspace_limit(**{**dict(tokens=8, hq=4, heads=2, d=64, nseq=2), **kw}) == -1

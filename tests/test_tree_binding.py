@@ -180,3 +180,19 @@ def test_another_device_is_refused(calls):
     b.device = 1
     with pytest.raises(RuntimeError, match="device"):
         CALLS["i8_kv_keep"](None, batch=b)
+
+
+def test_a_workspace_for_every_smaller_batch(monkeypatch):
+    """What a server sizes once for its largest batch, which needs none itself."""
+    monkeypatch.setattr(draft_tree._torch, "empty", lambda n, dtype, device: torch.zeros(n, dtype=dtype))
+    c = types.SimpleNamespace(heads=8, d=128, device=0)
+    large = types.SimpleNamespace(nseq=100, width=250)
+    assert tw.i8_kv_attend_tree_workspace_bytes(2400, 32, 8, 128, 100, 16000) == 0
+    for max_len in (None, 16000):
+        ws = tw.i8_kv_attend_tree_workspace(c, large, 2400, 32, max_len)
+        assert ws.nbytes >= max(tw.i8_kv_attend_tree_workspace_bytes(24 * n, 32, 8, 128, n, m)
+                                for n in range(1, 101) for m in (500, 4000, 16000, 10 ** 6))
+    assert tw.i8_kv_attend_tree_workspace(c, large, 0, 32) is None
+    for kw in (dict(tokens=-1), dict(hq=3), dict(max_len=0), dict(max_len=2 ** 31)):
+        with pytest.raises(RuntimeError):
+            tw.i8_kv_attend_tree_workspace(c, large, **{**dict(tokens=8, hq=32), **kw})

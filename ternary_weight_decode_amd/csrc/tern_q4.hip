@@ -385,7 +385,7 @@ __global__ __launch_bounds__(1024) void q4_gemv_kernel(const uint8_t* __restrict
         if (m >= M || n >= N) continue;
         float sum = 0;
         for (int v = 0; v < nw; ++v) sum += red[(i * nw + v) * (NI * kLanes) + e * kLanes + l];
-        y[m * N + n] = I8 ? s_x[m] * 0.0625f * sum : sum;
+        y[m * N + n] = I8 ? s_x[m] * (0.0625f * sum) : sum;      // s_x may be fp32's smallest number
     }
 }
 

@@ -157,3 +157,19 @@ def test_captured_and_on_another_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want[i][0]) and torch.equal(yi, want[i][1])
+
+
+@pytest.mark.parametrize("m", [1, 5, 16])
+def test_row_scales_of_every_size(m):
+    """Scales of activations down to fp32's smallest number and up to where results leave it."""
+    rng = np.random.default_rng(m)
+    n, k, group = 50, 1152, 32
+    t, s = weights(rng, n, k, group)
+    packed = tw.q4_pack(dev(t), dev(s))
+    q = rng.integers(-127, 128, (m, k)).astype(np.int8)
+    for size in (2.0 ** -149, 13 * 2.0 ** -149, 2.0 ** -130 * 1.37, 2.0 ** -126, 1e-30, 1.0, 2.0 ** 100):
+        sx = np.full(m, size, np.float32)
+        got = host(tw.q4_gemv_i8(packed, n, k, group, dev(q), dev(sx)))
+        want, bound = q4.gemv_i8(t, s, q, sx)
+        # a result below fp32's normal numbers has a step of 2^-149
+        assert np.all(np.abs(got - want) <= bound + 2.0 ** -149), size

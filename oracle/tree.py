@@ -117,9 +117,9 @@ def _keep(cache, mine, dst, h, side, f):
             elif not np.isfinite(old) or strange:
                 scale, zero = (old if not np.isfinite(old) else top), True
             else:
-                while top > f(127) * old * f(2.0 ** g):
+                while float(top) > np.ldexp(float(f(127) * old), g):     # 2^g alone may pass fp32
                     g += 1
-                scale = old * f(2.0 ** g)
+                scale = f(np.ldexp(float(old), g))
         if zero:
             new[:] = 0
         elif g:

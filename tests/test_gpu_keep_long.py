@@ -53,3 +53,11 @@ def test_a_branch_that_begins_in_front_of_the_cache():
         table = s.table.copy()
         table[0, gone] = -1
         kept_cache(s, path, table)
+
+
+def test_scales_from_the_smallest_numbers():
+    """Blocks whose scale has to grow from below fp32's normal numbers to ordinary sizes."""
+    for seed in range(4):
+        s = Case(tw, [91, seed], 64, 2, [200], [50])
+        s.scales[s.rng.random(s.scales.shape) < 0.4] = (2.0 ** -149, 1e-42, 2.0 ** -126, 1e-30)[seed]
+        kept_cache(s, some(s.rng, 200, 90, 90)[None])

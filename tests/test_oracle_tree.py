@@ -59,3 +59,16 @@ def test_tokens_move_within_and_across_blocks():
     v = c.tokens(0, 0, 1)
     assert c.scales[0, 0, 1] == 0.25 and np.array_equal(v[62], before[1][1][1]) and np.array_equal(v[0], before[0][1][0])
     assert np.array_equal(c.tokens(1, 0, 0), before[1][0])
+
+
+def test_a_scale_grows_by_any_power_of_two():
+    """From fp32's smallest numbers to ordinary ones: 2^g itself passes fp32."""
+    codes = np.full((2, 1, 2, 64 * 64), 100, np.int8)
+    for small in (2.0 ** -149, 1e-42, 1e-30):
+        scales = np.array([[[small, 0.5]], [[2.0, 2.0]]], np.float32)
+        c = kv.Cache(codes.copy(), scales)
+        tree.keep(c, [0, 10], [70], np.array([[0, 1]]), 10, [[0, 9]])     # slot 61 takes slot 69
+        g = np.log2(c.scales[0, 0] / scales[0, 0].astype(np.float64))
+        assert np.array_equal(g, np.rint(g)) and np.all(127 * c.scales[0, 0].astype(np.float64) >= 200)
+        assert np.all(127 * c.scales[0, 0] / 2 < 200)
+        assert np.all(c.tokens(0, 0, 0)[61] == np.rint(200 / np.float32(c.scales[0, 0, 0])))

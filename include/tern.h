@@ -648,8 +648,9 @@ int i8_kv_attend(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, 
 int draft_tree_mask(const i8_kv_batch* batch, int64_t T, const int32_t* parent, int64_t words, uint64_t* mask,
                     int32_t* pos, void* stream);
 
-/* Attention for the rows of trees, as i8_kv_attend without a window, but row j of
- * a sequence sees the cached tokens in front of the tree (positions below p0)
+/* Attention for the rows of trees, as i8_kv_attend without a window (which would go
+ * by the rows' positions, where the cache knows their slots), but row j of a
+ * sequence sees the cached tokens in front of the tree (positions below p0)
  * and, of the tree, the rows a <= j whose bit its mask has (its own among them as
  * any other).  mask as draft_tree_mask writes it, or any other; a row that sees
  * nothing gives zeros.
@@ -699,8 +700,9 @@ int draft_tree_accept(const i8_kv_batch* batch, int64_t T, const int32_t* parent
  *   where old is 0: scale = a / 127, the other codes 0.
  * A block that takes a token whose scale is not finite gets that scale, and one
  * that takes a value past fp32 an infinity; it then reads as NaN, as one whose
- * own scale is not finite does.  Slots behind the kept tokens stand for nothing.  Tokens whose block is not in the table are not moved, and nothing
- * is moved to where there is no block.
+ * own scale is not finite does.  Slots behind the kept tokens stand for nothing.
+ * Tokens whose block is not in the table are not moved, and nothing is moved to
+ * where there is no block.
  * The blocks from p0 on must be the sequence's own (as for the append). */
 int i8_kv_keep(const i8_kv_cache* cache, const i8_kv_batch* batch, int64_t T, const int32_t* path, int64_t width,
                int32_t* lens_out, void* stream);

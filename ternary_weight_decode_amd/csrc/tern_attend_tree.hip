@@ -19,11 +19,12 @@
 // XCD, and share its reads in L2.  The parts of a cut unit are joined by a second
 // kernel.
 //
-// Measured, us, kernel and join (MI355X, 32:8 heads of 128, caches used in turn):
-//   64 rows over 12338 tokens                  30.0 + 6.6   (26 MB, 16 of parts)
-//   32 trees of 9 to 33 rows over 200 to 8000  67.0 + 9.4   (154 MB, 21 of parts)
-//   500 rows over 4001, 130 over 900           62.5 + 7.8   (37.9e6 matrix-core cycles: 29% of them)
-//   8 rows over 512, 16:8 heads                 8.9
+// Measured, us, medians of the kernel and the join in a trace (MI355X, 32:8 heads of
+// 128, caches of 600 MB used in turn; 10% between cards):
+//   64 rows over 12338 tokens                  30.6 + 6.6    (26 MB, 16 of parts)
+//   32 trees of 9 to 33 rows over 200 to 8000  74.3 + 10.5   (154 MB, 21 of parts; at best 65.6 + 9.2)
+//   500 rows over 4001, 130 over 900           63.9 + 8.0    (37.9e6 matrix-core cycles: 28% of them)
+//   8 rows over 512, 16:8 heads                 8.8
 // What bounds the second and third: chunks of unlike length (with all blocks alike
 // and sequences in order the last ended at 65 us, the median at 44 to 46).  Equal
 // stretches of a line of all units, cut anywhere, were built: 63 and 63 us, but more
@@ -502,9 +503,10 @@ __global__ __launch_bounds__(64 * kAttWaves, COLS == 16 ? 3 : 2) void kv_attend_
             most += 1 + most / 16;
         }
         // The longest chunks first, so that the last to run are short (48 trees of 20 to
-        // 32 rows over 200 to 16000 tokens 309 us in order, 291 so, 32 of 9 to 33 over
-        // 200 to 8000 73.0 and 71.3); of whole units the order costs more than it gives (60 of 4 to
-        // 8 rows over 200 to 2000 38.5 and 42.6).
+        // 32 rows over 200 to 16000 tokens, at random, 309 us in order, 291 so, 32 of 9 to
+        // 33 over 200 to 8000 73.0 and 71.3; for up to 64 sequences, one a lane); of whole
+        // units the order costs more than it gives (60 of 4 to 8 rows over 200 to 2000 38.5
+        // and 42.6).
         if (a.groups > 0 && run == 1) {
             tree_chunks<COLS>(r.cost, most, each);
             base = 0;

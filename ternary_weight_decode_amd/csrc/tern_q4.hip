@@ -22,7 +22,9 @@ __device__ __forceinline__ f32x4 q4_mfma(u32x4 a, u32x4 b, f32x4 c)
 }
 
 // Eight weights of a word to fp16, exact: the low byte of 1024 + v is v, and
-// t + 8 = (t & 15) ^ 8; the nibbles at bit 4 stand for 16 (t + 8) there.
+// t + 8 = (t & 15) ^ 8; the nibbles at bit 4 stand for 16 (t + 8) there.  (Whole
+// numbers put into the mantissa of a constant, the known way from packed bits to
+// fp16: Kim, Henry, Fahim, Awadalla, "Who Says Elephants Can't Run", 2022.)
 __device__ __forceinline__ u32x4 q4_decode(uint32_t w)
 {
     const q4_f16x2 off = {(_Float16)1032.0f, (_Float16)1032.0f};
@@ -87,11 +89,12 @@ __global__ void q4_pack_kernel(const int8_t* __restrict__ t, const uint16_t* __r
 // become operands in nine instructions there; exact bf16 ones would take 14.
 // int8 weights are the nibbles where they stand, times 16: three instructions.
 //
-// What bounds it: the weights' bytes and a launch (24576 x 4096, groups of 128,
-// 52 MB out of memory: one row in int8 10.3 us, 5.0 TB/s with the 1.9 us of an
-// empty launch in it, in bf16 11.4; 16 rows 12.0 and 13.4).  A long K with many
-// rows: x, which every workgroup reads (4096 x 12288, groups of 64, 27 MB, int8:
-// one row 6.4 us, 7 rows 7.7, 16 rows 10.2, bf16 8.3, 12.2 and 17).
+// What bounds it: the weights' bytes and a launch (in a graph of calls over weights
+// out of memory; 24576 x 4096, groups of 128, 52 MB: one row in int8 10.2 us, 5.1
+// TB/s with the 1.9 us of an empty launch in it, in bf16 11.1; 16 rows 12.0 and
+// 13.6).  A long K with many rows: x, which every workgroup reads (4096 x 12288,
+// groups of 64, 27 MB, int8: one row 6.3 us, 7 rows 7.7, 16 rows 10.2, bf16 7.6,
+// 11.8 and 16.5).
 
 // operand of one step of 32 k: 8 activations
 template <bool I8>
@@ -407,9 +410,9 @@ struct Q4Config {
 };
 
 // One block a unit while that fills 16 waves or fewer, so that small matrices
-// wait for the shortest chain (4096 x 1024, one row in bf16: 2.9 us; two blocks
-// 3.0, four rows 3.1 and 3.7; 40000 x 2048 in 16 waves of one block 11.4, in 8 of
-// two 10.4).
+// wait for the shortest chain (in a graph, weights in the last-level cache, 4096 x
+// 1024, one row in bf16: 3.0 us, with two blocks 0.1 more; four rows 3.3 and 0.6 more;
+// 40000 x 2048 in 16 waves of one block 11.4, in 8 of two 10.4).
 // Row tiles: a workgroup with R of them pays for its x and its meeting once, and
 // 16 waves a CU run at once; the fewest (rounds) x (R + 1) is taken.  24576 x
 // 4096, one and sixteen rows in bf16: R = 6, one round, 11.4 and 13.4 us; 3, two

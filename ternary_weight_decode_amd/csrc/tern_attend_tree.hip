@@ -708,6 +708,9 @@ constexpr int64_t kTreeUnits = 1024;             // of 128 columns that are cut,
 //   64 rows over  12338 tokens     56     40     35.7
 //   16 x 64 rows over 3000        103    106     80
 //   32 trees of 9 to 33 rows over 200 to 8000     85     92     76
+// Held against all three at 65 further shapes (D 64 and 128, G 1, 4 and 8, 1 to 64
+// trees of 8 to 500 rows over 200 to 40000): within 6% of the best at 61, at most
+// 19% off (64 rows over 12338 tokens, D 64, G 8: 44 us, 16 cut 37).
 // 128 columns, one workgroup a CU or two: two leave parts twice as many, and pay off
 // where chunks are long or units many (us, 256 and 512 workgroups: 64 rows over 6000
 // tokens 29.4 and 31.3, over 12338 33.7 and 35.9, over 30000 54.3 and 53.2; 32 trees
